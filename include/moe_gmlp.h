@@ -65,6 +65,9 @@ typedef enum moe_status {
                                          running past the next group's start
                                          or past M_cap (its rows there are
                                          not computed)                       */
+#define MOE_DEVERR_NONFINITE 0x10     /* moe_grad_clip: the norm is infinite
+                                         or NaN; the gradients were copied
+                                         unscaled                            */
 
 /* Group-start alignment of the padded row layout (rows).  Every group of
  * the permuted layout starts at a multiple of it, so MXFP8 blocks of 32
@@ -710,6 +713,269 @@ typedef struct moe_router_route_args {
 
 size_t moe_router_route_workspace_size(int T, int E_total, int E);
 moe_status moe_router_route(const moe_router_route_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Block-scaled FP8: E4M3 codes with one fp32 scale for each block of
+ * MOE_FP8_BLOCK values, the form of 8-bit expert weights and activations
+ * whose scales are ordinary numbers (MXFP8 above: a power of two per 32).
+ *
+ * A row copy of an [R][K] operand, blocked along its contraction axis K:
+ *   codes   u8 [R][K], E4M3 (bias 7, largest finite 448, NaN 0x7f / 0xff)
+ *   scales  fp32 [ceil(K / 128)][R]: the scale of row r, block b (columns
+ *           [128 b, min(K, 128 b + 128))) is element b * R + r, so the rows
+ *           of a tile have their scales side by side at every K step.
+ * A tile copy of an [R][K] operand (weights), one scale per 128 x 128 tile:
+ *   codes   u8 [R][K]
+ *   scales  fp32 [ceil(R / 128)][ceil(K / 128)].
+ * A code stands for E4M3(code) * scale.  The last block or tile of an axis
+ * that is no multiple of 128 holds what is left.
+ *
+ * Encoding of a block v[i] (bf16), m = max(max|v[i]|, 2^-100), all in fp32
+ * with each operation rounded to nearest even:
+ *   scale = m / 448,  code_i = E4M3(v_i * (448 / m))         (pow2 == 0)
+ *   scale = 2^c, code_i = E4M3(v_i / 2^c), 2^c the smallest power of two
+ *           not below m / 448 (exact, and the same number in an E8M0 code)
+ *                                                            (pow2 != 0)
+ * E4M3() rounds to nearest even; no value exceeds 448 after the scaling.
+ * The sign is kept (-0 gives 0x80).  A NaN gives a NaN code and does not
+ * count for the maximum; a block with an infinity has an infinite scale, so
+ * all of it decodes to NaN.
+ * ---------------------------------------------------------------------- */
+#define MOE_FP8_BLOCK 128
+
+typedef enum moe_type { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type;
+
+/* moe_quantize_fp8 -- bf16 to block-scaled FP8.
+ *   x bf16 [batch][rows][cols], x_stride elements between batch entries
+ *   (0: rows * cols; a multiple of 8), rows contiguous; x, q, qT 16-byte
+ *   aligned.
+ *   MOE_QUANT_ROW:  the row copy: q [batch][rows][cols], s
+ *     [batch][ceil(cols/128)][rows].
+ *   MOE_QUANT_COL:  the row copy of the transposed matrix (blocks along
+ *     rows; the weight-gradient operand): q [batch][cols][rows], s
+ *     [batch][ceil(rows/128)][cols].
+ *   MOE_QUANT_BOTH: ROW into q / s and COL into qT / sT, reading x once.
+ *   MOE_QUANT_TILE: the tile copy: q [batch][rows][cols], s
+ *     [batch][ceil(rows/128)][ceil(cols/128)]; with qT and sT (both or
+ *     neither) also that of the transposed matrix, which has the same
+ *     values: qT [batch][cols][rows], sT
+ *     [batch][ceil(cols/128)][ceil(rows/128)] (the input-gradient operand).
+ *   Needs cols % 16 == 0 and, but for ROW, rows % 16 == 0; rows or batch 0
+ *   is a call with nothing to do.  live (optional, [batch], say the split
+ *   sizes): entries with live[b] == 0 are skipped, as in
+ *   moe_quantize_mxfp8.  row_end (optional, device int32, say
+ *   padded_offsets + E): rows at or past *row_end are not read and not
+ *   written in the copies that have rows as rows; a block of 128 rows that
+ *   starts there is not written in the others, and one that contains
+ *   *row_end has zeros for the rows past it. */
+#define MOE_QUANT_TILE 3
+
+typedef struct moe_quant_fp8_args {
+  int32_t mode;
+  int32_t batch, rows, cols;
+  int64_t x_stride;
+  const void* x;               /* bf16 device */
+  uint8_t* q;
+  float* s;
+  uint8_t* qT;                 /* BOTH, optional in TILE */
+  float* sT;
+  int32_t pow2;                /* scales are powers of two */
+  const int32_t* live;         /* optional device int32 [batch] */
+  const int32_t* row_end;      /* optional device int32 */
+} moe_quant_fp8_args;
+
+moe_status moe_quantize_fp8(const moe_quant_fp8_args* args, void* stream);
+
+/* moe_grouped_gemm_fp8 -- the grouped product on block-scaled operands:
+ *     C[r][n] = sum_b a_s[b][r] * b_s[e][n/128][b]
+ *                 * sum_{k in block b} a[r][k] * b[e][n][k]
+ *   for every row r in [padded_offsets[e], padded_offsets[e] +
+ *   split_sizes[e]); the inner sums run in the matrix cores, the scaled
+ *   sums over blocks in fp32, one rounding to the output type.
+ *   Precision: for a bf16 output the inner sums come from the FP8 matrix
+ *   instructions, which add eight neighbouring products aligned to the
+ *   largest and keep 13 bits below it: at most 7 * 2^-13 of the sum of
+ *   magnitudes, in practice 2e-5 to 4e-5 of the result (a fiftieth of its
+ *   rounding to bf16).  An fp32 output is summed in fp32 throughout, from
+ *   operands widened to bf16, at half that rate.
+ *   a: row copy [M_cap][K]; b: per expert a tile copy [N][K] (b_stride
+ *   bytes and b_s_stride floats apart, 0: N * K and ceil(N/128) *
+ *   ceil(K/128)).  Forward products take the weights' tile copy, input
+ *   gradients that of the transposed weights (qT, sT).
+ *   c: bf16 or fp32 (c_type) [M_cap][ldc], ldc elements per row (0: N; a
+ *   multiple of 8).  Rows outside the groups are not written.
+ *   Groups may start at any row (padded_offsets need no alignment).  Groups
+ *   that overlap, run past M_cap or have a negative size are cut as in
+ *   moe_grouped_gemm, with MOE_DEVERR_BAD_OFFSETS.
+ *   Needs N % 16 == 0, K % 16 == 0, E <= 1024, K <= 2^22; a, b and c
+ *   16-byte aligned (b_stride too).
+ *   max_rows: the most rows any group can hold if the caller knows it (a
+ *   decoding step of T tokens: T), 0 if not.  It chooses among kernels;
+ *   groups that turn out larger are computed all the same.
+ *   workspace: optional, moe_grouped_gemm_fp8_workspace_size(...) bytes; its
+ *   contents need no initialisation and calls that overlap in time must
+ *   not share one.  Without it the last round of tiles is not split. */
+typedef struct moe_gemm_fp8_args {
+  int32_t E, N, K;
+  int64_t M_cap;
+  const int32_t* split_sizes;     /* [E]   device */
+  const int32_t* padded_offsets;  /* [E+1] device */
+  const uint8_t* a;
+  const float* a_s;               /* [ceil(K/128)][M_cap] */
+  const uint8_t* b;
+  const float* b_s;
+  int64_t b_stride;
+  int64_t b_s_stride;
+  void* c;
+  int64_t ldc;
+  int32_t c_type;                 /* moe_type */
+  int32_t max_rows;
+  int32_t cu_margin;
+  int32_t* err_flag;              /* optional device int32 */
+  void* workspace;
+  size_t workspace_bytes;
+} moe_gemm_fp8_args;
+
+size_t moe_grouped_gemm_fp8_workspace_size(int E, int N, int K, int64_t M_cap,
+                                           int max_rows);
+moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* args, void* stream);
+
+/* moe_grouped_wgrad_fp8 -- weight gradients on block-scaled operands:
+ *     C_e[p][q] = sum over the 128-row blocks m of expert e's padded span
+ *                 a_s[m][p] * b_s[m][q] * sum_{r in m} a[p][r] * b[q][r]
+ *   a: row copy [P][M_cap] (scales [M_cap/128][P]) and b: [Q][M_cap], the
+ *   transposed copies (MOE_QUANT_COL) of the two routed activations: dz and
+ *   xp for dW1 (P = N1, Q = H), dyp and a for dW2 (P = H, Q = I).  c: bf16
+ *   or fp32 [E][P][Q]; accumulate != 0 (fp32 only): added to what c holds.
+ *   An expert with no rows gets zeros (accumulate: stays as it is).
+ *   Group starts must be multiples of 128 (as moe_permute makes them): a
+ *   group with another start, or one that overlaps or runs past M_cap, is
+ *   cut or taken as empty with MOE_DEVERR_BAD_OFFSETS.  The pad rows up to
+ *   the next multiple of 128 are read and must encode zeros (as they do
+ *   where the quantized tensor has zeros there).  Precision as in
+ *   moe_grouped_gemm_fp8.
+ *   Needs P % 16 == 0, Q % 16 == 0, M_cap % 128 == 0, M_cap <= 4194304. */
+typedef struct moe_wgrad_fp8_args {
+  int32_t E, P, Q;
+  int64_t M_cap;
+  const int32_t* split_sizes;
+  const int32_t* padded_offsets;
+  const uint8_t* a;
+  const float* a_s;
+  const uint8_t* b;
+  const float* b_s;
+  void* c;
+  int32_t c_type;
+  int32_t accumulate;
+  int32_t cu_margin;
+  int32_t* err_flag;
+} moe_wgrad_fp8_args;
+
+moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_router_loss -- the router's auxiliary losses and per-expert counts
+ *   (moe_router_topk's softmax router).  With p[t] = softmax(logits[t]) over
+ *   all E experts, lse[t] = log sum exp logits[t], and the n tokens that
+ *   token_mask keeps (NULL: all T; byte 0 leaves a token out):
+ *     counts[e]    = how often e stands in expert_idx of a kept token
+ *     prob_mean[e] = (1/n) sum_t p[t][e]
+ *     loss[0] = balance_coef * E * sum_e counts[e] / (k n) * prob_mean[e]
+ *     loss[1] = z_coef * (1/n) sum_t lse[t]^2
+ *     n_tokens[0]  = n
+ *   An id outside [0, E) (a dropped pick) counts nowhere, one listed twice
+ *   twice.  Logits may be -infinity (an expert ruled out); a token whose
+ *   logits are all -infinity is left out as a masked one.  n == 0 gives
+ *   zeros.  Sums over tokens are made in a fixed order (fp32 inside a
+ *   workgroup, fp64 over workgroups): the same inputs give the same bits.
+ *   Needs 0 <= T, 1 <= E <= 1024, 1 <= k <= min(E, 8), T * k < 2^31;
+ *   workspace of moe_router_loss_workspace_size(T, E) bytes, no
+ *   initialisation.
+ *   Several processes: sum counts and n_tokens over them (and prob_mean
+ *   weighted by n_tokens) before moe_router_bwd, whose gradients are then
+ *   those of the joint loss. */
+typedef struct moe_router_loss_args {
+  int32_t T, E, k;
+  const float* logits;            /* [T][E] device */
+  const int32_t* expert_idx;      /* [T][k] device */
+  const uint8_t* token_mask;      /* optional [T] device */
+  float balance_coef, z_coef;
+  int32_t* counts;                /* [E] device, out */
+  int32_t* n_tokens;              /* [1] device, out */
+  float* prob_mean;               /* [E] device, out */
+  float* loss;                    /* [2] device, out */
+  void* workspace;
+  size_t workspace_bytes;
+} moe_router_loss_args;
+
+size_t moe_router_loss_workspace_size(int T, int E);
+moe_status moe_router_loss(const moe_router_loss_args* args, void* stream);
+
+/* moe_router_bwd -- the gradient with respect to the router's logits, of
+ *   the kept probabilities (dprobs [T][k], moe_unpermute's, optional) and of
+ *   both losses (dloss [2], their upstream gradients, optional: ones):
+ *     v[t][e] = sum_{s: expert_idx[t][s] = e} dprobs[t][s]
+ *               + kept(t) * dloss[0] * balance_coef * E * counts[e] / (k n^2)
+ *     dlogits[t][e] = p[t][e] * (v[t][e] - sum_i p[t][i] v[t][i]
+ *               + kept(t) * dloss[1] * 2 z_coef * lse[t] / n)
+ *   with counts and n = n_tokens[0] as moe_router_loss wrote them (n == 0: no
+ *   loss terms).  The mask leaves a token out of the losses only; its dprobs
+ *   act as any other's.  A token whose logits are all -infinity gets zeros.
+ *   counts and n_tokens may be NULL if both coefficients are 0. */
+typedef struct moe_router_bwd_args {
+  int32_t T, E, k;
+  const float* logits;            /* [T][E] device */
+  const int32_t* expert_idx;      /* [T][k] device */
+  const uint8_t* token_mask;      /* optional [T] device */
+  const float* dprobs;            /* optional [T][k] device */
+  const float* dloss;             /* optional [2] device */
+  float balance_coef, z_coef;
+  const int32_t* counts;          /* [E] device */
+  const int32_t* n_tokens;        /* [1] device */
+  float* dlogits;                 /* [T][E] device, out */
+} moe_router_bwd_args;
+
+moe_status moe_router_bwd(const moe_router_bwd_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Global gradient norm and clipping over a list of tensors (the weight
+ * gradients, the router's and any others of a step).
+ *   moe_grad_sumsq: *sumsq = sum of g^2 over every element of every tensor,
+ *     in fp64 and in an order that depends on the list alone.  Processes
+ *     that hold different parameters add their sums before clipping.
+ *   moe_grad_clip: norm = sqrt(*sumsq), f = min(1, max_norm / (norm +
+ *     1e-6)) (fp64, rounded to fp32 unless that is below its normal range),
+ *     out = g * f in fp32, one rounding to the tensor's type; *norm (optional) = norm.  out == data (or NULL)
+ *     scales in place.  If norm is infinite or NaN, f = 1 and
+ *     MOE_DEVERR_NONFINITE is set: the caller decides about the step.
+ *   tensors: host array, read before the call returns; n_tensors >= 0; data
+ *   contiguous, aligned to its type, numel >= 0.  moe_grad_clip refuses
+ *   lists in which a tensor to be written overlaps another one (the same
+ *   tensor twice, say): MOE_ERR_INVALID_ARG.
+ *   workspace: moe_grad_workspace_size(n_tensors) bytes, no initialisation.
+ * ---------------------------------------------------------------------- */
+typedef struct moe_tensor {
+  void* data;                     /* device */
+  void* out;                      /* device; NULL: data (moe_grad_clip) */
+  int64_t numel;
+  int32_t type;                   /* moe_type */
+} moe_tensor;
+
+typedef struct moe_grad_args {
+  const moe_tensor* tensors;      /* host */
+  int32_t n_tensors;
+  float max_norm;                 /* moe_grad_clip: >= 0 */
+  double* sumsq;                  /* device: out of moe_grad_sumsq, read by
+                                     moe_grad_clip */
+  float* norm;                    /* moe_grad_clip: optional device, out */
+  int32_t* err_flag;              /* moe_grad_clip: optional device */
+  void* workspace;                /* moe_grad_sumsq */
+  size_t workspace_bytes;
+} moe_grad_args;
+
+size_t moe_grad_workspace_size(int n_tensors);
+moe_status moe_grad_sumsq(const moe_grad_args* args, void* stream);
+moe_status moe_grad_clip(const moe_grad_args* args, void* stream);
 
 /* Workspace bytes for these sizes: the backward needs at least the dprobs
  * partials (fp32 M_cap x ceil(I / 256)); the full size adds the area where

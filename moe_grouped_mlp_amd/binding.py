@@ -19,12 +19,14 @@ ACT_SWIGLU, ACT_GEGLU, ACT_SRELU = 0, 1, 2
 PREC_BF16, PREC_MXFP8, PREC_MXFP4 = 0, 1, 2
 PERMUTE_BUILD_MAP, PERMUTE_GATHER, PERMUTE_WRITE_MX = 0x1, 0x2, 0x4
 PERMUTE_WRITE_MX4 = 0x8
-QUANT_ROW, QUANT_COL, QUANT_BOTH = 0, 1, 2
+QUANT_ROW, QUANT_COL, QUANT_BOTH, QUANT_TILE = 0, 1, 2, 3
+TYPE_BF16, TYPE_F32 = 0, 1
+FP8_BLOCK = 128
 GROUP_ALIGN = 128
 INTERLEAVE = 64
 MX_BLOCK = 32
 DEVERR_MCAP_OVERFLOW, DEVERR_DUP_EXPERT, DEVERR_SYNC_TIMEOUT = 0x1, 0x2, 0x4
-DEVERR_BAD_OFFSETS = 0x8
+DEVERR_BAD_OFFSETS, DEVERR_NONFINITE = 0x8, 0x10
 NOALLOC_SCRATCH_BYTES = 16 << 20
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_LAUNCH, ERR_DEVICE = 0, -1, -2, -3, -4, -5
 
@@ -37,6 +39,9 @@ EXPORTED_SYMBOLS = (
     "moe_mx_scale_offset", "moe_grouped_mlp_bwd_noalloc", "moe_router_route",
     "moe_router_route_workspace_size", "moe_clock_tick_rate_hz",
     "moe_gemm_clock_trace", "moe_bench_occupy", "moe_grouped_gemm_workspace_size",
+    "moe_quantize_fp8", "moe_grouped_gemm_fp8", "moe_grouped_gemm_fp8_workspace_size",
+    "moe_grouped_wgrad_fp8", "moe_router_loss", "moe_router_loss_workspace_size",
+    "moe_router_bwd", "moe_grad_sumsq", "moe_grad_clip", "moe_grad_workspace_size",
 )
 
 
@@ -169,6 +174,63 @@ class WgradArgs(ctypes.Structure):
                 ("timing_events", c_void_p * 3), ("err_flag", c_void_p)]
 
 
+class QuantFp8Args(ctypes.Structure):
+    _fields_ = [("mode", c_int32), ("batch", c_int32), ("rows", c_int32),
+                ("cols", c_int32), ("x_stride", c_int64), ("x", c_void_p),
+                ("q", c_void_p), ("s", c_void_p), ("qT", c_void_p),
+                ("sT", c_void_p), ("pow2", c_int32), ("live", c_void_p),
+                ("row_end", c_void_p)]
+
+
+class GemmFp8Args(ctypes.Structure):
+    _fields_ = [("E", c_int32), ("N", c_int32), ("K", c_int32),
+                ("M_cap", c_int64), ("split_sizes", c_void_p),
+                ("padded_offsets", c_void_p), ("a", c_void_p), ("a_s", c_void_p),
+                ("b", c_void_p), ("b_s", c_void_p), ("b_stride", c_int64),
+                ("b_s_stride", c_int64), ("c", c_void_p), ("ldc", c_int64),
+                ("c_type", c_int32), ("max_rows", c_int32), ("cu_margin", c_int32),
+                ("err_flag", c_void_p), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t)]
+
+
+class WgradFp8Args(ctypes.Structure):
+    _fields_ = [("E", c_int32), ("P", c_int32), ("Q", c_int32),
+                ("M_cap", c_int64), ("split_sizes", c_void_p),
+                ("padded_offsets", c_void_p), ("a", c_void_p), ("a_s", c_void_p),
+                ("b", c_void_p), ("b_s", c_void_p), ("c", c_void_p),
+                ("c_type", c_int32), ("accumulate", c_int32), ("cu_margin", c_int32),
+                ("err_flag", c_void_p)]
+
+
+class RouterLossArgs(ctypes.Structure):
+    _fields_ = [("T", c_int32), ("E", c_int32), ("k", c_int32),
+                ("logits", c_void_p), ("expert_idx", c_void_p),
+                ("token_mask", c_void_p), ("balance_coef", c_float),
+                ("z_coef", c_float), ("counts", c_void_p), ("n_tokens", c_void_p),
+                ("prob_mean", c_void_p), ("loss", c_void_p),
+                ("workspace", c_void_p), ("workspace_bytes", c_size_t)]
+
+
+class RouterBwdArgs(ctypes.Structure):
+    _fields_ = [("T", c_int32), ("E", c_int32), ("k", c_int32),
+                ("logits", c_void_p), ("expert_idx", c_void_p),
+                ("token_mask", c_void_p), ("dprobs", c_void_p), ("dloss", c_void_p),
+                ("balance_coef", c_float), ("z_coef", c_float),
+                ("counts", c_void_p), ("n_tokens", c_void_p), ("dlogits", c_void_p)]
+
+
+class Tensor(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("out", c_void_p), ("numel", c_int64),
+                ("type", c_int32)]
+
+
+class GradArgs(ctypes.Structure):
+    _fields_ = [("tensors", ctypes.POINTER(Tensor)), ("n_tensors", c_int32),
+                ("max_norm", c_float), ("sumsq", c_void_p), ("norm", c_void_p),
+                ("err_flag", c_void_p), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t)]
+
+
 # ---- library loading ------------------------------------------------------
 _LIB = None
 
@@ -206,6 +268,12 @@ def lib() -> ctypes.CDLL:
         L.moe_grouped_mlp_workspace_size.restype = c_size_t
         L.moe_grouped_mlp_workspace_size.argtypes = [
             c_int, c_int, c_int, c_int64, c_int, c_int]
+        L.moe_grouped_gemm_fp8_workspace_size.restype = c_size_t
+        L.moe_grouped_gemm_fp8_workspace_size.argtypes = [c_int, c_int, c_int, c_int64, c_int]
+        L.moe_router_loss_workspace_size.restype = c_size_t
+        L.moe_router_loss_workspace_size.argtypes = [c_int, c_int]
+        L.moe_grad_workspace_size.restype = c_size_t
+        L.moe_grad_workspace_size.argtypes = [c_int]
         for name, st in (("moe_permute", PermuteArgs),
                          ("moe_unpermute", UnpermuteArgs),
                          ("moe_quantize_mxfp8", QuantArgs),
@@ -217,7 +285,14 @@ def lib() -> ctypes.CDLL:
                          ("moe_router_topk", RouterArgs),
                          ("moe_router_route", RouterRouteArgs),
                          ("moe_grouped_gemm", GemmArgs),
-                         ("moe_glu_unfused", GluArgs)):
+                         ("moe_glu_unfused", GluArgs),
+                         ("moe_quantize_fp8", QuantFp8Args),
+                         ("moe_grouped_gemm_fp8", GemmFp8Args),
+                         ("moe_grouped_wgrad_fp8", WgradFp8Args),
+                         ("moe_router_loss", RouterLossArgs),
+                         ("moe_router_bwd", RouterBwdArgs),
+                         ("moe_grad_sumsq", GradArgs),
+                         ("moe_grad_clip", GradArgs)):
             f = getattr(L, name)
             f.restype = c_int
             f.argtypes = [ctypes.POINTER(st), c_void_p]
@@ -462,3 +537,171 @@ def moe_glu_unfused(*, direction, E, I, M_cap, split_sizes, padded_offsets,
                    _ptr(padded_offsets), _ptr(probs_p), _ptr(z), _ptr(a),
                    _ptr(amax), _ptr(da), _ptr(dz), _ptr(dprobs_p))
     _check("moe_glu_unfused", lib().moe_glu_unfused(ctypes.byref(args), _stream(stream)))
+
+
+# ---- block-scaled FP8, router losses, gradient norm -----------------------
+# These check what the C ABI cannot see: that a tensor is contiguous device
+# memory of the type and at least the size the call reads or writes, on the
+# device the call runs on (torch's current one).
+def _buf(fn, name, t, dtypes, n, dev):
+    if t is None:
+        return None
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise ValueError(f"{fn}: {name} must be a tensor of type {' or '.join(map(str, dtypes))}")
+    if not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{fn}: {name} must be contiguous with at least {n} elements")
+    if not t.is_cuda or t.device.index != dev:
+        raise ValueError(f"{fn}: {name} must be on the current device (cuda:{dev})")
+    return t.data_ptr()
+
+
+def _dtypes():
+    import torch
+    global _F32, _BF16, _U8, _I32, _F64, _CODES, _MASK
+    _F32, _BF16, _U8, _I32 = (torch.float32,), (torch.bfloat16,), (torch.uint8,), (torch.int32,)
+    _F64, _CODES, _MASK = (torch.float64,), (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.bool)
+
+
+_F32 = None
+
+
+def _device():
+    """The current device's index, for _buf."""
+    import torch
+    if _F32 is None:
+        _dtypes()
+    return torch.cuda.current_device()
+
+
+def _blocks(n):
+    return -(-n // FP8_BLOCK)
+
+
+def moe_quantize_fp8(*, mode, batch, rows, cols, x, q, s, qT=None, sT=None, pow2=False,
+                     x_stride=0, live=None, row_end=None, stream=None):
+    """bf16 -> block-scaled FP8 (E4M3 codes with fp32 scales per 128)."""
+    f, d = "moe_quantize_fp8", _device()
+    n = batch * rows * cols
+    rb, cb = _blocks(rows), _blocks(cols)
+    ns = {QUANT_ROW: cb * rows, QUANT_COL: rb * cols, QUANT_BOTH: cb * rows,
+          QUANT_TILE: rb * cb}.get(mode, 0) * batch
+    nsT = (rb * cb if mode == QUANT_TILE else rb * cols) * batch
+    nx = (batch - 1) * x_stride + rows * cols if x_stride and batch else n
+    a = QuantFp8Args(mode, batch, rows, cols, x_stride, _buf(f, "x", x, _BF16, nx, d),
+                     _buf(f, "q", q, _CODES, n, d), _buf(f, "s", s, _F32, ns, d),
+                     _buf(f, "qT", qT, _CODES, n, d), _buf(f, "sT", sT, _F32, nsT, d),
+                     int(bool(pow2)), _buf(f, "live", live, _I32, batch, d),
+                     _buf(f, "row_end", row_end, _I32, 1, d))
+    _check(f, lib().moe_quantize_fp8(ctypes.byref(a), _stream(stream)))
+
+
+def moe_grouped_gemm_fp8_workspace_size(E, N, K, M_cap, max_rows=0) -> int:
+    return lib().moe_grouped_gemm_fp8_workspace_size(E, N, K, M_cap, max_rows)
+
+
+def moe_grouped_gemm_fp8(*, E, N, K, M_cap, split_sizes, padded_offsets, a, a_s, b, b_s, c,
+                         b_stride=0, b_s_stride=0, ldc=0, c_type=TYPE_BF16, max_rows=0,
+                         cu_margin=0, err_flag=None, workspace=None, stream=None):
+    """C[r] = A[r] . B_e^T on block-scaled FP8 operands for every group's rows."""
+    f, d = "moe_grouped_gemm_fp8", _device()
+    nk, ns = N * K, _blocks(N) * _blocks(K)
+    args = GemmFp8Args(
+        E, N, K, M_cap, _buf(f, "split_sizes", split_sizes, _I32, E, d),
+        _buf(f, "padded_offsets", padded_offsets, _I32, E + 1, d),
+        _buf(f, "a", a, _CODES, M_cap * K, d), _buf(f, "a_s", a_s, _F32, M_cap * _blocks(K), d),
+        _buf(f, "b", b, _CODES, (E - 1) * (b_stride or nk) + nk, d),
+        _buf(f, "b_s", b_s, _F32, (E - 1) * (b_s_stride or ns) + ns, d), b_stride, b_s_stride,
+        _buf(f, "c", c, _F32 if c_type == TYPE_F32 else _BF16, (M_cap - 1) * (ldc or N) + N, d),
+        ldc, c_type, max_rows, cu_margin, _buf(f, "err_flag", err_flag, _I32, 1, d),
+        _buf(f, "workspace", workspace, _U8, 0, d), _nbytes(workspace))
+    _check(f, lib().moe_grouped_gemm_fp8(ctypes.byref(args), _stream(stream)))
+
+
+def moe_grouped_wgrad_fp8(*, E, P, Q, M_cap, split_sizes, padded_offsets, a, a_s, b, b_s, c,
+                          c_type=TYPE_BF16, accumulate=False, cu_margin=0, err_flag=None,
+                          stream=None):
+    """C_e = A_e . B_e^T over each group's routed rows (transposed FP8 copies)."""
+    f, d = "moe_grouped_wgrad_fp8", _device()
+    args = WgradFp8Args(
+        E, P, Q, M_cap, _buf(f, "split_sizes", split_sizes, _I32, E, d),
+        _buf(f, "padded_offsets", padded_offsets, _I32, E + 1, d),
+        _buf(f, "a", a, _CODES, P * M_cap, d), _buf(f, "a_s", a_s, _F32, P * _blocks(M_cap), d),
+        _buf(f, "b", b, _CODES, Q * M_cap, d), _buf(f, "b_s", b_s, _F32, Q * _blocks(M_cap), d),
+        _buf(f, "c", c, _F32 if c_type == TYPE_F32 else _BF16, E * P * Q, d), c_type,
+        int(bool(accumulate)), cu_margin, _buf(f, "err_flag", err_flag, _I32, 1, d))
+    _check(f, lib().moe_grouped_wgrad_fp8(ctypes.byref(args), _stream(stream)))
+
+
+def moe_router_loss_workspace_size(T, E) -> int:
+    return lib().moe_router_loss_workspace_size(T, E)
+
+
+def moe_router_loss(*, T, E, k, logits, expert_idx, counts, n_tokens, prob_mean, loss, workspace,
+                    balance_coef=0.0, z_coef=0.0, token_mask=None, stream=None):
+    """Per-expert counts, mean probabilities and loss = [balance, z]."""
+    f, d = "moe_router_loss", _device()
+    args = RouterLossArgs(
+        T, E, k, _buf(f, "logits", logits, _F32, T * E, d),
+        _buf(f, "expert_idx", expert_idx, _I32, T * k, d),
+        _buf(f, "token_mask", token_mask, _MASK, T, d), balance_coef, z_coef,
+        _buf(f, "counts", counts, _I32, E, d), _buf(f, "n_tokens", n_tokens, _I32, 1, d),
+        _buf(f, "prob_mean", prob_mean, _F32, E, d), _buf(f, "loss", loss, _F32, 2, d),
+        _buf(f, "workspace", workspace, _U8, 0, d), _nbytes(workspace))
+    _check(f, lib().moe_router_loss(ctypes.byref(args), _stream(stream)))
+
+
+def moe_router_bwd(*, T, E, k, logits, expert_idx, dlogits, dprobs=None, dloss=None, counts=None,
+                   n_tokens=None, balance_coef=0.0, z_coef=0.0, token_mask=None, stream=None):
+    """Gradient of the kept probabilities and of both losses with respect to
+    the router's logits."""
+    f, d = "moe_router_bwd", _device()
+    args = RouterBwdArgs(
+        T, E, k, _buf(f, "logits", logits, _F32, T * E, d),
+        _buf(f, "expert_idx", expert_idx, _I32, T * k, d),
+        _buf(f, "token_mask", token_mask, _MASK, T, d),
+        _buf(f, "dprobs", dprobs, _F32, T * k, d), _buf(f, "dloss", dloss, _F32, 2, d),
+        balance_coef, z_coef, _buf(f, "counts", counts, _I32, E, d),
+        _buf(f, "n_tokens", n_tokens, _I32, 1, d), _buf(f, "dlogits", dlogits, _F32, T * E, d))
+    _check(f, lib().moe_router_bwd(ctypes.byref(args), _stream(stream)))
+
+
+def moe_grad_workspace_size(n_tensors) -> int:
+    return lib().moe_grad_workspace_size(n_tensors)
+
+
+def _tensor_list(fn, tensors, out, dev):
+    import torch
+    outs = [None] * len(tensors) if out is None else list(out)
+    if len(outs) != len(tensors):
+        raise ValueError(f"{fn}: out must have as many tensors as the list")
+    arr = (Tensor * len(tensors))()
+    for i, (t, o) in enumerate(zip(tensors, outs)):
+        if t.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"{fn}: tensor {i} is {t.dtype}: bfloat16 or float32 is needed")
+        if o is not None and (o.dtype != t.dtype or o.numel() != t.numel()):
+            raise ValueError(f"{fn}: out {i} must have tensor {i}'s type and size")
+        arr[i] = Tensor(_buf(fn, f"tensor {i}", t, (t.dtype,), 0, dev),
+                        _buf(fn, f"out {i}", o, (t.dtype,), 0, dev), t.numel(),
+                        TYPE_BF16 if t.dtype == torch.bfloat16 else TYPE_F32)
+    return arr
+
+
+def moe_grad_sumsq(*, tensors, sumsq, workspace, stream=None):
+    """sumsq (float64 [1]) = sum of squares over a list of gradients."""
+    f, d = "moe_grad_sumsq", _device()
+    arr = _tensor_list(f, tensors, None, d)
+    args = GradArgs(arr, len(tensors), 0.0, _buf(f, "sumsq", sumsq, _F64, 1, d), None, None,
+                    _buf(f, "workspace", workspace, _U8, 0, d), _nbytes(workspace))
+    _check(f, lib().moe_grad_sumsq(ctypes.byref(args), _stream(stream)))
+
+
+def moe_grad_clip(*, tensors, sumsq, max_norm, out=None, norm=None, err_flag=None, stream=None):
+    """Scale the gradients (in place, or into out) so that their norm
+    sqrt(sumsq) is at most max_norm."""
+    f, d = "moe_grad_clip", _device()
+    arr = _tensor_list(f, tensors, out, d)
+    args = GradArgs(arr, len(tensors), max_norm, _buf(f, "sumsq", sumsq, _F64, 1, d),
+                    _buf(f, "norm", norm, _F32, 1, d), _buf(f, "err_flag", err_flag, _I32, 1, d),
+                    None, 0)
+    _check(f, lib().moe_grad_clip(ctypes.byref(args), _stream(stream)))

@@ -24,6 +24,8 @@ SOURCES = ["api.cpp", "route.hip", "router.hip", "unfused.hip", "permute.hip", "
            "gemm_glu_bf16.hip", "gemm_glu_mx.hip", "gemm_dglu_bf16.hip", "gemm_dglu_mx.hip", "gemm_wgrad.hip",
            "gemm_store_mx4.hip", "gemm_glu_mx4.hip", "gemm_dglu_mx4.hip", "gemm_wgrad_mx4.hip",
            "noalloc.hip",
+           "api_step.cpp", "fp8_quant.hip", "fp8_gemm.hip", "fp8_wgrad.hip", "fp8_gemm_rows.hip",
+           "router_loss.hip", "grad.hip",
            "router_route.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -768,4 +768,5 @@ moe_status grouped_mlp_bwd_impl(const moe_bwd_args* a, void* ws, size_t ws_bytes
 }
 moe_status grouped_mlp_bwd_check(const moe_bwd_args* a) { return bwd_check(a); }
 int64_t grouped_mlp_dprobs_parts(int I) { return dgrad_parts(I); }
+moe_status current_device(int* cu_count) { return device_info(cu_count); }
 }  // namespace moe

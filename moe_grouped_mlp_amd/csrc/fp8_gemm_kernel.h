@@ -1,0 +1,390 @@
+#pragma once
+
+// Grouped products on block-scaled FP8 operands (E4M3 codes, one fp32 scale
+// per 128 values along K) for gfx950.
+//
+//   C[t][n] = sum_b sa[b][t] sb[.][b] * sum_{k in block b} a[t][k] w[n][k]
+//
+// One v_mfma_f32_16x16x128_f8f6f4 covers a whole scale block of a 16 x 16
+// output tile, so the matrix core sums a block from zero and the vector ALU
+// adds it, scaled, to the fp32 accumulators: 4 fused multiply-adds (16
+// cycles) behind a 32-cycle MFMA, which the SIMD's other wave hides.  The
+// weight operand sits on the MFMA's rows and the tokens on its columns, so a
+// lane holds one token's outputs: the token's scale is one register per
+// column tile and the 128 x 128 weight scale is uniform.
+//
+// Work decomposition
+//   * Workgroup: 8 waves (two per SIMD), tile 64 J tokens x 256 weight rows,
+//     wave (wn, wt) = 128 weight rows x 16 J tokens (8 x J MFMA tiles).
+//   * Operands go from HBM straight into LDS (buffer loads with the LDS
+//     destination), two stages of one scale block (128 bytes of every row)
+//     each; their scales ride along.  16-byte chunk c of a row is stored at
+//     c ^ swizzle(row), which spreads the 16 rows of an operand read over all
+//     banks.
+//   * MFMA row m of weight tile i is weight row 64 (i / 4) + 16 (m / 4) +
+//     4 (i % 4) + m % 4: a lane then holds 16 consecutive outputs of its
+//     token per four tiles and stores them as whole 16-byte words.
+//   * Persistent workgroups walk the tiles of all experts, whose sizes are
+//     read from device memory.
+// Precision: the FP8 MFMAs add eight neighbouring products aligned to the
+// largest of them and keep 13 bits below it (seen with two products 2^-14
+// apart, in all four FP8 forms; products of different eights add exactly in
+// fp32).  On activations that is 2e-5 to 4e-5 of the result, a fiftieth of a
+// bf16 rounding, so bf16 outputs take it.  fp32 outputs would not be worth
+// their bits: there the codes are widened to bf16 in registers (16
+// conversions per 32 codes of a lane) and four 16x16x32 bf16 MFMAs, whose
+// sums are exact to 1e-8, stand for one FP8 MFMA, at half its peak rate.
+//
+// The weight gradient is the same product with the routed rows as K: both
+// operands transposed copies with one scale per row and block, so its
+// accumulation multiplies by two scales.
+#include "common.h"
+#include "kernels.h"
+
+namespace moe {
+namespace {
+
+constexpr int kFp8Threads = 512;
+constexpr int kFp8Waves = kFp8Threads / kWave;
+constexpr int kFp8BN = 256;            // weight rows of a tile
+constexpr int kFp8Blk = MOE_FP8_BLOCK; // K values (bytes) of a stage
+
+typedef __attribute__((address_space(3))) void fp8_lds_t;
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kFp8OutOfRange = 0x7fffffff;   // buffer offset past any record
+
+MOE_DEV __amdgpu_buffer_rsrc_t fp8_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0),
+                                           static_cast<int>(bytes), 0x00020000);
+}
+MOE_DEV void fp8_dma16(__amdgpu_buffer_rsrc_t r, void* lds, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (fp8_lds_t*)lds, 16, voff, soff, 0, 0);
+}
+MOE_DEV void fp8_dma4(__amdgpu_buffer_rsrc_t r, void* lds, int voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (fp8_lds_t*)lds, 4, voff, soff, 0, 0);
+}
+constexpr int fp8_wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0F70; }
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2_v __attribute__((ext_vector_type(2)));
+
+// One lane's operand of a 16 x 128 block: its 32 codes, or (WIDE) these
+// widened to bf16, which holds every E4M3 value.
+template <bool WIDE>
+struct Fp8Frag;
+template <>
+struct Fp8Frag<false> {
+  i32x8 v;
+  MOE_DEV void set(i32x4 x, i32x4 y) { v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7); }
+};
+template <>
+struct Fp8Frag<true> {
+  bf16x8_t v[4];
+  MOE_DEV static bf16x8_t widen(int a, int b) {
+    const bf16x2_v r0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+    const bf16x2_v r1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+    const bf16x2_v r2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+    const bf16x2_v r3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+    return bf16x8_t{r0[0], r0[1], r1[0], r1[1], r2[0], r2[1], r3[0], r3[1]};
+  }
+  MOE_DEV void set(i32x4 x, i32x4 y) {
+    v[0] = widen(x[0], x[1]);
+    v[1] = widen(x[2], x[3]);
+    v[2] = widen(y[0], y[1]);
+    v[3] = widen(y[2], y[3]);
+  }
+};
+
+// D = A . B over one scale block, summed from zero.
+MOE_DEV f32x4 fp8_block_mfma(const Fp8Frag<false>& a, const Fp8Frag<false>& b) {
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, zero, 0, 0, 0, 0, 0, 0);
+}
+MOE_DEV f32x4 fp8_block_mfma(const Fp8Frag<true>& a, const Fp8Frag<true>& b) {
+  f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], d, 0, 0, 0);
+  return d;
+}
+
+// Chunk swizzles of the LDS images.  An operand read takes one logical
+// 16-byte chunk of 16 rows per LDS cycle (256 bytes): tokens are 16
+// consecutive rows; weights are rows 16 x + y, x < 4, y in a run of 4.
+MOE_DEV int fp8_swz_t(int row) { return (row >> 1) & 7; }
+MOE_DEV int fp8_swz_w(int row) { return ((row >> 1) & 1) | ((row >> 3) & 6); }
+
+// A group's rows as the kernels see them: cut to what lies between its start,
+// the next start and the buffer's end.
+MOE_DEV int fp8_group_rows(const Fp8Args& g, int e, bool aligned, bool& bad) {
+  const int64_t n = g.split[e], p0 = g.padded[e], p1 = g.padded[e + 1];
+  const int64_t end = p1 < g.M_cap ? p1 : g.M_cap;
+  const int64_t span = aligned ? (n + kFp8Blk - 1) / kFp8Blk * kFp8Blk : n;
+  bad = n < 0 || p0 < 0 || p0 + span > end || (aligned && n > 0 && p0 % kFp8Blk != 0);
+  if (!bad) return static_cast<int>(n);
+  if (n < 0 || p0 < 0 || p0 >= end || (aligned && (p0 % kFp8Blk != 0))) return 0;
+  if (aligned) return static_cast<int>((end - p0) / kFp8Blk * kFp8Blk);
+  return static_cast<int>(end - p0);
+}
+
+// One operand tile of R rows x 128 bytes per stage: this wave's share of the
+// R / 8 one-kilobyte loads (8 rows each).
+template <int R, bool W>
+struct Fp8Loader {
+  static constexpr int kInstr = R / 8 / kFp8Waves;
+  __amdgpu_buffer_rsrc_t rsrc;
+  int voff[kInstr];
+  int kbyte[kInstr];
+
+  // base: the tile's first row at the group's first K value; ld: bytes
+  // between rows; rows: rows that exist; k: K values that exist
+  MOE_DEV void init(const uint8_t* base, int rows, int64_t ld, int k, int wave, int lane) {
+    const int64_t bytes = rows > 0 ? (rows < R ? rows - 1 : R - 1) * ld + k : 0;
+    rsrc = fp8_rsrc(base, static_cast<uint32_t>(bytes));
+#pragma unroll
+    for (int j = 0; j < kInstr; ++j) {
+      const int row = (wave * kInstr + j) * 8 + (lane >> 3);
+      const int c = (lane & 7) ^ (W ? fp8_swz_w(row) : fp8_swz_t(row));
+      kbyte[j] = 16 * c;
+      voff[j] = row < rows ? static_cast<int>(row * ld) + 16 * c : kFp8OutOfRange;
+    }
+  }
+  // Stage kt; chunks at or past K value k read as zeros.
+  MOE_DEV void issue(uint8_t* stage, int kt, int wave_s, int k) {
+    const int left = k - kt * kFp8Blk;
+#pragma unroll
+    for (int j = 0; j < kInstr; ++j)
+      fp8_dma16(rsrc, stage + (wave_s * kInstr + j) * 1024, kbyte[j] < left ? voff[j] : kFp8OutOfRange,
+                left > 0 ? kt * kFp8Blk : 0);
+  }
+};
+
+// J: MFMA token tiles per wave; WG: the weight gradient; F32: fp32 output,
+// summed from widened operands.
+template <int J, bool WG, bool F32>
+__global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 2))) void fp8_gemm_kernel(
+    const Fp8Args g) {
+  constexpr int BT = 64 * J;   // tokens of a tile
+  __shared__ __attribute__((aligned(1024))) uint8_t sT0[BT * kFp8Blk], sT1[BT * kFp8Blk];
+  __shared__ __attribute__((aligned(1024))) uint8_t sW0[kFp8BN * kFp8Blk], sW1[kFp8BN * kFp8Blk];
+  // scales of a stage: tokens at 0, weights at 256 (WG: one per row, else the
+  // tile's two 128-row blocks)
+  __shared__ __attribute__((aligned(16))) float sS0[512], sS1[512];
+  __shared__ int s_start[kMaxExperts + 1], s_rows[kMaxExperts], s_tmp[kFp8Waves];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wave_s = __builtin_amdgcn_readfirstlane(wave);
+  const int wn = wave & 1, wt = wave >> 1;
+  const int tiles_n = (g.N + kFp8BN - 1) / kFp8BN;
+
+  // ---- tile prefix over the experts ----
+  auto tiles_of = [&](int rows) { return (WG ? (g.P + BT - 1) / BT : (rows + BT - 1) / BT) * tiles_n; };
+  {
+    const int per = (g.E + kFp8Threads - 1) / kFp8Threads;   // 1 or 2
+    int mine = 0;
+    for (int i = 0; i < per; ++i) {
+      const int e = tid * per + i;
+      if (e < g.E) {
+        bool bad;
+        const int n = fp8_group_rows(g, e, WG, bad);
+        if (bad && blockIdx.x == 0) set_err(g.err, MOE_DEVERR_BAD_OFFSETS);
+        s_rows[e] = n;
+        mine += tiles_of(n);
+      }
+    }
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int v = __shfl_up(inc, o, kWave);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 63) s_tmp[wave] = inc;
+    __syncthreads();
+    int run = inc - mine, total = 0;
+    for (int w = 0; w < kFp8Waves; ++w) {
+      if (w < wave) run += s_tmp[w];
+      total += s_tmp[w];
+    }
+    for (int i = 0; i < per; ++i) {
+      const int e = tid * per + i;
+      if (e < g.E) {
+        s_start[e] = run;
+        run += tiles_of(s_rows[e]);
+      }
+    }
+    if (tid == 0) s_start[g.E] = total;
+    __syncthreads();
+  }
+  const int total = s_start[g.E];
+
+  // contiguous runs of tiles for each XCD (workgroup ids go round the XCDs)
+  const int G = gridDim.x;
+  int vid = blockIdx.x;
+  if (G % kNumXcd == 0) vid = (blockIdx.x % kNumXcd) * (G / kNumXcd) + blockIdx.x / kNumXcd;
+
+  // operand reads: byte offsets of the lane's row and its two chunks
+  const int l16 = lane & 15, g4 = lane >> 4;
+  const int t_row = 16 * J * wt + l16;
+  const int w_row = 128 * wn + 16 * (l16 >> 2) + (l16 & 3);
+  const int t_sw = fp8_swz_t(t_row);   // unchanged by + 16 j
+
+  for (int id = vid; id < total; id += G) {
+    int lo = 0, hi = g.E - 1;   // the expert of the tile
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_start[mid] <= id) lo = mid; else hi = mid - 1;
+    }
+    const int e = __builtin_amdgcn_readfirstlane(lo);
+    const int in_e = __builtin_amdgcn_readfirstlane(id - s_start[lo]);
+    const int n_e = __builtin_amdgcn_readfirstlane(s_rows[lo]);
+    const int start = __builtin_amdgcn_readfirstlane(g.padded[lo]);
+    const int rows_t = WG ? g.P : n_e;   // token rows of the expert
+    // bands of group_m token tiles, all weight tiles of a band in turn
+    const int tiles_t = (rows_t + BT - 1) / BT;
+    const int band = in_e / (g.group_m * tiles_n), in_b = in_e - band * g.group_m * tiles_n;
+    const int gm = tiles_t - band * g.group_m < g.group_m ? tiles_t - band * g.group_m : g.group_m;
+    const int t0 = (band * g.group_m + in_b % gm) * BT, n0 = in_b / gm * kFp8BN;
+
+    const int K = WG ? (n_e + kFp8Blk - 1) / kFp8Blk * kFp8Blk : g.K;
+    const int steps = (K + kFp8Blk - 1) / kFp8Blk;
+    const int rows_a = rows_t - t0, rows_b = g.N - n0;
+    Fp8Loader<BT, false> lt;
+    Fp8Loader<kFp8BN, true> lw;
+    const uint8_t* b_e = static_cast<const uint8_t*>(g.b) + (WG ? start : e * g.b_stride);
+    lt.init(g.a + (WG ? static_cast<int64_t>(t0) * g.M_cap + start
+                      : static_cast<int64_t>(start + t0) * g.K),
+            rows_a, WG ? g.M_cap : g.K, K, wave_s, lane);
+    const int64_t ld_b = WG ? g.M_cap : g.K;
+    lw.init(b_e + n0 * ld_b, rows_b, ld_b, K, wave_s, lane);
+    // this wave's 64 scales of a stage: waves 0 .. 3 tokens, 4 .. 7 weights
+    const bool s_tok = wave_s < 4;
+    const int s_i = (wave_s & 3) * 64 + lane;
+    const float* s_base;
+    int64_t s_step;
+    int s_voff = kFp8OutOfRange;
+    if (s_tok) {
+      s_base = WG ? g.a_s + static_cast<int64_t>(start / kFp8Blk) * g.P + t0 : g.a_s + start + t0;
+      s_step = WG ? g.P : g.M_cap;
+      if (s_i < BT && s_i < rows_a) s_voff = 4 * s_i;
+    } else if constexpr (WG) {
+      s_base = g.b_s + static_cast<int64_t>(start / kFp8Blk) * g.N + n0;
+      s_step = g.N;
+      if (s_i < rows_b) s_voff = 4 * s_i;
+    } else {
+      s_base = g.b_s + e * g.b_s_stride + static_cast<int64_t>(n0 / kFp8Blk) * steps;
+      s_step = 1;
+      if (s_i < 2 && s_i * kFp8Blk < rows_b) s_voff = 4 * s_i * steps;
+    }
+    auto issue = [&](uint8_t* sT, uint8_t* sW, float* sS, int kt) {
+      const int k_left = kt < steps ? K : 0;   // past the end: zeros
+      lt.issue(sT, kt, wave_s, k_left);
+      lw.issue(sW, kt, wave_s, k_left);
+      fp8_dma4(fp8_rsrc(s_base + (kt < steps ? kt : 0) * s_step, 0x7ffffffeu), sS + wave_s * 64,
+               kt < steps ? s_voff : kFp8OutOfRange, 0);
+    };
+    constexpr int kLoads = Fp8Loader<BT, false>::kInstr + Fp8Loader<kFp8BN, true>::kInstr + 1;
+
+    f32x4 acc[8][J];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < J; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    auto step = [&](const uint8_t* sT, const uint8_t* sW, const float* sS) {
+      float f[J];
+      Fp8Frag<F32> t[J];
+      const float ws = WG ? 1.0f : sS[256 + wn];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        f[j] = sS[t_row + 16 * j] * ws;
+        const uint8_t* r = sT + (t_row + 16 * j) * kFp8Blk;
+        const i32x4 x = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4) ^ t_sw));
+        const i32x4 y = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4 + 1) ^ t_sw));
+        t[j].set(x, y);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = w_row + 64 * (i >> 2) + 4 * (i & 3);
+        const uint8_t* r = sW + row * kFp8Blk;
+        const int sw = fp8_swz_w(row);
+        const i32x4 x = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4) ^ sw));
+        const i32x4 y = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4 + 1) ^ sw));
+        Fp8Frag<F32> w;
+        w.set(x, y);
+        f32x4 wf;
+        if constexpr (WG)
+          wf = *reinterpret_cast<const f32x4*>(sS + 256 + 128 * wn + 64 * (i >> 2) + 16 * g4 + 4 * (i & 3));
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const f32x4 p = fp8_block_mfma(w, t[j]);
+#pragma unroll
+          for (int r4 = 0; r4 < 4; ++r4) {
+            const float s = WG ? f[j] * wf[r4] : f[j];
+            acc[i][j][r4] = __builtin_fmaf(p[r4], s, acc[i][j][r4]);
+          }
+        }
+      }
+    };
+    // waits for this wave's LDS reads first, whose results the compiler may
+    // use only behind the barrier
+    auto barrier = [&]() {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+
+    if (steps > 0) {
+      issue(sT0, sW0, sS0, 0);
+      issue(sT1, sW1, sS1, 1);
+      for (int kt = 0; kt < steps; kt += 2) {
+        __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kLoads));   // stage kt landed
+        barrier();
+        step(sT0, sW0, sS0);
+        barrier();   // every wave has read the stage
+        issue(sT0, sW0, sS0, kt + 2);
+        __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kLoads));
+        barrier();
+        if (kt + 1 < steps) step(sT1, sW1, sS1);
+        barrier();
+        issue(sT1, sW1, sS1, kt + 3);
+      }
+      __builtin_amdgcn_s_waitcnt(fp8_wait_vm(0));   // the zero fills past the end
+      barrier();
+    }
+
+    // ---- store: 16 consecutive outputs of a token per four weight tiles ----
+    const int64_t c_row0 = WG ? static_cast<int64_t>(e) * g.P + t0 : static_cast<int64_t>(start) + t0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      const int tok = t_row + 16 * j;
+      if (tok < rows_a) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int n = 128 * wn + 64 * v + 16 * g4;
+          if (n < rows_b) {   // N % 16 == 0: all 16 or none
+            const int64_t at = (c_row0 + tok) * g.ldc + n0 + n;
+            if constexpr (F32) {
+              f32x4* c = reinterpret_cast<f32x4*>(static_cast<float*>(g.c) + at);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                c[i] = WG && g.accumulate ? c[i] + acc[4 * v + i][j] : acc[4 * v + i][j];
+            } else {
+              uint4* c = reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.c) + at);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const f32x4 &x = acc[4 * v + 2 * i][j], &y = acc[4 * v + 2 * i + 1][j];
+                c[i] = uint4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                             pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace moe

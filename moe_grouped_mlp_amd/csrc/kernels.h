@@ -133,11 +133,69 @@ hipError_t launch_dprobs_reduce(const float* part, int n_part, const int32_t* sp
                                 const int32_t* padded, int E, int64_t M_cap,
                                 float* dprobs_p, hipStream_t s);
 
+// ---- block-scaled FP8 -----------------------------------------------------
+hipError_t launch_quantize_fp8(const moe_quant_fp8_args& a, hipStream_t s);
+
+// A grouped product: tokens a (rows of the groups) against weights b.  The
+// weight gradient takes the same kernel with the transposed copies: tokens
+// are a's P rows, weights b's N = Q rows, K the group's routed rows.
+struct Fp8Args {
+  int E, N, K;             // K: not for the weight gradient
+  int P;                   // weight gradient: rows of a and of each expert's C
+  int64_t M_cap;
+  const int32_t* split;
+  const int32_t* padded;
+  const uint8_t* a;
+  const float* a_s;
+  const uint8_t* b;
+  const float* b_s;
+  int64_t b_stride, b_s_stride;   // between experts (product only)
+  void* c;
+  int64_t ldc;
+  int accumulate;          // weight gradient, fp32: C +=
+  int group_m;             // token tiles per band of the tile order
+  int32_t* err;            // nullable
+};
+// tile_rows: 64, 128 or (bf16 output) 256 tokens per workgroup tile
+hipError_t launch_fp8_gemm(const Fp8Args& g, int tile_rows, bool f32, int grid, hipStream_t s);
+// groups of few rows; tile_rows: 16 or 32 tokens at a time
+hipError_t launch_fp8_rows(const Fp8Args& g, int tile_rows, bool f32, hipStream_t s);
+hipError_t launch_fp8_wgrad(const Fp8Args& g, bool f32, int grid, hipStream_t s);
+
+// ---- router losses ----------------------------------------------------------
+int router_loss_blocks(int T, int E);   // workgroups of the loss kernel
+hipError_t launch_router_loss(const moe_router_loss_args& a, hipStream_t s);
+hipError_t launch_router_bwd(const moe_router_bwd_args& a, hipStream_t s);
+
+// ---- gradient norm and clipping -----------------------------------------------
+constexpr int kGradList = 96;         // tensors of one launch (3 KB of arguments)
+constexpr int kGradBlocks = 2048;     // workgroups of one launch at most
+constexpr int64_t kGradChunk = 16384; // elements a workgroup takes at a time
+struct GradEntry {
+  const void* data;
+  void* out;
+  int64_t numel;
+  int64_t first;           // chunks of the entries before it
+  int32_t type;
+};
+struct GradList {
+  GradEntry t[kGradList];
+  int n;
+  int64_t chunks;
+};
+int grad_blocks(int64_t chunks);
+hipError_t launch_grad_sumsq(const GradList& l, double* partial, hipStream_t s);
+hipError_t launch_grad_sum(const double* partial, int n, double* sumsq, hipStream_t s);
+hipError_t launch_grad_scale(const GradList& l, const double* sumsq, float max_norm, float* norm,
+                             int32_t* err, hipStream_t s);
+
 // ---- entry-point bodies shared between C-ABI variants (api.cpp) ---------
 // moe_grouped_mlp_bwd with the workspace given apart from the arguments
 moe_status grouped_mlp_bwd_impl(const moe_bwd_args* a, void* ws, size_t ws_bytes,
                                 void* stream);
 moe_status grouped_mlp_bwd_check(const moe_bwd_args* a);  // host-side checks only
 int64_t grouped_mlp_dprobs_parts(int I);  // fp32 dprobs partials per row
+// the current device's CU count, or MOE_ERR_DEVICE (looked up once per device)
+moe_status current_device(int* cu_count);
 
 }  // namespace moe

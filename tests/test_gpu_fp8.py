@@ -1,0 +1,574 @@
+"""Block-scaled FP8 (moe_quantize_fp8, moe_grouped_gemm_fp8,
+moe_grouped_wgrad_fp8) against the float64 oracle through the C ABI.
+
+* Codes and scales are bit-exact (the encoding is defined operation by
+  operation).
+* Products of small integers with power-of-two scales are exact, so they are
+  compared bit for bit; on random data every element is held to the bound of
+  its own sum: with S the sum of |a w| (dequantized), each of the at most 128
+  additions inside a block and of the scaled additions over blocks is off by
+  at most one fp32 step (2^-23) of a partial sum that S bounds, so
+      |err| <= (128 + blocks + 4) 2^-23 S   for fp32 outputs.
+  bf16 outputs add half a bf16 step, 2^-8 |c|, and what the FP8 matrix
+  instructions drop: of eight neighbouring products the other seven lose what
+  lies more than 13 bits below the largest, so at most 7 * 2^-13 of the
+  largest, which S bounds over the groups of eight."""
+
+import numpy as np
+import pytest
+import torch
+
+import moe_grouped_mlp_amd as mg
+from oracle import numerics as nu
+from oracle import step as st
+
+from .gpu_util import dev_bf16
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+NAN_BITS = 0x7FC1
+
+
+def setup_module(module):
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    mg.lib()
+
+
+def _bf16(rng, *shape, spread=2.0):
+    v = rng.standard_normal(shape) * np.exp(spread * rng.standard_normal(shape[:-1] + (1,)))
+    return nu.round_bf16(v)
+
+
+def _up(x):
+    return dev_bf16(nu.f64_to_bf16_bits(x))
+
+
+def _u8(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+
+
+# --------------------------------------------------------------- quantize --
+def _quantize(x, mode, pow2=False, batch=1, sentinel=0xA5, **kw):
+    """x float64 [batch][rows][cols]; returns host q, s, qT, sT."""
+    b, R, K = x.shape
+    nb, nr = -(-K // 128), -(-R // 128)
+    q = torch.full((b, R, K), sentinel, dtype=torch.uint8, device=DEV)
+    qT = torch.full((b, K, R), sentinel, dtype=torch.uint8, device=DEV)
+    s = torch.full((b, nr, nb) if mode == mg.QUANT_TILE else (b, nb, R), -7.0, device=DEV)
+    sT = torch.full((b, nb, nr) if mode == mg.QUANT_TILE else (b, nr, K), -7.0, device=DEV)
+    xd = kw.pop("dev", None)
+    kw["x"] = _up(x) if xd is None else xd
+    if mode == mg.QUANT_COL:
+        mg.moe_quantize_fp8(mode=mode, batch=b, rows=R, cols=K, q=qT, s=sT, pow2=pow2, **kw)
+    else:
+        mg.moe_quantize_fp8(mode=mode, batch=b, rows=R, cols=K, q=q, s=s, pow2=pow2,
+                            qT=None if mode == mg.QUANT_ROW else qT,
+                            sT=None if mode == mg.QUANT_ROW else sT, **kw)
+    torch.cuda.synchronize()
+    return [t.cpu().numpy() for t in (q, s, qT, sT)]
+
+
+ROW_SIZES = [(1, 16), (1, 128), (3, 144), (16, 4096), (17, 2880), (33, 48), (130, 272), (2050, 1040)]
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("R,K", ROW_SIZES)
+def test_quantize_rows(R, K, pow2):
+    x = _bf16(np.random.default_rng(R * 7 + K), 1, R, K)
+    q, s, _, _ = _quantize(x, mg.QUANT_ROW, pow2)
+    rq, rs = st.quantize_rows(x[0], pow2)
+    np.testing.assert_array_equal(s[0], rs)
+    np.testing.assert_array_equal(q[0], rq)
+
+
+TILE_SIZES = [(16, 16), (128, 128), (144, 32), (272, 400), (640, 1296), (1040, 2064)]
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("R,K", TILE_SIZES)
+def test_quantize_both_and_col(R, K, pow2):
+    x = _bf16(np.random.default_rng(R + K), 1, R, K)
+    rq, rs = st.quantize_rows(x[0], pow2)
+    tq, ts = st.quantize_rows(x[0].T, pow2)
+    q, s, qT, sT = _quantize(x, mg.QUANT_BOTH, pow2)
+    np.testing.assert_array_equal(s[0], rs)
+    np.testing.assert_array_equal(q[0], rq)
+    np.testing.assert_array_equal(sT[0], ts)
+    np.testing.assert_array_equal(qT[0], tq)
+    _, _, qT, sT = _quantize(x, mg.QUANT_COL, pow2)
+    np.testing.assert_array_equal(sT[0], ts)
+    np.testing.assert_array_equal(qT[0], tq)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("R,K", TILE_SIZES)
+def test_quantize_tiles_batched_with_live_mask(R, K, pow2):
+    b = 3
+    x = _bf16(np.random.default_rng(R * K), b, R, K)
+    live = torch.tensor([5, 0, 1], dtype=torch.int32, device=DEV)
+    q, s, qT, sT = _quantize(x, mg.QUANT_TILE, pow2, live=live)
+    for i in (0, 2):
+        rq, rs = st.quantize_tiles(x[i], pow2)
+        np.testing.assert_array_equal(s[i], rs)
+        np.testing.assert_array_equal(sT[i], rs.T)
+        np.testing.assert_array_equal(q[i], rq)
+        np.testing.assert_array_equal(qT[i], rq.T)
+    for t in (q, qT):
+        assert (t[1] == 0xA5).all()
+    assert (s[1] == -7).all() and (sT[1] == -7).all()
+    # without the transposed copy
+    q2 = torch.empty(b, R, K, dtype=torch.uint8, device=DEV)
+    s2 = torch.empty(*s.shape, device=DEV)
+    mg.moe_quantize_fp8(mode=mg.QUANT_TILE, batch=b, rows=R, cols=K, x=_up(x), q=q2, s=s2, pow2=pow2)
+    assert np.array_equal(q2.cpu().numpy()[0], q[0]) and np.array_equal(s2.cpu().numpy()[2], s[2])
+
+
+def test_quantize_strided_batch_and_float8_views():
+    rng = np.random.default_rng(4)
+    x = _bf16(rng, 3, 32, 144)
+    flat = torch.full((3 * 5000,), float("nan"), dtype=torch.bfloat16, device=DEV)
+    for i in range(3):
+        flat[i * 5000:i * 5000 + 32 * 144] = _up(x[i]).reshape(-1)
+    q = torch.empty(3, 32, 144, dtype=torch.float8_e4m3fn, device=DEV)
+    s = torch.empty(3, 2, 32, device=DEV)
+    mg.moe_quantize_fp8(mode=mg.QUANT_ROW, batch=3, rows=32, cols=144, x=flat, x_stride=5000, q=q, s=s)
+    for i in range(3):
+        rq, rs = st.quantize_rows(x[i])
+        np.testing.assert_array_equal(q.view(torch.uint8)[i].cpu().numpy(), rq)
+        np.testing.assert_array_equal(s[i].cpu().numpy(), rs)
+
+
+def _special():
+    """Zeros, -0, the smallest and largest bf16 magnitudes, NaN, infinities."""
+    x = _bf16(np.random.default_rng(9), 1, 144, 144)
+    x[0, 0] = 0.0
+    x[0, 1] = -0.0
+    x[0, 2, :128] = 2.0 ** -133
+    x[0, 3, 5] = 3.3895313892515355e38
+    x[0, 4] = 2.0 ** -101
+    x[0, 5, 7] = 448.0
+    x[0, 5, 8:] = 0.01
+    return nu.round_bf16(x)   # what the device gets
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+def test_quantize_special_values(pow2):
+    x = _special()
+    for mode in (mg.QUANT_ROW, mg.QUANT_BOTH):
+        q, s, qT, sT = _quantize(x, mode, pow2)
+        rq, rs = st.quantize_rows(x[0], pow2)
+        np.testing.assert_array_equal(s[0], rs)
+        np.testing.assert_array_equal(q[0], rq)
+        if mode == mg.QUANT_BOTH:
+            tq, ts = st.quantize_rows(x[0].T, pow2)
+            np.testing.assert_array_equal(sT[0], ts)
+            np.testing.assert_array_equal(qT[0], tq)
+
+
+@pytest.mark.parametrize("pow2", [False, True])
+def test_quantize_nan_and_infinity(pow2):
+    x = _bf16(np.random.default_rng(10), 1, 16, 256)
+    x[0, 3, 10] = np.nan
+    x[0, 6, 20] = np.inf
+    q, s, _, _ = _quantize(x, mg.QUANT_ROW, pow2)
+    rq, rs = st.quantize_rows(x[0], pow2)
+    np.testing.assert_array_equal(s[0], rs)
+    assert q[0, 3, 10] & 0x7F == 0x7F and np.isinf(s[0, 0, 6])
+    ok = np.ones_like(rq, bool)
+    ok[3, 10] = False
+    ok[6, 20] = False
+    np.testing.assert_array_equal(q[0][ok], rq[ok])
+    with np.errstate(invalid="ignore"):
+        assert np.isnan(st.dequantize_rows(q[0], s[0])[6, :128]).all()
+
+
+@pytest.mark.parametrize("used", [0, 1, 16, 100, 128, 129, 300, 400])
+def test_quantize_row_end(used):
+    R, K = 320, 144
+    x = _bf16(np.random.default_rng(used), 1, R, K)
+    end = torch.tensor([used], dtype=torch.int32, device=DEV)
+    xd = _up(x)
+    xd[0, min(used, R):] = float("nan")   # not read
+    n = min(used, R)
+    z = x[0].copy()
+    z[n:] = 0.0
+    blocks = -(-n // 128) * 128
+    rq, rs = st.quantize_rows(x[0])
+    tq, ts = st.quantize_rows(z.T)
+    for mode in (mg.QUANT_ROW, mg.QUANT_BOTH):
+        q, s, qT, sT = _quantize(x, mode, dev=xd, row_end=end)
+        np.testing.assert_array_equal(q[0, :n], rq[:n])
+        np.testing.assert_array_equal(s[0][:, :n], rs[:, :n])
+        assert (q[0, n:] == 0xA5).all() and (s[0][:, n:] == -7).all()
+        if mode == mg.QUANT_BOTH:
+            m = min(blocks, R)
+            np.testing.assert_array_equal(qT[0][:, :m], tq[:, :m])
+            np.testing.assert_array_equal(sT[0][:blocks // 128], ts[:blocks // 128])
+            assert (qT[0][:, m:] == 0xA5).all() and (sT[0][blocks // 128:] == -7).all()
+    zq, zs = st.quantize_tiles(z)
+    q, s, qT, sT = _quantize(x, mg.QUANT_TILE, dev=xd, row_end=end)
+    np.testing.assert_array_equal(q[0, :n], zq[:n])
+    np.testing.assert_array_equal(s[0][:blocks // 128], zs[:blocks // 128])
+    np.testing.assert_array_equal(qT[0][:, :min(blocks, R)], zq.T[:, :min(blocks, R)])
+
+
+# ---------------------------------------------------------------- product --
+def _starts(sizes, align=128):
+    o = [0]
+    for n in sizes:
+        o.append(o[-1] + -(-n // align) * align)
+    return o
+
+
+def _operands(rng, sizes, starts, M_cap, N, K, exact=False):
+    """Codes and scales of a row copy [M_cap][K] and of E tile copies [N][K].
+    exact: integers up to 7 and power-of-two scales."""
+    E = len(sizes)
+    nk, nn = -(-K // 128), -(-N // 128)
+    if exact:
+        a_q = nu.e4m3_encode(rng.integers(-7, 8, (M_cap, K)).astype(np.float64))
+        b_q = nu.e4m3_encode(rng.integers(-7, 8, (E, N, K)).astype(np.float64))
+        a_s = 2.0 ** rng.integers(-2, 3, (nk, M_cap)).astype(np.float32)
+        b_s = 2.0 ** rng.integers(-2, 3, (E, nn, nk)).astype(np.float32)
+    else:
+        a_q, a_s = st.quantize_rows(_bf16(rng, M_cap, K, spread=1.0))
+        w = [st.quantize_tiles(0.05 * _bf16(rng, N, K, spread=0.5)) for _ in range(E)]
+        b_q, b_s = np.stack([q for q, _ in w]), np.stack([s for _, s in w])
+    # rows that belong to no group hold NaN codes and NaN scales
+    used = np.zeros(M_cap, bool)
+    for n, o in zip(sizes, starts):
+        used[o:o + n] = True
+    a_q[~used] = 0x7F
+    a_s[:, ~used] = np.nan
+    return a_q, a_s.astype(np.float32), b_q, b_s.astype(np.float32)
+
+
+def _reference(a_q, a_s, b_q, b_s, sizes, starts):
+    a = st.dequantize_rows(a_q, a_s)
+    w = np.stack([st.dequantize_tiles(q, s) for q, s in zip(b_q, b_s)])
+    return st.grouped_product(a, w, sizes, starts)
+
+
+def _product(a_q, a_s, b_q, b_s, sizes, starts, c_type=mg.TYPE_F32, max_rows=0, ldc=0, err=None,
+             workspace=True, **kw):
+    E, N, K = b_q.shape
+    M_cap = a_q.shape[0]
+    dt = torch.float32 if c_type == mg.TYPE_F32 else torch.bfloat16
+    c = torch.full((M_cap, ldc or N), -77.0, dtype=dt, device=DEV)
+    ws = mg.moe_grouped_gemm_fp8_workspace_size(E, N, K, M_cap, max_rows) if workspace else 0
+    mg.moe_grouped_gemm_fp8(
+        E=E, N=N, K=K, M_cap=M_cap, split_sizes=torch.tensor(sizes, dtype=torch.int32, device=DEV),
+        padded_offsets=torch.tensor(starts, dtype=torch.int32, device=DEV), a=_u8(a_q), a_s=_u8(a_s),
+        b=kw.pop("b", None) if "b" in kw else _u8(b_q), b_s=_u8(b_s), c=c, c_type=c_type, ldc=ldc,
+        max_rows=max_rows, err_flag=err,
+        workspace=torch.full((ws,), 0xFF, dtype=torch.uint8, device=DEV) if ws else None, **kw)
+    torch.cuda.synchronize()
+    return c
+
+
+def _check(c, ref, mag, K, bf16):
+    """Every routed element within its bound; the others untouched."""
+    c = c[:, :ref.shape[1]].double().cpu().numpy()
+    routed = ~np.isnan(ref)
+    tol = (128 + -(-K // 128) + 4) * 2.0 ** -23 * mag
+    if bf16:
+        tol = tol + 7 * 2.0 ** -13 * mag
+        tol = tol + 2.0 ** -8 * (np.abs(np.nan_to_num(ref)) + tol)
+    bad = routed & ~(np.abs(c - ref) <= tol)
+    assert not bad.any(), (np.argwhere(bad)[:4], c[bad][:4], ref[bad][:4], tol[bad][:4])
+    assert (c[~routed] == -77.0).all()
+
+
+SIZES = {
+    "one_token": [1],
+    "decode": [2, 0, 1, 16, 0, 3],
+    "around_16_32": [15, 17, 31, 33, 0],
+    "around_64_128": [63, 65, 127, 129],
+    "around_256": [255, 257, 300, 0, 1],
+    "empty": [0, 0],
+}
+SHAPES = [(16, 16), (48, 128), (272, 144), (512, 400), (400, 272)]
+HINTS = (16, 32, 64, 128, 0)
+
+
+@pytest.mark.parametrize("hint", HINTS)
+@pytest.mark.parametrize("N,K", SHAPES)
+@pytest.mark.parametrize("name", SIZES)
+def test_product_exact_on_integers(name, N, K, hint):
+    """fp32 outputs; the bf16 kernels below, with integers that bf16 holds."""
+    sizes = SIZES[name]
+    rng = np.random.default_rng(N + K + len(name))
+    starts = _starts(sizes)
+    M_cap = max(128, starts[-1])
+    ops = _operands(rng, sizes, starts, M_cap, N, K, exact=True)
+    ref, _ = _reference(*ops, sizes, starts)
+    c = _product(*ops, sizes, starts, max_rows=hint).double().cpu().numpy()
+    routed = ~np.isnan(ref)
+    np.testing.assert_array_equal(c[routed], ref[routed])
+    assert (c[~routed] == -77.0).all()
+
+
+@pytest.mark.parametrize("hint", HINTS)
+@pytest.mark.parametrize("N,K", SHAPES)
+@pytest.mark.parametrize("name", SIZES)
+def test_product_exact_on_integers_bf16(name, N, K, hint):
+    """Integers whose products lie within 6 bits of one another, so that no
+    alignment drops a bit; the sum is rounded once to bf16."""
+    sizes = SIZES[name]
+    rng = np.random.default_rng(N + K + len(name))
+    starts = _starts(sizes)
+    ops = _operands(rng, sizes, starts, max(128, starts[-1]), N, K, exact=True)
+    ref, _ = _reference(*ops, sizes, starts)
+    c = _product(*ops, sizes, starts, mg.TYPE_BF16, hint).double().cpu().numpy()
+    routed = ~np.isnan(ref)
+    np.testing.assert_array_equal(c[routed], nu.round_bf16(ref[routed]))
+    assert (c[~routed] == -77.0).all()
+
+
+@pytest.mark.parametrize("c_type", [mg.TYPE_F32, mg.TYPE_BF16])
+@pytest.mark.parametrize("hint", HINTS)
+@pytest.mark.parametrize("name", ["decode", "around_16_32", "around_64_128", "around_256"])
+def test_product_random(name, hint, c_type):
+    N, K = 528, 1168
+    sizes = SIZES[name]
+    rng = np.random.default_rng(len(name))
+    starts = _starts(sizes)
+    ops = _operands(rng, sizes, starts, starts[-1], N, K)
+    ref, mag = _reference(*ops, sizes, starts)
+    _check(_product(*ops, sizes, starts, c_type, hint), ref, mag, K, c_type == mg.TYPE_BF16)
+
+
+@pytest.mark.parametrize("hint", HINTS)
+def test_product_packed_groups_wide_output_and_strided_weights(hint):
+    """Groups with no alignment, an output wider than N, weights apart."""
+    N, K, sizes = 144, 272, [5, 0, 37, 130, 1]
+    rng = np.random.default_rng(3)
+    starts = _starts(sizes, 1)
+    M_cap = starts[-1] + 3
+    ops = _operands(rng, sizes, starts, M_cap, N, K)
+    ref, mag = _reference(*ops, sizes, starts)
+    stride = N * K + 16 * 5
+    flat = torch.full((len(sizes) * stride,), 0x7F, dtype=torch.uint8, device=DEV)
+    for e in range(len(sizes)):
+        flat[e * stride:e * stride + N * K] = _u8(ops[2][e]).reshape(-1)
+    c = _product(*ops, sizes, starts, mg.TYPE_BF16, hint, ldc=N + 24, b=flat, b_stride=stride)
+    _check(c, ref, mag, K, True)
+    assert (c[:, N:] == -77.0).all()
+
+
+@pytest.mark.parametrize("hint", HINTS)
+def test_product_many_experts(hint):
+    rng = np.random.default_rng(11)
+    sizes = [int(v) for v in rng.integers(0, 4, 600)]
+    starts = _starts(sizes, 1)
+    ops = _operands(rng, sizes, starts, max(starts[-1], 1), 32, 48, exact=True)
+    ref, _ = _reference(*ops, sizes, starts)
+    c = _product(*ops, sizes, starts, max_rows=hint).double().cpu().numpy()
+    np.testing.assert_array_equal(c[~np.isnan(ref)], ref[~np.isnan(ref)])
+
+
+@pytest.mark.parametrize("hint", HINTS)
+@pytest.mark.parametrize("split,pad,M_cap,cut", [
+    ([200, 50], [0, 128, 256], 384, [128, 50]),     # group 0 runs into group 1
+    ([-5, 50], [0, 128, 256], 256, [0, 50]),        # a negative size
+    ([100, 300], [0, 128, 512], 256, [100, 128]),   # group 1 runs past M_cap
+    ([100, 30], [-128, 128, 256], 256, [0, 30]),    # a negative start
+    ([100, 30], [0, 512, 640], 256, [100, 0]),      # a start past M_cap
+])
+def test_product_bad_offsets_are_cut_and_flagged(split, pad, M_cap, cut, hint):
+    rng = np.random.default_rng(5)
+    at = [max(0, p) for p in pad]
+    ops = _operands(rng, cut, at, M_cap, 48, 144, exact=True)
+    ref, _ = _reference(*ops, cut, at)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    c = _product(*ops, split, pad, max_rows=hint, err=err).double().cpu().numpy()
+    assert err.item() == mg.DEVERR_BAD_OFFSETS
+    np.testing.assert_array_equal(c[~np.isnan(ref)], ref[~np.isnan(ref)])
+    assert (c[np.isnan(ref)] == -77.0).all()
+
+
+@pytest.mark.parametrize("hint", HINTS)
+def test_product_same_bits_again_without_workspace_and_on_another_stream(hint):
+    rng = np.random.default_rng(6)
+    sizes = [300, 0, 77, 511]
+    starts = _starts(sizes)
+    ops = _operands(rng, sizes, starts, starts[-1], 272, 1040)
+    ref, mag = _reference(*ops, sizes, starts)
+    c = _product(*ops, sizes, starts, max_rows=hint)
+    assert torch.equal(c, _product(*ops, sizes, starts, max_rows=hint))
+    _check(_product(*ops, sizes, starts, max_rows=hint, workspace=False), ref, mag, 1040, False)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        d = _product(*ops, sizes, starts, max_rows=hint)
+    torch.cuda.synchronize()
+    assert torch.equal(c, d)
+
+
+# -------------------------------------------------------- weight gradient --
+def _wgrad_operands(rng, sizes, starts, M_cap, P, Q, exact=False):
+    nb = M_cap // 128
+    used = np.zeros(M_cap, bool)
+    span = np.zeros(M_cap, bool)
+    for n, o in zip(sizes, starts):
+        used[o:o + n] = True
+        span[o:o + -(-n // 128) * 128] = True
+    out = []
+    for R in (P, Q):
+        if exact:
+            q = nu.e4m3_encode(rng.integers(-7, 8, (R, M_cap)).astype(np.float64))
+            s = 2.0 ** rng.integers(-2, 3, (nb, R)).astype(np.float32)
+        else:
+            q, s = st.quantize_rows(_bf16(rng, M_cap, R, spread=1.0).T.copy())
+        q[:, ~used] = 0            # pad rows encode zeros ...
+        q[:, ~span] = 0x7F         # ... and what belongs to no group is not read
+        s[~span[::128]] = np.nan
+        out += [q, s.astype(np.float32)]
+    return out
+
+
+def _wgrad(a_q, a_s, b_q, b_s, sizes, starts, c_type=mg.TYPE_F32, c=None, err=None, **kw):
+    E, P, Q, M_cap = len(sizes), a_q.shape[0], b_q.shape[0], a_q.shape[1]
+    dt = torch.float32 if c_type == mg.TYPE_F32 else torch.bfloat16
+    if c is None:
+        c = torch.full((E, P, Q), float("nan"), dtype=dt, device=DEV)
+    mg.moe_grouped_wgrad_fp8(
+        E=E, P=P, Q=Q, M_cap=M_cap, split_sizes=torch.tensor(sizes, dtype=torch.int32, device=DEV),
+        padded_offsets=torch.tensor(starts, dtype=torch.int32, device=DEV), a=_u8(a_q), a_s=_u8(a_s),
+        b=_u8(b_q), b_s=_u8(b_s), c=c, c_type=c_type, err_flag=err, **kw)
+    torch.cuda.synchronize()
+    return c
+
+
+def _wgrad_ref(a_q, a_s, b_q, b_s, sizes, starts):
+    return st.grouped_weight_grad(np.nan_to_num(st.dequantize_rows(a_q, a_s)),
+                                  np.nan_to_num(st.dequantize_rows(b_q, b_s)), sizes, starts)
+
+
+WSIZES = {"one_token": [1], "mixed": [128, 0, 1, 129, 300], "empty": [0, 0], "long": [1500, 7]}
+
+
+@pytest.mark.parametrize("P,Q", [(16, 16), (48, 272), (272, 48), (512, 528)])
+@pytest.mark.parametrize("name", WSIZES)
+def test_wgrad_exact_on_integers_and_accumulation(name, P, Q):
+    sizes = WSIZES[name]
+    starts = _starts(sizes)
+    M_cap = max(256, starts[-1] + 128)
+    rng = np.random.default_rng(P + Q)
+    ops = _wgrad_operands(rng, sizes, starts, M_cap, P, Q, exact=True)
+    ref, _ = _wgrad_ref(*ops, sizes, starts)
+    np.testing.assert_array_equal(_wgrad(*ops, sizes, starts).double().cpu().numpy(), ref)
+    np.testing.assert_array_equal(_wgrad(*ops, sizes, starts, mg.TYPE_BF16).double().cpu().numpy(), nu.round_bf16(ref))
+    c = torch.full((len(sizes), P, Q), 3.0, device=DEV)
+    _wgrad(*ops, sizes, starts, c=c, accumulate=True)
+    np.testing.assert_array_equal(c.double().cpu().numpy(), ref + 3.0)
+
+
+@pytest.mark.parametrize("c_type", [mg.TYPE_F32, mg.TYPE_BF16])
+@pytest.mark.parametrize("name", WSIZES)
+def test_wgrad_random(name, c_type):
+    sizes = WSIZES[name]
+    starts = _starts(sizes)
+    M_cap = max(256, starts[-1] + 128)
+    rng = np.random.default_rng(len(name))
+    ops = _wgrad_operands(rng, sizes, starts, M_cap, 272, 400)
+    ref, mag = _wgrad_ref(*ops, sizes, starts)
+    c = _wgrad(*ops, sizes, starts, c_type).double().cpu().numpy()
+    # one rounding more per addition than the product: two scales
+    tol = 2 * (128 + M_cap // 128 + 4) * 2.0 ** -23 * mag
+    if c_type == mg.TYPE_BF16:
+        tol = tol + 7 * 2.0 ** -13 * mag
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    assert (np.abs(c - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("split,pad,M_cap,cut", [
+    ([200, 50], [0, 128, 256], 384, [128, 50]),
+    ([-5, 50], [0, 128, 256], 256, [0, 50]),
+    ([100, 300], [0, 128, 512], 256, [100, 128]),
+    ([100, 30], [64, 256, 384], 384, [0, 30]),      # a start that is no multiple of 128
+])
+def test_wgrad_bad_offsets_are_cut_and_flagged(split, pad, M_cap, cut):
+    rng = np.random.default_rng(5)
+    ops = _wgrad_operands(rng, cut, pad, M_cap, 48, 144, exact=True)
+    ref, _ = _wgrad_ref(*ops, cut, pad)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    c = _wgrad(*ops, split, pad, err=err).double().cpu().numpy()
+    assert err.item() == mg.DEVERR_BAD_OFFSETS
+    np.testing.assert_array_equal(c, ref)
+
+
+# ----------------------------------------------------------------- a run ---
+def test_quantize_product_and_gradients_together_in_a_graph():
+    """bf16 rows and weights -> quantize -> product, input gradient (the
+    transposed tile copy) and weight gradient (the transposed row copies),
+    captured once and replayed on new inputs, against the same calls made
+    eagerly and the oracle."""
+    E, N, K, sizes = 3, 272, 400, [130, 0, 70]
+    starts = _starts(sizes)
+    M = starts[-1]
+    u8, f32 = dict(dtype=torch.uint8, device=DEV), dict(dtype=torch.float32, device=DEV)
+    x, dy = (torch.empty(M, n, dtype=torch.bfloat16, device=DEV) for n in (K, N))
+    w = torch.empty(E, N, K, dtype=torch.bfloat16, device=DEV)
+    nb = lambda n: -(-n // 128)
+    buf = {}
+    for name, r in (("x", K), ("dy", N)):
+        buf[name] = [torch.empty(M, r, **u8), torch.empty(nb(r), M, **f32),
+                     torch.empty(r, M, **u8), torch.empty(nb(M), r, **f32)]
+    buf["w"] = [torch.empty(E, N, K, **u8), torch.empty(E, nb(N), nb(K), **f32),
+                torch.empty(E, K, N, **u8), torch.empty(E, nb(K), nb(N), **f32)]
+    split = torch.tensor(sizes, dtype=torch.int32, device=DEV)
+    pad = torch.tensor(starts, dtype=torch.int32, device=DEV)
+    y, dx, dw = torch.zeros(M, N, **f32), torch.zeros(M, K, **f32), torch.zeros(E, N, K, **f32)
+    size = dict(E=E, M_cap=M, split_sizes=split, padded_offsets=pad, c_type=mg.TYPE_F32)
+
+    def step():
+        for t, name in ((x, "x"), (dy, "dy")):
+            q, s, qT, sT = buf[name]
+            mg.moe_quantize_fp8(mode=mg.QUANT_BOTH, batch=1, rows=M, cols=t.shape[1], x=t, q=q, s=s, qT=qT, sT=sT)
+        q, s, qT, sT = buf["w"]
+        mg.moe_quantize_fp8(mode=mg.QUANT_TILE, batch=E, rows=N, cols=K, x=w, q=q, s=s, qT=qT, sT=sT)
+        mg.moe_grouped_gemm_fp8(**size, N=N, K=K, a=buf["x"][0], a_s=buf["x"][1], b=q, b_s=s, c=y)
+        mg.moe_grouped_gemm_fp8(**size, N=K, K=N, a=buf["dy"][0], a_s=buf["dy"][1], b=qT, b_s=sT, c=dx)
+        mg.moe_grouped_wgrad_fp8(**size, P=N, Q=K, a=buf["dy"][2], a_s=buf["dy"][3], b=buf["x"][2], b_s=buf["x"][3], c=dw)
+
+    def fill(seed):
+        rng = np.random.default_rng(seed)
+        keep = np.zeros((M, 1))
+        for n, o in zip(sizes, starts):
+            keep[o:o + n] = 1
+        hx, hdy, hw = _bf16(rng, M, K, spread=1.0) * keep, _bf16(rng, M, N, spread=1.0) * keep, 0.1 * _bf16(rng, E, N, K, spread=0.5)
+        hw = nu.round_bf16(hw)
+        x.copy_(_up(hx)); dy.copy_(_up(hdy)); w.copy_(_up(hw))
+        return hx, hdy, hw
+
+    side = torch.cuda.Stream()
+    fill(0)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for seed in (1, 2, 3):
+        hx, hdy, hw = fill(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (y, dx, dw)]
+        step()
+        torch.cuda.synchronize()
+        for g, t in zip(got, (y, dx, dw)):
+            assert torch.equal(g, t)
+        wq = [st.quantize_tiles(m) for m in hw]
+        wd = np.stack([st.dequantize_tiles(*q) for q in wq])
+        ref, mag = st.grouped_product(st.dequantize_rows(*st.quantize_rows(hx)), wd, sizes, starts)
+        ok = ~np.isnan(ref)
+        assert (np.abs(got[0].double().cpu().numpy() - ref)[ok] <= (132 + nb(K)) * 2.0 ** -23 * mag[ok]).all()
+        ref, mag = st.grouped_product(st.dequantize_rows(*st.quantize_rows(hdy)), wd.transpose(0, 2, 1), sizes, starts)
+        ok = ~np.isnan(ref)
+        assert (np.abs(got[1].double().cpu().numpy() - ref)[ok] <= (132 + nb(N)) * 2.0 ** -23 * mag[ok]).all()
+        ref, mag = st.grouped_weight_grad(st.dequantize_rows(*st.quantize_rows(hdy.T.copy())),
+                                          st.dequantize_rows(*st.quantize_rows(hx.T.copy())), sizes, starts)
+        assert (np.abs(got[2].double().cpu().numpy() - ref) <= 2 * (132 + nb(M)) * 2.0 ** -23 * mag).all()
