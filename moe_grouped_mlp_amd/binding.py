@@ -542,36 +542,48 @@ def moe_glu_unfused(*, direction, E, I, M_cap, split_sizes, padded_offsets,
 # ---- block-scaled FP8, router losses, gradient norm -----------------------
 # These check what the C ABI cannot see: that a tensor is contiguous device
 # memory of the type and at least the size the call reads or writes, on the
-# device the call runs on (torch's current one).
+# device the call runs on (torch's current one).  A small call is as long as
+# its marshalling, so the checks are few attribute reads, and what they need
+# of torch is looked up once.
 def _buf(fn, name, t, dtypes, n, dev):
     if t is None:
         return None
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
-        raise ValueError(f"{fn}: {name} must be a tensor of type {' or '.join(map(str, dtypes))}")
-    if not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{fn}: {name} must be contiguous with at least {n} elements")
-    if not t.is_cuda or t.device.index != dev:
-        raise ValueError(f"{fn}: {name} must be on the current device (cuda:{dev})")
-    return t.data_ptr()
-
-
-def _dtypes():
-    import torch
-    global _F32, _BF16, _U8, _I32, _F64, _CODES, _MASK
-    _F32, _BF16, _U8, _I32 = (torch.float32,), (torch.bfloat16,), (torch.uint8,), (torch.int32,)
-    _F64, _CODES, _MASK = (torch.float64,), (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.bool)
+    try:
+        if (t.dtype in dtypes and t.numel() >= n and t.get_device() == dev
+                and t.is_contiguous()):
+            return t.data_ptr()
+    except (AttributeError, TypeError):
+        pass
+    raise ValueError(f"{fn}: {name} must be a contiguous tensor of type "
+                     f"{' or '.join(map(str, dtypes))} with at least {n} elements "
+                     f"on the current device (cuda:{dev})")
 
 
 _F32 = None
 
 
-def _device():
-    """The current device's index, for _buf."""
+def _setup():
     import torch
+    global _F32, _BF16, _U8, _I32, _F64, _CODES, _MASK, _GRADS, _current_device, _raw_stream
+    _BF16, _U8, _I32 = (torch.bfloat16,), (torch.uint8,), (torch.int32,)
+    _F64, _CODES, _MASK = (torch.float64,), (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.bool)
+    _GRADS = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
+    _current_device = torch.cuda.current_device
+    # the current stream's handle without the Stream object around it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+    _F32 = (torch.float32,)
+
+
+def _device():
+    """The current device's index, for _buf and _stream_on."""
     if _F32 is None:
-        _dtypes()
-    return torch.cuda.current_device()
+        _setup()
+    return _current_device()
+
+
+def _stream_on(dev, stream):
+    return _raw_stream(dev) if stream is None else _stream(stream)
 
 
 def _blocks(n):
@@ -593,7 +605,7 @@ def moe_quantize_fp8(*, mode, batch, rows, cols, x, q, s, qT=None, sT=None, pow2
                      _buf(f, "qT", qT, _CODES, n, d), _buf(f, "sT", sT, _F32, nsT, d),
                      int(bool(pow2)), _buf(f, "live", live, _I32, batch, d),
                      _buf(f, "row_end", row_end, _I32, 1, d))
-    _check(f, lib().moe_quantize_fp8(ctypes.byref(a), _stream(stream)))
+    _check(f, lib().moe_quantize_fp8(ctypes.byref(a), _stream_on(d, stream)))
 
 
 def moe_grouped_gemm_fp8_workspace_size(E, N, K, M_cap, max_rows=0) -> int:
@@ -615,7 +627,7 @@ def moe_grouped_gemm_fp8(*, E, N, K, M_cap, split_sizes, padded_offsets, a, a_s,
         _buf(f, "c", c, _F32 if c_type == TYPE_F32 else _BF16, (M_cap - 1) * (ldc or N) + N, d),
         ldc, c_type, max_rows, cu_margin, _buf(f, "err_flag", err_flag, _I32, 1, d),
         _buf(f, "workspace", workspace, _U8, 0, d), _nbytes(workspace))
-    _check(f, lib().moe_grouped_gemm_fp8(ctypes.byref(args), _stream(stream)))
+    _check(f, lib().moe_grouped_gemm_fp8(ctypes.byref(args), _stream_on(d, stream)))
 
 
 def moe_grouped_wgrad_fp8(*, E, P, Q, M_cap, split_sizes, padded_offsets, a, a_s, b, b_s, c,
@@ -630,7 +642,7 @@ def moe_grouped_wgrad_fp8(*, E, P, Q, M_cap, split_sizes, padded_offsets, a, a_s
         _buf(f, "b", b, _CODES, Q * M_cap, d), _buf(f, "b_s", b_s, _F32, Q * _blocks(M_cap), d),
         _buf(f, "c", c, _F32 if c_type == TYPE_F32 else _BF16, E * P * Q, d), c_type,
         int(bool(accumulate)), cu_margin, _buf(f, "err_flag", err_flag, _I32, 1, d))
-    _check(f, lib().moe_grouped_wgrad_fp8(ctypes.byref(args), _stream(stream)))
+    _check(f, lib().moe_grouped_wgrad_fp8(ctypes.byref(args), _stream_on(d, stream)))
 
 
 def moe_router_loss_workspace_size(T, E) -> int:
@@ -648,7 +660,7 @@ def moe_router_loss(*, T, E, k, logits, expert_idx, counts, n_tokens, prob_mean,
         _buf(f, "counts", counts, _I32, E, d), _buf(f, "n_tokens", n_tokens, _I32, 1, d),
         _buf(f, "prob_mean", prob_mean, _F32, E, d), _buf(f, "loss", loss, _F32, 2, d),
         _buf(f, "workspace", workspace, _U8, 0, d), _nbytes(workspace))
-    _check(f, lib().moe_router_loss(ctypes.byref(args), _stream(stream)))
+    _check(f, lib().moe_router_loss(ctypes.byref(args), _stream_on(d, stream)))
 
 
 def moe_router_bwd(*, T, E, k, logits, expert_idx, dlogits, dprobs=None, dloss=None, counts=None,
@@ -663,7 +675,7 @@ def moe_router_bwd(*, T, E, k, logits, expert_idx, dlogits, dprobs=None, dloss=N
         _buf(f, "dprobs", dprobs, _F32, T * k, d), _buf(f, "dloss", dloss, _F32, 2, d),
         balance_coef, z_coef, _buf(f, "counts", counts, _I32, E, d),
         _buf(f, "n_tokens", n_tokens, _I32, 1, d), _buf(f, "dlogits", dlogits, _F32, T * E, d))
-    _check(f, lib().moe_router_bwd(ctypes.byref(args), _stream(stream)))
+    _check(f, lib().moe_router_bwd(ctypes.byref(args), _stream_on(d, stream)))
 
 
 def moe_grad_workspace_size(n_tensors) -> int:
@@ -671,20 +683,26 @@ def moe_grad_workspace_size(n_tensors) -> int:
 
 
 def _tensor_list(fn, tensors, out, dev):
-    import torch
-    outs = [None] * len(tensors) if out is None else list(out)
-    if len(outs) != len(tensors):
+    """The host array of moe_tensor (four 8-byte words each: data, out, numel,
+    type)."""
+    if out is None:
+        out = (None,) * len(tensors)
+    elif len(out) != len(tensors):
         raise ValueError(f"{fn}: out must have as many tensors as the list")
-    arr = (Tensor * len(tensors))()
-    for i, (t, o) in enumerate(zip(tensors, outs)):
-        if t.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError(f"{fn}: tensor {i} is {t.dtype}: bfloat16 or float32 is needed")
-        if o is not None and (o.dtype != t.dtype or o.numel() != t.numel()):
-            raise ValueError(f"{fn}: out {i} must have tensor {i}'s type and size")
-        arr[i] = Tensor(_buf(fn, f"tensor {i}", t, (t.dtype,), 0, dev),
-                        _buf(fn, f"out {i}", o, (t.dtype,), 0, dev), t.numel(),
-                        TYPE_BF16 if t.dtype == torch.bfloat16 else TYPE_F32)
-    return arr
+    words = []
+    for t, o in zip(tensors, out):
+        dt = getattr(t, "dtype", None)
+        if dt not in _GRADS:
+            raise ValueError(f"{fn}: tensor {len(words) // 4} must be a bfloat16 or float32 tensor")
+        n = t.numel()
+        if o is not None and (o.dtype is not dt or o.numel() != n):
+            raise ValueError(f"{fn}: out {len(words) // 4} must have its tensor's type and size")
+        if (t.get_device() != dev or not t.is_contiguous()
+                or o is not None and (o.get_device() != dev or not o.is_contiguous())):
+            raise ValueError(f"{fn}: tensor {len(words) // 4} and its out must be contiguous and "
+                             f"on the current device (cuda:{dev})")
+        words += (t.data_ptr(), 0 if o is None else o.data_ptr(), n, _GRADS[dt])
+    return ctypes.cast((c_int64 * max(1, len(words)))(*words), ctypes.POINTER(Tensor))
 
 
 def moe_grad_sumsq(*, tensors, sumsq, workspace, stream=None):
@@ -693,7 +711,7 @@ def moe_grad_sumsq(*, tensors, sumsq, workspace, stream=None):
     arr = _tensor_list(f, tensors, None, d)
     args = GradArgs(arr, len(tensors), 0.0, _buf(f, "sumsq", sumsq, _F64, 1, d), None, None,
                     _buf(f, "workspace", workspace, _U8, 0, d), _nbytes(workspace))
-    _check(f, lib().moe_grad_sumsq(ctypes.byref(args), _stream(stream)))
+    _check(f, lib().moe_grad_sumsq(ctypes.byref(args), _stream_on(d, stream)))
 
 
 def moe_grad_clip(*, tensors, sumsq, max_norm, out=None, norm=None, err_flag=None, stream=None):
@@ -704,4 +722,4 @@ def moe_grad_clip(*, tensors, sumsq, max_norm, out=None, norm=None, err_flag=Non
     args = GradArgs(arr, len(tensors), max_norm, _buf(f, "sumsq", sumsq, _F64, 1, d),
                     _buf(f, "norm", norm, _F32, 1, d), _buf(f, "err_flag", err_flag, _I32, 1, d),
                     None, 0)
-    _check(f, lib().moe_grad_clip(ctypes.byref(args), _stream(stream)))
+    _check(f, lib().moe_grad_clip(ctypes.byref(args), _stream_on(d, stream)))

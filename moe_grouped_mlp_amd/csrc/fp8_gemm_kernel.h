@@ -38,6 +38,8 @@
 // The weight gradient is the same product with the routed rows as K: both
 // operands transposed copies with one scale per row and block, so its
 // accumulation multiplies by two scales.
+#include <utility>
+
 #include "common.h"
 #include "kernels.h"
 
@@ -109,6 +111,16 @@ MOE_DEV f32x4 fp8_block_mfma(const Fp8Frag<true>& a, const Fp8Frag<true>& b) {
   return d;
 }
 
+// Compile-time loop, so that indices into register arrays are constants.
+template <typename F, int... Is>
+MOE_DEV void fp8_for_impl(F&& f, std::integer_sequence<int, Is...>) {
+  (f(std::integral_constant<int, Is>{}), ...);
+}
+template <int N, typename F>
+MOE_DEV void fp8_for(F&& f) {
+  fp8_for_impl(f, std::make_integer_sequence<int, N>{});
+}
+
 // Chunk swizzles of the LDS images.  An operand read takes one logical
 // 16-byte chunk of 16 rows per LDS cycle (256 bytes): tokens are 16
 // consecutive rows; weights are rows 16 x + y, x < 4, y in a run of 4.
@@ -132,10 +144,13 @@ MOE_DEV int fp8_group_rows(const Fp8Args& g, int e, bool aligned, bool& bad) {
 // R / 8 one-kilobyte loads (8 rows each).
 template <int R, bool W>
 struct Fp8Loader {
-  static constexpr int kInstr = R / 8 / kFp8Waves;
+  static constexpr int kInstr = R / 8 / kFp8Waves;   // 1, 2 or 4
   __amdgpu_buffer_rsrc_t rsrc;
   int voff[kInstr];
-  int kbyte[kInstr];
+  // K bytes of the lane's chunk: the swizzle depends on load j through j % 2
+  // (tokens) or j / 2 (weights)
+  int kbyte[2];
+  MOE_DEV static constexpr int which(int j) { return W ? j / 2 : j % 2; }
 
   // base: the tile's first row at the group's first K value; ld: bytes
   // between rows; rows: rows that exist; k: K values that exist
@@ -145,9 +160,9 @@ struct Fp8Loader {
 #pragma unroll
     for (int j = 0; j < kInstr; ++j) {
       const int row = (wave * kInstr + j) * 8 + (lane >> 3);
-      const int c = (lane & 7) ^ (W ? fp8_swz_w(row) : fp8_swz_t(row));
-      kbyte[j] = 16 * c;
-      voff[j] = row < rows ? static_cast<int>(row * ld) + 16 * c : kFp8OutOfRange;
+      const int c = 16 * ((lane & 7) ^ (W ? fp8_swz_w(row) : fp8_swz_t(row)));
+      kbyte[which(j)] = c;
+      voff[j] = row < rows ? static_cast<int>(row * ld) + c : kFp8OutOfRange;
     }
   }
   // Stage kt; chunks at or past K value k read as zeros.
@@ -155,8 +170,8 @@ struct Fp8Loader {
     const int left = k - kt * kFp8Blk;
 #pragma unroll
     for (int j = 0; j < kInstr; ++j)
-      fp8_dma16(rsrc, stage + (wave_s * kInstr + j) * 1024, kbyte[j] < left ? voff[j] : kFp8OutOfRange,
-                left > 0 ? kt * kFp8Blk : 0);
+      fp8_dma16(rsrc, stage + (wave_s * kInstr + j) * 1024,
+                kbyte[which(j)] < left ? voff[j] : kFp8OutOfRange, left > 0 ? kt * kFp8Blk : 0);
   }
 };
 
@@ -227,7 +242,8 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
   const int l16 = lane & 15, g4 = lane >> 4;
   const int t_row = 16 * J * wt + l16;
   const int w_row = 128 * wn + 16 * (l16 >> 2) + (l16 & 3);
-  const int t_sw = fp8_swz_t(t_row);   // unchanged by + 16 j
+  // unchanged by + 16 j, and by + 64 v + 4 i
+  const int t_sw = fp8_swz_t(t_row), w_sw = fp8_swz_w(w_row);
 
   for (int id = vid; id < total; id += G) {
     int lo = 0, hi = g.E - 1;   // the expert of the tile
@@ -291,67 +307,96 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
 #pragma unroll
       for (int j = 0; j < J; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto step = [&](const uint8_t* sT, const uint8_t* sW, const float* sS) {
-      float f[J];
-      Fp8Frag<F32> t[J];
-      const float ws = WG ? 1.0f : sS[256 + wn];
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        f[j] = sS[t_row + 16 * j] * ws;
-        const uint8_t* r = sT + (t_row + 16 * j) * kFp8Blk;
-        const i32x4 x = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4) ^ t_sw));
-        const i32x4 y = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4 + 1) ^ t_sw));
-        t[j].set(x, y);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = w_row + 64 * (i >> 2) + 4 * (i & 3);
-        const uint8_t* r = sW + row * kFp8Blk;
-        const int sw = fp8_swz_w(row);
-        const i32x4 x = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4) ^ sw));
-        const i32x4 y = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4 + 1) ^ sw));
-        Fp8Frag<F32> w;
-        w.set(x, y);
-        f32x4 wf;
-        if constexpr (WG)
-          wf = *reinterpret_cast<const f32x4*>(sS + 256 + 128 * wn + 64 * (i >> 2) + 16 * g4 + 4 * (i & 3));
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const f32x4 p = fp8_block_mfma(w, t[j]);
-#pragma unroll
-          for (int r4 = 0; r4 < 4; ++r4) {
-            const float s = WG ? f[j] * wf[r4] : f[j];
-            acc[i][j][r4] = __builtin_fmaf(p[r4], s, acc[i][j][r4]);
-          }
-        }
-      }
+    // Registers of the pipeline: the weight tile in use and the next one, the
+    // step's tokens, and their scales for this step and the next.
+    struct Raw {
+      i32x4 x, y;
     };
-    // waits for this wave's LDS reads first, whose results the compiler may
-    // use only behind the barrier
-    auto barrier = [&]() {
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
+    Raw wr[2], tr[J];
+    float fr[2][J];
+    f32x4 wf[2];
+    auto read_w = [&](auto i, const uint8_t* sW, const float* sS) {
+      const uint8_t* r = sW + w_row * kFp8Blk + (64 * (i / 4) + 4 * (i % 4)) * kFp8Blk;
+      wr[i & 1].x = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4) ^ w_sw));
+      wr[i & 1].y = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4 + 1) ^ w_sw));
+      if constexpr (WG)
+        wf[i & 1] = *reinterpret_cast<const f32x4*>(sS + 256 + 128 * wn + 64 * (i / 4) + 16 * g4 +
+                                                    4 * (i % 4));
+    };
+    auto read_t = [&](auto par, auto j, const uint8_t* sT, const float* sS) {
+      const uint8_t* r = sT + (t_row + 16 * j) * kFp8Blk;
+      tr[j].x = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4) ^ t_sw));
+      tr[j].y = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4 + 1) ^ t_sw));
+      fr[par][j] = sS[t_row + 16 * j];
+      if constexpr (!WG) fr[par][j] *= sS[256 + wn];
+    };
+    // One step on the stage in (sT, sW, sS), par: which registers hold its
+    // token scales.  Weight tile i + 1 is read while tile i's MFMAs run, and an
+    // MFMA's sums are added two MFMAs later.  Before the last weight tile
+    // every wave has read all of the stage and the next one has landed (one
+    // barrier), so its loads go out there, and the next step's tokens are read
+    // into the registers that the last MFMAs leave.
+    auto step = [&](auto par, uint8_t* sT, uint8_t* sW, float* sS, const uint8_t* nT,
+                    const uint8_t* nW, const float* nS, int kt) {
+      constexpr int P = decltype(par)::value;
+      Fp8Frag<F32> t[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) t[j].set(tr[j].x, tr[j].y);
+      constexpr int kLag = 2, kRing = 4;
+      f32x4 p[kRing];
+      f32x4 wfm[2];
+      auto add = [&](auto m) {   // the sums of MFMA m
+        constexpr int i = m / J, j = m % J;
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const float s = WG ? fr[P][j] * wfm[i & 1][r4] : fr[P][j];
+          acc[i][j][r4] = __builtin_fmaf(p[m % kRing][r4], s, acc[i][j][r4]);
+        }
+      };
+      fp8_for<8>([&](auto i) {
+        if constexpr (i < 7) {
+          read_w(std::integral_constant<int, i + 1>{}, sW, sS);
+        } else {
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) and lgkmcnt(0)
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          read_w(std::integral_constant<int, 0>{}, nW, nS);
+          issue(sT, sW, sS, kt + 2);
+        }
+        Fp8Frag<F32> w;
+        w.set(wr[i & 1].x, wr[i & 1].y);
+        if constexpr (WG) wfm[i & 1] = wf[i & 1];
+        fp8_for<J>([&](auto j) {
+          constexpr int m = i * J + j;
+          p[m % kRing] = fp8_block_mfma(w, t[j]);
+          if constexpr (m >= kLag) add(std::integral_constant<int, m - kLag>{});
+          if constexpr (i == 7) read_t(std::integral_constant<int, 1 - P>{}, j, nT, nS);
+        });
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      fp8_for<kLag>([&](auto l) { add(std::integral_constant<int, 8 * J - kLag + l>{}); });
     };
 
     if (steps > 0) {
       issue(sT0, sW0, sS0, 0);
       issue(sT1, sW1, sS1, 1);
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kLoads));   // stage 0 landed
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      fp8_for<J>([&](auto j) { read_t(std::integral_constant<int, 0>{}, j, sT0, sS0); });
+      read_w(std::integral_constant<int, 0>{}, sW0, sS0);
       for (int kt = 0; kt < steps; kt += 2) {
-        __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kLoads));   // stage kt landed
-        barrier();
-        step(sT0, sW0, sS0);
-        barrier();   // every wave has read the stage
-        issue(sT0, sW0, sS0, kt + 2);
-        __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kLoads));
-        barrier();
-        if (kt + 1 < steps) step(sT1, sW1, sS1);
-        barrier();
-        issue(sT1, sW1, sS1, kt + 3);
+        step(std::integral_constant<int, 0>{}, sT0, sW0, sS0, sT1, sW1, sS1, kt);
+        if (kt + 1 == steps) break;
+        step(std::integral_constant<int, 1>{}, sT1, sW1, sS1, sT0, sW0, sS0, kt + 1);
       }
-      __builtin_amdgcn_s_waitcnt(fp8_wait_vm(0));   // the zero fills past the end
-      barrier();
+      // the zero fills past the end, and reads of the stage behind the last
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0070);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
     }
 
     // ---- store: 16 consecutive outputs of a token per four weight tiles ----

@@ -223,7 +223,7 @@ def test_binding_refuses_other_tensors():
     idx = torch.zeros(4, 2, dtype=torch.int32)
     both = dict(T=4, E=8, k=2, expert_idx=idx)
     import unittest.mock as mock
-    with mock.patch.object(B, "_device", lambda: (B._dtypes(), 0)[1]):
+    with mock.patch.object(B, "_device", lambda: (B._setup(), 0)[1]):
         for logits in (f32.double(), torch.zeros(4, 7), torch.zeros(8, 4).t(), f32, "x"):   # the last tensor: not on a device
             with pytest.raises(ValueError):
                 m.moe_router_bwd(**both, logits=logits, dlogits=f32)
