@@ -121,9 +121,13 @@ MOE_DEV void fp8_for(F&& f) {
   fp8_for_impl(f, std::make_integer_sequence<int, N>{});
 }
 
-// Chunk swizzles of the LDS images.  An operand read takes one logical
-// 16-byte chunk of 16 rows per LDS cycle (256 bytes): tokens are 16
-// consecutive rows; weights are rows 16 x + y, x < 4, y in a run of 4.
+// Chunk swizzles of the LDS images.  A lane's operand is chunks g and g + 4 of
+// its row (g = lane / 16; which K values these are does not matter as long as
+// both operands agree).  A 16-byte read serves lanes of two neighbouring g in
+// one LDS cycle (lanes 0 .. 3 go with 20 .. 23); with chunk c of the m-th row
+// of 16 at c ^ (m / 2) they fall on different banks (chunks 2 g and 2 g + 1
+// instead cost 3.5 conflict cycles a read).  Tokens are 16 consecutive rows; weights are rows 16 x + y, x < 4,
+// y in a run of 4.
 MOE_DEV int fp8_swz_t(int row) { return (row >> 1) & 7; }
 MOE_DEV int fp8_swz_w(int row) { return ((row >> 1) & 1) | ((row >> 3) & 6); }
 
@@ -317,16 +321,16 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
     f32x4 wf[2];
     auto read_w = [&](auto i, const uint8_t* sW, const float* sS) {
       const uint8_t* r = sW + w_row * kFp8Blk + (64 * (i / 4) + 4 * (i % 4)) * kFp8Blk;
-      wr[i & 1].x = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4) ^ w_sw));
-      wr[i & 1].y = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4 + 1) ^ w_sw));
+      wr[i & 1].x = *reinterpret_cast<const i32x4*>(r + 16 * (g4 ^ w_sw));
+      wr[i & 1].y = *reinterpret_cast<const i32x4*>(r + 16 * ((g4 + 4) ^ w_sw));
       if constexpr (WG)
         wf[i & 1] = *reinterpret_cast<const f32x4*>(sS + 256 + 128 * wn + 64 * (i / 4) + 16 * g4 +
                                                     4 * (i % 4));
     };
     auto read_t = [&](auto par, auto j, const uint8_t* sT, const float* sS) {
       const uint8_t* r = sT + (t_row + 16 * j) * kFp8Blk;
-      tr[j].x = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4) ^ t_sw));
-      tr[j].y = *reinterpret_cast<const i32x4*>(r + 16 * ((2 * g4 + 1) ^ t_sw));
+      tr[j].x = *reinterpret_cast<const i32x4*>(r + 16 * (g4 ^ t_sw));
+      tr[j].y = *reinterpret_cast<const i32x4*>(r + 16 * ((g4 + 4) ^ t_sw));
       fr[par][j] = sS[t_row + 16 * j];
       if constexpr (!WG) fr[par][j] *= sS[256 + wn];
     };
