@@ -38,6 +38,7 @@
 // The weight gradient is the same product with the routed rows as K: both
 // operands transposed copies with one scale per row and block, so its
 // accumulation multiplies by two scales.
+#include <type_traits>
 #include <utility>
 
 #include "common.h"
@@ -149,12 +150,22 @@ MOE_DEV int fp8_group_rows(const Fp8Args& g, int e, bool aligned, bool& bad) {
 template <int R, bool W>
 struct Fp8Loader {
   static constexpr int kInstr = R / 8 / kFp8Waves;   // 1, 2 or 4
+  // First row of load j in its LDS array, the wave's loads side by side, and
+  // in the tile.  Of the weights, loads 0 and 1 fill the array of tiles 0 .. 3
+  // (tile rows 0 .. 63 and 128 .. 191), loads 2 and 3 that of tiles 4 .. 7.
+  MOE_DEV static constexpr int lds_row(int wave, int j) {
+    return W ? (2 * wave + j % 2) * 8 : (wave * kInstr + j) * 8;
+  }
+  MOE_DEV static constexpr int tile_row(int wave, int j) {
+    const int r = lds_row(wave, j);
+    return W ? r % 64 + r / 64 * 128 + j / 2 * 64 : r;
+  }
   __amdgpu_buffer_rsrc_t rsrc;
   int voff[kInstr];
   // K bytes of the lane's chunk: the swizzle depends on load j through j % 2
-  // (tokens) or j / 2 (weights)
+  // (tokens), or not at all (weights)
   int kbyte[2];
-  MOE_DEV static constexpr int which(int j) { return W ? j / 2 : j % 2; }
+  MOE_DEV static constexpr int which(int j) { return W ? 0 : j % 2; }
 
   // base: the tile's first row at the group's first K value; ld: bytes
   // between rows; rows: rows that exist; k: K values that exist
@@ -163,18 +174,19 @@ struct Fp8Loader {
     rsrc = fp8_rsrc(base, static_cast<uint32_t>(bytes));
 #pragma unroll
     for (int j = 0; j < kInstr; ++j) {
-      const int row = (wave * kInstr + j) * 8 + (lane >> 3);
+      const int row = tile_row(wave, j) + (lane >> 3);
       const int c = 16 * ((lane & 7) ^ (W ? fp8_swz_w(row) : fp8_swz_t(row)));
       kbyte[which(j)] = c;
       voff[j] = row < rows ? static_cast<int>(row * ld) + c : kFp8OutOfRange;
     }
   }
-  // Stage kt; chunks at or past K value k read as zeros.
+  // Loads j0 .. j1 - 1 of stage kt; chunks at or past K value k read as zeros.
+  template <int j0 = 0, int j1 = kInstr>
   MOE_DEV void issue(uint8_t* stage, int kt, int wave_s, int k) {
     const int left = k - kt * kFp8Blk;
 #pragma unroll
-    for (int j = 0; j < kInstr; ++j)
-      fp8_dma16(rsrc, stage + (wave_s * kInstr + j) * 1024,
+    for (int j = j0; j < j1; ++j)
+      fp8_dma16(rsrc, stage + lds_row(wave_s, j) * kFp8Blk,
                 kbyte[which(j)] < left ? voff[j] : kFp8OutOfRange, left > 0 ? kt * kFp8Blk : 0);
   }
 };
@@ -186,10 +198,18 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
     const Fp8Args g) {
   constexpr int BT = 64 * J;   // tokens of a tile
   __shared__ __attribute__((aligned(1024))) uint8_t sT0[BT * kFp8Blk], sT1[BT * kFp8Blk];
-  __shared__ __attribute__((aligned(1024))) uint8_t sW0[kFp8BN * kFp8Blk], sW1[kFp8BN * kFp8Blk];
-  // scales of a stage: tokens at 0, weights at 256 (WG: one per row, else the
-  // tile's two 128-row blocks)
-  __shared__ __attribute__((aligned(16))) float sS0[512], sS1[512];
+  // weights: the rows of tiles 0 .. 3 (a) and 4 .. 7 (b) of both wave columns;
+  // behind the latter the stage's scales: tokens at 0, weights at 256 (WG:
+  // one per row, else the tile's two 128-row blocks).  The compiler waits for
+  // every load in flight into an array before it reads from it, and tells
+  // six arrays apart but not eight: hence what shares one.
+  constexpr int kHalfW = kFp8BN * kFp8Blk / 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t sWa0[kHalfW], sWa1[kHalfW];
+  __shared__ __attribute__((aligned(1024))) uint8_t sWb0[kHalfW + 2048], sWb1[kHalfW + 2048];
+  auto scales = [](auto* sWb) {
+    using F = std::conditional_t<std::is_const_v<std::remove_pointer_t<decltype(sWb)>>, const float, float>;
+    return reinterpret_cast<F*>(sWb + kHalfW);
+  };
   __shared__ int s_start[kMaxExperts + 1], s_rows[kMaxExperts], s_tmp[kFp8Waves];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -245,8 +265,8 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
   // operand reads: byte offsets of the lane's row and its two chunks
   const int l16 = lane & 15, g4 = lane >> 4;
   const int t_row = 16 * J * wt + l16;
-  const int w_row = 128 * wn + 16 * (l16 >> 2) + (l16 & 3);
-  // unchanged by + 16 j, and by + 64 v + 4 i
+  const int w_row = 64 * wn + 16 * (l16 >> 2) + (l16 & 3);
+  // unchanged by + 16 j, and by + 4 i
   const int t_sw = fp8_swz_t(t_row), w_sw = fp8_swz_w(w_row);
 
   for (int id = vid; id < total; id += G) {
@@ -296,14 +316,20 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
       s_step = 1;
       if (s_i < 2 && s_i * kFp8Blk < rows_b) s_voff = 4 * s_i * steps;
     }
-    auto issue = [&](uint8_t* sT, uint8_t* sW, float* sS, int kt) {
+    // A stage's loads: the tokens and the weights of tiles 0 .. 3, whose room
+    // is free half a step before the rest's, then the other weights and the
+    // scales.
+    auto issue_early = [&](uint8_t* sT, uint8_t* sWa, int kt) {
       const int k_left = kt < steps ? K : 0;   // past the end: zeros
       lt.issue(sT, kt, wave_s, k_left);
-      lw.issue(sW, kt, wave_s, k_left);
-      fp8_dma4(fp8_rsrc(s_base + (kt < steps ? kt : 0) * s_step, 0x7ffffffeu), sS + wave_s * 64,
+      lw.template issue<0, 2>(sWa, kt, wave_s, k_left);
+    };
+    auto issue_late = [&](uint8_t* sWb, int kt) {
+      lw.template issue<2, 4>(sWb, kt, wave_s, kt < steps ? K : 0);
+      fp8_dma4(fp8_rsrc(s_base + (kt < steps ? kt : 0) * s_step, 0x7ffffffeu), scales(sWb) + wave_s * 64,
                kt < steps ? s_voff : kFp8OutOfRange, 0);
     };
-    constexpr int kLoads = Fp8Loader<BT, false>::kInstr + Fp8Loader<kFp8BN, true>::kInstr + 1;
+    constexpr int kEarly = Fp8Loader<BT, false>::kInstr + 2, kLate = 3;
 
     f32x4 acc[8][J];
 #pragma unroll
@@ -319,8 +345,8 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
     Raw wr[2], tr[J];
     float fr[2][J];
     f32x4 wf[2];
-    auto read_w = [&](auto i, const uint8_t* sW, const float* sS) {
-      const uint8_t* r = sW + w_row * kFp8Blk + (64 * (i / 4) + 4 * (i % 4)) * kFp8Blk;
+    auto read_w = [&](auto i, const uint8_t* sW, const float* sS) {   // sW: the half with tile i
+      const uint8_t* r = sW + (w_row + 4 * (i % 4)) * kFp8Blk;
       wr[i & 1].x = *reinterpret_cast<const i32x4*>(r + 16 * (g4 ^ w_sw));
       wr[i & 1].y = *reinterpret_cast<const i32x4*>(r + 16 * ((g4 + 4) ^ w_sw));
       if constexpr (WG)
@@ -334,14 +360,17 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
       fr[par][j] = sS[t_row + 16 * j];
       if constexpr (!WG) fr[par][j] *= sS[256 + wn];
     };
-    // One step on the stage in (sT, sW, sS), par: which registers hold its
+    // One step on the stage in (sT, sWa, sWb), par: which registers hold its
     // token scales.  Weight tile i + 1 is read while tile i's MFMAs run, and an
-    // MFMA's sums are added two MFMAs later.  Before the last weight tile
-    // every wave has read all of the stage and the next one has landed (one
-    // barrier), so its loads go out there, and the next step's tokens are read
-    // into the registers that the last MFMAs leave.
-    auto step = [&](auto par, uint8_t* sT, uint8_t* sW, float* sS, const uint8_t* nT,
-                    const uint8_t* nW, const float* nS, int kt) {
+    // MFMA's sums are added two MFMAs later.  Half way every wave is done with
+    // the stage's tokens and the first half of its weights (a barrier), so the
+    // loads of stage kt + 2 into that room go out; before the last weight tile
+    // all of the stage is read and the next one has landed (the other
+    // barrier), so the rest goes out, and the next step's tokens are read into
+    // the registers that the last MFMAs leave.
+    auto step = [&](auto par, uint8_t* sT, uint8_t* sWa, uint8_t* sWb,
+                    const uint8_t* nT, const uint8_t* nWa, const uint8_t* nWb, int kt) {
+      const float *sS = scales(sWb), *nS = scales(nWb);
       constexpr int P = decltype(par)::value;
       Fp8Frag<F32> t[J];
 #pragma unroll
@@ -358,15 +387,22 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
         }
       };
       fp8_for<8>([&](auto i) {
-        if constexpr (i < 7) {
-          read_w(std::integral_constant<int, i + 1>{}, sW, sS);
-        } else {
+        if constexpr (i == 4) {
           asm volatile("" ::: "memory");
-          __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) and lgkmcnt(0)
+          __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
           __builtin_amdgcn_s_barrier();
           asm volatile("" ::: "memory");
-          read_w(std::integral_constant<int, 0>{}, nW, nS);
-          issue(sT, sW, sS, kt + 2);
+          issue_early(sT, sWa, kt + 2);
+        }
+        if constexpr (i < 7) {
+          read_w(std::integral_constant<int, i + 1>{}, i < 3 ? sWa : sWb, sS);
+        } else {
+          asm volatile("" ::: "memory");
+          __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kEarly) & 0xC07F);   // and lgkmcnt(0)
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          read_w(std::integral_constant<int, 0>{}, nWa, nS);
+          issue_late(sWb, kt + 2);
         }
         Fp8Frag<F32> w;
         w.set(wr[i & 1].x, wr[i & 1].y);
@@ -383,19 +419,24 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
     };
 
     if (steps > 0) {
-      issue(sT0, sW0, sS0, 0);
-      issue(sT1, sW1, sS1, 1);
+      issue_early(sT0, sWa0, 0);
+      issue_late(sWb0, 0);
+      issue_early(sT1, sWa1, 1);
+      issue_late(sWb1, 1);
       asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kLoads));   // stage 0 landed
+      __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kEarly + kLate));   // stage 0 landed
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      fp8_for<J>([&](auto j) { read_t(std::integral_constant<int, 0>{}, j, sT0, sS0); });
-      read_w(std::integral_constant<int, 0>{}, sW0, sS0);
-      for (int kt = 0; kt < steps; kt += 2) {
-        step(std::integral_constant<int, 0>{}, sT0, sW0, sS0, sT1, sW1, sS1, kt);
-        if (kt + 1 == steps) break;
-        step(std::integral_constant<int, 1>{}, sT1, sW1, sS1, sT0, sW0, sS0, kt + 1);
+      fp8_for<J>([&](auto j) { read_t(std::integral_constant<int, 0>{}, j, sT0, scales(sWb0)); });
+      read_w(std::integral_constant<int, 0>{}, sWa0, scales(sWb0));
+      // (a loop with its exit in the middle would make the compiler wait for
+      // loads that only that way out leaves in flight)
+      int kt = 0;
+      for (; kt + 1 < steps; kt += 2) {
+        step(std::integral_constant<int, 0>{}, sT0, sWa0, sWb0, sT1, sWa1, sWb1, kt);
+        step(std::integral_constant<int, 1>{}, sT1, sWa1, sWb1, sT0, sWa0, sWb0, kt + 1);
       }
+      if (kt < steps) step(std::integral_constant<int, 0>{}, sT0, sWa0, sWb0, sT1, sWa1, sWb1, kt);
       // the zero fills past the end, and reads of the stage behind the last
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_waitcnt(0x0070);
