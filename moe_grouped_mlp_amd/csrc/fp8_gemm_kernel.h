@@ -362,7 +362,8 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
     };
     // One step on the stage in (sT, sWa, sWb), par: which registers hold its
     // token scales.  Weight tile i + 1 is read while tile i's MFMAs run, and an
-    // MFMA's sums are added two MFMAs later.  Half way every wave is done with
+    // MFMA's sums are added three MFMAs later, when they are there (held in that
+    // order, else the compiler adds them at once, behind wait states).  Half way every wave is done with
     // the stage's tokens and the first half of its weights (a barrier), so the
     // loads of stage kt + 2 into that room go out; before the last weight tile
     // all of the stage is read and the next one has landed (the other
@@ -375,14 +376,15 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
       Fp8Frag<F32> t[J];
 #pragma unroll
       for (int j = 0; j < J; ++j) t[j].set(tr[j].x, tr[j].y);
-      constexpr int kLag = 2, kRing = 4;
+      constexpr int kLag = 3, kRing = 4;
       f32x4 p[kRing];
-      f32x4 wfm[2];
+      constexpr int kW = J >= kLag ? 2 : 4;   // weight tiles whose sums are outstanding
+      f32x4 wfm[kW];
       auto add = [&](auto m) {   // the sums of MFMA m
         constexpr int i = m / J, j = m % J;
 #pragma unroll
         for (int r4 = 0; r4 < 4; ++r4) {
-          const float s = WG ? fr[P][j] * wfm[i & 1][r4] : fr[P][j];
+          const float s = WG ? fr[P][j] * wfm[i % kW][r4] : fr[P][j];
           acc[i][j][r4] = __builtin_fmaf(p[m % kRing][r4], s, acc[i][j][r4]);
         }
       };
@@ -406,14 +408,14 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
         }
         Fp8Frag<F32> w;
         w.set(wr[i & 1].x, wr[i & 1].y);
-        if constexpr (WG) wfm[i & 1] = wf[i & 1];
+        if constexpr (WG) wfm[i % kW] = wf[i & 1];
         fp8_for<J>([&](auto j) {
           constexpr int m = i * J + j;
           p[m % kRing] = fp8_block_mfma(w, t[j]);
           if constexpr (m >= kLag) add(std::integral_constant<int, m - kLag>{});
           if constexpr (i == 7) read_t(std::integral_constant<int, 1 - P>{}, j, nT, nS);
+          __builtin_amdgcn_sched_barrier(0);
         });
-        __builtin_amdgcn_sched_barrier(0);
       });
       fp8_for<kLag>([&](auto l) { add(std::integral_constant<int, 8 * J - kLag + l>{}); });
     };
