@@ -21,9 +21,10 @@
 //     each; their scales ride along.  16-byte chunk c of a row is stored at
 //     c ^ swizzle(row), which spreads the 16 rows of an operand read over all
 //     banks.
-//   * MFMA row m of weight tile i is weight row 64 (i / 4) + 16 (m / 4) +
-//     4 (i % 4) + m % 4: a lane then holds 16 consecutive outputs of its
-//     token per four tiles and stores them as whole 16-byte words.
+//   * MFMA row m of weight tile i is weight row 32 (i / 2) + 8 (m / 4) +
+//     4 (i % 2) + m % 4 (bf16 output) or 16 i + m (fp32), so that a lane's
+//     outputs of two tiles, or of one, are 16 consecutive bytes of its token
+//     and a store covers 64 consecutive bytes of 16 rows.
 //   * Persistent workgroups walk the tiles of all experts, whose sizes are
 //     read from device memory.
 // Precision: the FP8 MFMAs add eight neighbouring products aligned to the
@@ -127,10 +128,14 @@ MOE_DEV void fp8_for(F&& f) {
 // both operands agree).  A 16-byte read serves lanes of two neighbouring g in
 // one LDS cycle (lanes 0 .. 3 go with 20 .. 23); with chunk c of the m-th row
 // of 16 at c ^ (m / 2) they fall on different banks (chunks 2 g and 2 g + 1
-// instead cost 3.5 conflict cycles a read).  Tokens are 16 consecutive rows; weights are rows 16 x + y, x < 4,
+// instead cost 3.5 conflict cycles a read).  Tokens, and weights for an fp32
+// output, are 16 consecutive rows; for a bf16 one they are rows 8 x + y, x < 4,
 // y in a run of 4.
 MOE_DEV int fp8_swz_t(int row) { return (row >> 1) & 7; }
-MOE_DEV int fp8_swz_w(int row) { return ((row >> 1) & 1) | ((row >> 3) & 6); }
+template <bool F32>
+MOE_DEV int fp8_swz_w(int row) {
+  return F32 ? (row >> 1) & 7 : ((row >> 1) & 1) | ((row >> 2) & 6);
+}
 
 // A group's rows as the kernels see them: cut to what lies between its start,
 // the next start and the buffer's end.
@@ -147,7 +152,7 @@ MOE_DEV int fp8_group_rows(const Fp8Args& g, int e, bool aligned, bool& bad) {
 
 // One operand tile of R rows x 128 bytes per stage: this wave's share of the
 // R / 8 one-kilobyte loads (8 rows each).
-template <int R, bool W>
+template <int R, bool W, bool F32>
 struct Fp8Loader {
   static constexpr int kInstr = R / 8 / kFp8Waves;   // 1, 2 or 4
   // First row of load j in its LDS array, the wave's loads side by side, and
@@ -163,9 +168,8 @@ struct Fp8Loader {
   __amdgpu_buffer_rsrc_t rsrc;
   int voff[kInstr];
   // K bytes of the lane's chunk: the swizzle depends on load j through j % 2
-  // (tokens), or not at all (weights)
   int kbyte[2];
-  MOE_DEV static constexpr int which(int j) { return W ? 0 : j % 2; }
+  MOE_DEV static constexpr int which(int j) { return j % 2; }
 
   // base: the tile's first row at the group's first K value; ld: bytes
   // between rows; rows: rows that exist; k: K values that exist
@@ -175,7 +179,7 @@ struct Fp8Loader {
 #pragma unroll
     for (int j = 0; j < kInstr; ++j) {
       const int row = tile_row(wave, j) + (lane >> 3);
-      const int c = 16 * ((lane & 7) ^ (W ? fp8_swz_w(row) : fp8_swz_t(row)));
+      const int c = 16 * ((lane & 7) ^ (W ? fp8_swz_w<F32>(row) : fp8_swz_t(row)));
       kbyte[which(j)] = c;
       voff[j] = row < rows ? static_cast<int>(row * ld) + c : kFp8OutOfRange;
     }
@@ -265,9 +269,10 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
   // operand reads: byte offsets of the lane's row and its two chunks
   const int l16 = lane & 15, g4 = lane >> 4;
   const int t_row = 16 * J * wt + l16;
-  const int w_row = 64 * wn + 16 * (l16 >> 2) + (l16 & 3);
-  // unchanged by + 16 j, and by + 4 i
-  const int t_sw = fp8_swz_t(t_row), w_sw = fp8_swz_w(w_row);
+  const int w_row = 64 * wn + (F32 ? l16 : 8 * (l16 >> 2) + (l16 & 3));
+  auto w_off = [](int i) { return F32 ? 16 * (i % 4) : 32 * (i % 4 / 2) + 4 * (i % 2); };
+  // unchanged by + 16 j and + w_off(i)
+  const int t_sw = fp8_swz_t(t_row), w_sw = fp8_swz_w<F32>(w_row);
 
   for (int id = vid; id < total; id += G) {
     int lo = 0, hi = g.E - 1;   // the expert of the tile
@@ -284,13 +289,14 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
     const int tiles_t = (rows_t + BT - 1) / BT;
     const int band = in_e / (g.group_m * tiles_n), in_b = in_e - band * g.group_m * tiles_n;
     const int gm = tiles_t - band * g.group_m < g.group_m ? tiles_t - band * g.group_m : g.group_m;
-    const int t0 = (band * g.group_m + in_b % gm) * BT, n0 = in_b / gm * kFp8BN;
+    const int m_b = in_b % gm, t_n = in_b / gm;
+    const int t0 = (band * g.group_m + m_b) * BT, n0 = t_n * kFp8BN;
 
     const int K = WG ? (n_e + kFp8Blk - 1) / kFp8Blk * kFp8Blk : g.K;
     const int steps = (K + kFp8Blk - 1) / kFp8Blk;
     const int rows_a = rows_t - t0, rows_b = g.N - n0;
-    Fp8Loader<BT, false> lt;
-    Fp8Loader<kFp8BN, true> lw;
+    Fp8Loader<BT, false, F32> lt;
+    Fp8Loader<kFp8BN, true, F32> lw;
     const uint8_t* b_e = static_cast<const uint8_t*>(g.b) + (WG ? start : e * g.b_stride);
     lt.init(g.a + (WG ? static_cast<int64_t>(t0) * g.M_cap + start
                       : static_cast<int64_t>(start + t0) * g.K),
@@ -316,20 +322,24 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
       s_step = 1;
       if (s_i < 2 && s_i * kFp8Blk < rows_b) s_voff = 4 * s_i * steps;
     }
-    // A stage's loads: the tokens and the weights of tiles 0 .. 3, whose room
-    // is free half a step before the rest's, then the other weights and the
-    // scales.
-    auto issue_early = [&](uint8_t* sT, uint8_t* sWa, int kt) {
+    // A stage's loads in the order they go out: the tokens and the weights of
+    // tiles 0 .. 3 (early: their room is free half a step before the rest's),
+    // the other weights, the scales.  Each is issued by itself between two
+    // MFMAs: a wave that issues several in a row waits for the memory pipe,
+    // 16 cycles a load and eight waves at it, with its MFMAs behind.
+    constexpr int kTok = Fp8Loader<BT, false, F32>::kInstr, kEarly = kTok + 2;
+    auto issue_early = [&](auto l, uint8_t* sT, uint8_t* sWa, int kt) {
       const int k_left = kt < steps ? K : 0;   // past the end: zeros
-      lt.issue(sT, kt, wave_s, k_left);
-      lw.template issue<0, 2>(sWa, kt, wave_s, k_left);
+      if constexpr (l < kTok) lt.template issue<l, l + 1>(sT, kt, wave_s, k_left);
+      else lw.template issue<l - kTok, l - kTok + 1>(sWa, kt, wave_s, k_left);
     };
-    auto issue_late = [&](uint8_t* sWb, int kt) {
-      lw.template issue<2, 4>(sWb, kt, wave_s, kt < steps ? K : 0);
+    auto issue_late = [&](auto l, uint8_t* sWb, int kt) {
+      lw.template issue<2 + l, 3 + l>(sWb, kt, wave_s, kt < steps ? K : 0);
+    };
+    auto issue_scales = [&](uint8_t* sWb, int kt) {
       fp8_dma4(fp8_rsrc(s_base + (kt < steps ? kt : 0) * s_step, 0x7ffffffeu), scales(sWb) + wave_s * 64,
                kt < steps ? s_voff : kFp8OutOfRange, 0);
     };
-    constexpr int kEarly = Fp8Loader<BT, false>::kInstr + 2, kLate = 3;
 
     f32x4 acc[8][J];
 #pragma unroll
@@ -346,12 +356,12 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
     float fr[2][J];
     f32x4 wf[2];
     auto read_w = [&](auto i, const uint8_t* sW, const float* sS) {   // sW: the half with tile i
-      const uint8_t* r = sW + (w_row + 4 * (i % 4)) * kFp8Blk;
+      const uint8_t* r = sW + (w_row + w_off(i)) * kFp8Blk;
       wr[i & 1].x = *reinterpret_cast<const i32x4*>(r + 16 * (g4 ^ w_sw));
       wr[i & 1].y = *reinterpret_cast<const i32x4*>(r + 16 * ((g4 + 4) ^ w_sw));
       if constexpr (WG)
-        wf[i & 1] = *reinterpret_cast<const f32x4*>(sS + 256 + 128 * wn + 64 * (i / 4) + 16 * g4 +
-                                                    4 * (i % 4));
+        wf[i & 1] = *reinterpret_cast<const f32x4*>(sS + 256 + 128 * wn + 64 * (i / 4) + w_off(i) +
+                                                    (F32 ? 4 : 8) * g4);
     };
     auto read_t = [&](auto par, auto j, const uint8_t* sT, const float* sS) {
       const uint8_t* r = sT + (t_row + 16 * j) * kFp8Blk;
@@ -367,11 +377,13 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
     // the stage's tokens and the first half of its weights (a barrier), so the
     // loads of stage kt + 2 into that room go out; before the last weight tile
     // all of the stage is read and the next one has landed (the other
-    // barrier), so the rest goes out, and the next step's tokens are read into
-    // the registers that the last MFMAs leave.
+    // barrier), so the other weights go out (the scales follow in the next
+    // step), and the next step's tokens are read into the registers that the
+    // last MFMAs leave.
     auto step = [&](auto par, uint8_t* sT, uint8_t* sWa, uint8_t* sWb,
-                    const uint8_t* nT, const uint8_t* nWa, const uint8_t* nWb, int kt) {
-      const float *sS = scales(sWb), *nS = scales(nWb);
+                    const uint8_t* nT, const uint8_t* nWa, uint8_t* nWb, int kt) {
+      const float* sS = scales(sWb);
+      const float* nS = scales(nWb);
       constexpr int P = decltype(par)::value;
       Fp8Frag<F32> t[J];
 #pragma unroll
@@ -394,7 +406,6 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
           __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
           __builtin_amdgcn_s_barrier();
           asm volatile("" ::: "memory");
-          issue_early(sT, sWa, kt + 2);
         }
         if constexpr (i < 7) {
           read_w(std::integral_constant<int, i + 1>{}, i < 3 ? sWa : sWb, sS);
@@ -404,7 +415,6 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
           __builtin_amdgcn_s_barrier();
           asm volatile("" ::: "memory");
           read_w(std::integral_constant<int, 0>{}, nWa, nS);
-          issue_late(sWb, kt + 2);
         }
         Fp8Frag<F32> w;
         w.set(wr[i & 1].x, wr[i & 1].y);
@@ -414,6 +424,14 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
           p[m % kRing] = fp8_block_mfma(w, t[j]);
           if constexpr (m >= kLag) add(std::integral_constant<int, m - kLag>{});
           if constexpr (i == 7) read_t(std::integral_constant<int, 1 - P>{}, j, nT, nS);
+          if constexpr (i == 0 && j == J - 1) issue_scales(nWb, kt + 1);
+          if constexpr (i == 7)
+            fp8_for<2>([&](auto l) {
+              if constexpr (j == (J == 4 ? 1 + 2 * l : J - 1)) issue_late(l, sWb, kt + 2);
+            });
+          fp8_for<kEarly>([&](auto l) {   // two for each of tiles 4, 5 and 6
+            if constexpr (i == 4 + l / 2 && j == (l % 2 ? J - 1 : J / 2 - (J == 4))) issue_early(l, sT, sWa, kt + 2);
+          });
           __builtin_amdgcn_sched_barrier(0);
         });
       });
@@ -421,12 +439,13 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
     };
 
     if (steps > 0) {
-      issue_early(sT0, sWa0, 0);
-      issue_late(sWb0, 0);
-      issue_early(sT1, sWa1, 1);
-      issue_late(sWb1, 1);
+      fp8_for<kEarly>([&](auto l) { issue_early(l, sT0, sWa0, 0); });
+      fp8_for<2>([&](auto l) { issue_late(l, sWb0, 0); });
+      issue_scales(sWb0, 0);
+      fp8_for<kEarly>([&](auto l) { issue_early(l, sT1, sWa1, 1); });
+      fp8_for<2>([&](auto l) { issue_late(l, sWb1, 1); });
       asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kEarly + kLate));   // stage 0 landed
+      __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kEarly + 2));   // stage 0 landed
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       fp8_for<J>([&](auto j) { read_t(std::integral_constant<int, 0>{}, j, sT0, scales(sWb0)); });
@@ -446,30 +465,25 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
       asm volatile("" ::: "memory");
     }
 
-    // ---- store: 16 consecutive outputs of a token per four weight tiles ----
+    // ---- store: 16 consecutive bytes of a token per one or two weight tiles ----
     const int64_t c_row0 = WG ? static_cast<int64_t>(e) * g.P + t0 : static_cast<int64_t>(start) + t0;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
       const int tok = t_row + 16 * j;
       if (tok < rows_a) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int n = 128 * wn + 64 * v + 16 * g4;
-          if (n < rows_b) {   // N % 16 == 0: all 16 or none
-            const int64_t at = (c_row0 + tok) * g.ldc + n0 + n;
+        for (int i = 0; i < 8; i += F32 ? 1 : 2) {
+          const int n = 128 * wn + 64 * (i / 4) + w_off(i);   // N % 16 == 0: the lanes' 16 or 32 go or stay ..
+          if (n + (F32 ? 4 : 8) * g4 < rows_b) {              // .. in whole groups of 16
+            const int64_t at = (c_row0 + tok) * g.ldc + n0 + n + (F32 ? 4 : 8) * g4;
             if constexpr (F32) {
               f32x4* c = reinterpret_cast<f32x4*>(static_cast<float*>(g.c) + at);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                c[i] = WG && g.accumulate ? c[i] + acc[4 * v + i][j] : acc[4 * v + i][j];
+              *c = WG && g.accumulate ? *c + acc[i][j] : acc[i][j];
             } else {
-              uint4* c = reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.c) + at);
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const f32x4 &x = acc[4 * v + 2 * i][j], &y = acc[4 * v + 2 * i + 1][j];
-                c[i] = uint4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                             pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3])};
-              }
+              const f32x4 &x = acc[i][j], &y = acc[i + 1][j];
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.c) + at) =
+                  uint4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]),
+                        pack_bf16x2(y[2], y[3])};
             }
           }
         }
