@@ -23,8 +23,8 @@
 //     banks.
 //   * MFMA row m of weight tile i is weight row 32 (i / 2) + 8 (m / 4) +
 //     4 (i % 2) + m % 4 (bf16 output) or 16 i + m (fp32), so that a lane's
-//     outputs of two tiles, or of one, are 16 consecutive bytes of its token
-//     and a store covers 64 consecutive bytes of 16 rows.
+//     outputs of two tiles, or of one, are 16 consecutive bytes of its token;
+//     they leave through LDS as whole rows.
 //   * Persistent workgroups walk the tiles of all experts, whose sizes are
 //     read from device memory.
 // Precision: the FP8 MFMAs add eight neighbouring products aligned to the
@@ -56,6 +56,7 @@ constexpr int kFp8Blk = MOE_FP8_BLOCK; // K values (bytes) of a stage
 typedef __attribute__((address_space(3))) void fp8_lds_t;
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int fp8_u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFp8OutOfRange = 0x7fffffff;   // buffer offset past any record
 
@@ -465,30 +466,71 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
       asm volatile("" ::: "memory");
     }
 
-    // ---- store: 16 consecutive bytes of a token per one or two weight tiles ----
+    // ---- store ----
+    // Straight from the accumulators a store would cover 64 bytes of 16 rows.
+    // Instead each wave passes its outputs, 16 tokens (4 or 8 KB) at a time,
+    // through LDS of its own (the stages are drained) and stores whole rows of
+    // its 128 columns: 235 -> 179 us where an output of 755 MB is all there is
+    // to do.  16-byte chunk c of row r lies at c ^ r, so that writes (16 rows,
+    // one chunk) and reads (one row) fall on different banks.
+    constexpr int kOut = F32 ? 4 : 2, kRow = 128 * kOut, kChunks = kRow / 16;
+    // token groups that have room at once: all of a 256-token tile's 128 KB
+    // and of smaller bf16 ones, else one
+    constexpr int kAtOnce = F32 ? 1 : J, kOwn = kAtOnce * 16 * kRow;
+    static_assert(kOwn <= (J == 4 ? 16384 : 8192), "a wave's room");
+    uint8_t* own = J == 4 ? (wave < 2   ? sT0 + (wave & 1) * kOwn
+                             : wave < 4 ? sT1 + (wave & 1) * kOwn
+                             : wave < 6 ? (wave & 1 ? sWa1 : sWa0)
+                                        : (wave & 1 ? sWb1 : sWb0))
+                          : (wave < 4 ? (wave < 2 ? sWa0 : sWa1) : (wave < 6 ? sWb0 : sWb1)) + (wave & 1) * 8192;
     const int64_t c_row0 = WG ? static_cast<int64_t>(e) * g.P + t0 : static_cast<int64_t>(start) + t0;
+    // opaque, so that no address here is held in registers over the K loop
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int r16 = ln & 15, q4 = ln >> 4;
+    const int chunk = ln % kChunks, n = 128 * wn + chunk * (16 / kOut);
+    char* c_tile = static_cast<char*>(g.c) + (c_row0 * g.ldc + n0 + n) * kOut;
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int tok = t_row + 16 * j;
-      if (tok < rows_a) {
+    for (int j0 = 0; j0 < J; j0 += kAtOnce) {
+#pragma unroll
+      for (int jj = 0; jj < kAtOnce; ++jj) {
+        const int j = j0 + jj;
 #pragma unroll
         for (int i = 0; i < 8; i += F32 ? 1 : 2) {
-          const int n = 128 * wn + 64 * (i / 4) + w_off(i);   // N % 16 == 0: the lanes' 16 or 32 go or stay ..
-          if (n + (F32 ? 4 : 8) * g4 < rows_b) {              // .. in whole groups of 16
-            const int64_t at = (c_row0 + tok) * g.ldc + n0 + n + (F32 ? 4 : 8) * g4;
-            if constexpr (F32) {
-              f32x4* c = reinterpret_cast<f32x4*>(static_cast<float*>(g.c) + at);
-              *c = WG && g.accumulate ? *c + acc[i][j] : acc[i][j];
-            } else {
-              const f32x4 &x = acc[i][j], &y = acc[i + 1][j];
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.c) + at) =
-                  uint4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]),
-                        pack_bf16x2(y[2], y[3])};
-            }
+          const int cw = (64 * (i / 4) + w_off(i)) * kOut / 16 + q4;
+          fp8_u32x4 w;
+          if constexpr (F32) {
+            w = __builtin_bit_cast(fp8_u32x4, acc[i][j]);
+          } else {
+            const f32x4 &x = acc[i][j], &y = acc[i + 1][j];
+            w = fp8_u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]),
+                          pack_bf16x2(y[2], y[3])};
           }
+          *reinterpret_cast<fp8_u32x4*>(own + (16 * jj + r16) * kRow + 16 * (cw ^ r16)) = w;
         }
       }
+      // LDS operations of one wave complete in order
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int q = 0; q < kAtOnce * 16 * kChunks / kWave; ++q) {
+        const int r = ln / kChunks + q * (kWave / kChunks), tok = 16 * J * wt + 16 * j0 + r;
+        fp8_u32x4 w = *reinterpret_cast<const fp8_u32x4*>(own + r * kRow + 16 * (chunk ^ (r & 15)));
+        if (tok < rows_a && n < rows_b) {   // N % 16 == 0: the 16 bytes are inside or outside
+          auto* c = reinterpret_cast<fp8_u32x4*>(c_tile + static_cast<int64_t>(tok) * g.ldc * kOut);
+          if (F32 && WG && g.accumulate)
+            w = __builtin_bit_cast(fp8_u32x4, __builtin_bit_cast(f32x4, *c) + __builtin_bit_cast(f32x4, w));
+          *c = w;
+        }
+      }
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_wave_barrier();
     }
+    // every wave has read its rows: the next tile's loads may come
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
   }
 }
 
