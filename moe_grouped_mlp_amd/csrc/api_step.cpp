@@ -35,12 +35,6 @@ int tile_grid(int cu, int margin, int64_t tiles) {
   return g < 1 ? 1 : g;
 }
 
-// Tokens of a product's tile for groups of at most `most` rows.  An fp32
-// output's widened operands take twice the registers, so its tiles end at 128.
-int tile_tokens(int64_t most, bool f32) {
-  return most <= 16 ? 16 : most <= 32 ? 32 : most <= 64 ? 64 : most <= 128 || f32 ? 128 : 256;
-}
-
 struct Range {
   uintptr_t lo, hi;
   bool write;
@@ -145,8 +139,7 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
     return MOE_ERR_INVALID_ARG;
   const int64_t most = a->max_rows ? std::min<int64_t>(a->max_rows, a->M_cap) : a->M_cap;
   const bool f32 = a->c_type == MOE_TYPE_F32;
-  const int tokens = tile_tokens(most, f32);
-  const int64_t tiles = (ceil_div(a->M_cap, std::max(tokens, 64)) + a->E) * ceil_div(a->N, kTileN);
+  const int64_t tiles = (ceil_div(a->M_cap, moe::fp8_tile_tokens(f32)) + a->E) * ceil_div(a->N, kTileN);
   if (tiles > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   int cu = 0;
   if (moe_status st = moe::current_device(&cu)) return st;
@@ -169,8 +162,8 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
   g.group_m = 4;
   g.err = a->err_flag;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (tokens <= 32) return launched(moe::launch_fp8_rows(g, tokens, f32, s));
-  return launched(moe::launch_fp8_gemm(g, tokens, f32, tile_grid(cu, a->cu_margin, tiles), s));
+  if (most <= 32) return launched(moe::launch_fp8_rows(g, most <= 16 ? 16 : 32, f32, s));
+  return launched(moe::launch_fp8_gemm(g, f32, tile_grid(cu, a->cu_margin, tiles), s));
 }
 
 moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {
@@ -181,7 +174,7 @@ moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {
       !aligned16(a->a) || !aligned16(a->b) || !aligned16(a->c))
     return MOE_ERR_INVALID_ARG;
   const bool f32 = a->c_type == MOE_TYPE_F32;
-  const int64_t tiles = a->E * ceil_div(a->P, f32 ? 128 : 256) * ceil_div(a->Q, kTileN);
+  const int64_t tiles = a->E * ceil_div(a->P, moe::fp8_tile_tokens(f32)) * ceil_div(a->Q, kTileN);
   if (tiles > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   int cu = 0;
   if (moe_status st = moe::current_device(&cu)) return st;

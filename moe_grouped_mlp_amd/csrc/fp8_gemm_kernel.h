@@ -14,8 +14,10 @@
 // column tile and the 128 x 128 weight scale is uniform.
 //
 // Work decomposition
-//   * Workgroup: 8 waves (two per SIMD), tile 64 J tokens x 256 weight rows,
-//     wave (wn, wt) = 128 weight rows x 16 J tokens (8 x J MFMA tiles).
+//   * Workgroup: 8 waves (two per SIMD), tile 256 tokens (fp32 output: 128) x
+//     256 weight rows, wave (wn, wt) = 128 weight rows x a quarter of the
+//     tokens (8 x 4 MFMA tiles).  A group's last tile runs with 64, 128 or 192
+//     tokens if it holds no more.
 //   * Operands go from HBM straight into LDS (buffer loads with the LDS
 //     destination), two stages of one scale block (128 bytes of every row)
 //     each; their scales ride along.  16-byte chunk c of a row is stored at
@@ -196,12 +198,12 @@ struct Fp8Loader {
   }
 };
 
-// J: MFMA token tiles per wave; WG: the weight gradient; F32: fp32 output,
+// JMAX: MFMA token tiles per wave; WG: the weight gradient; F32: fp32 output,
 // summed from widened operands.
-template <int J, bool WG, bool F32>
+template <int JMAX, bool WG, bool F32>
 __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 2))) void fp8_gemm_kernel(
     const Fp8Args g) {
-  constexpr int BT = 64 * J;   // tokens of a tile
+  constexpr int BT = 64 * JMAX;   // tokens of a tile
   __shared__ __attribute__((aligned(1024))) uint8_t sT0[BT * kFp8Blk], sT1[BT * kFp8Blk];
   // weights: the rows of tiles 0 .. 3 (a) and 4 .. 7 (b) of both wave columns;
   // behind the latter the stage's scales: tokens at 0, weights at 256 (WG:
@@ -267,14 +269,6 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
   int vid = blockIdx.x;
   if (G % kNumXcd == 0) vid = (blockIdx.x % kNumXcd) * (G / kNumXcd) + blockIdx.x / kNumXcd;
 
-  // operand reads: byte offsets of the lane's row and its two chunks
-  const int l16 = lane & 15, g4 = lane >> 4;
-  const int t_row = 16 * J * wt + l16;
-  const int w_row = 64 * wn + (F32 ? l16 : 8 * (l16 >> 2) + (l16 & 3));
-  auto w_off = [](int i) { return F32 ? 16 * (i % 4) : 32 * (i % 4 / 2) + 4 * (i % 2); };
-  // unchanged by + 16 j and + w_off(i)
-  const int t_sw = fp8_swz_t(t_row), w_sw = fp8_swz_w<F32>(w_row);
-
   for (int id = vid; id < total; id += G) {
     int lo = 0, hi = g.E - 1;   // the expert of the tile
     while (lo < hi) {
@@ -293,244 +287,268 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
     const int m_b = in_b % gm, t_n = in_b / gm;
     const int t0 = (band * g.group_m + m_b) * BT, n0 = t_n * kFp8BN;
 
-    const int K = WG ? (n_e + kFp8Blk - 1) / kFp8Blk * kFp8Blk : g.K;
-    const int steps = (K + kFp8Blk - 1) / kFp8Blk;
-    const int rows_a = rows_t - t0, rows_b = g.N - n0;
-    Fp8Loader<BT, false, F32> lt;
-    Fp8Loader<kFp8BN, true, F32> lw;
-    const uint8_t* b_e = static_cast<const uint8_t*>(g.b) + (WG ? start : e * g.b_stride);
-    lt.init(g.a + (WG ? static_cast<int64_t>(t0) * g.M_cap + start
-                      : static_cast<int64_t>(start + t0) * g.K),
-            rows_a, WG ? g.M_cap : g.K, K, wave_s, lane);
-    const int64_t ld_b = WG ? g.M_cap : g.K;
-    lw.init(b_e + n0 * ld_b, rows_b, ld_b, K, wave_s, lane);
-    // this wave's 64 scales of a stage: waves 0 .. 3 tokens, 4 .. 7 weights
-    const bool s_tok = wave_s < 4;
-    const int s_i = (wave_s & 3) * 64 + lane;
-    const float* s_base;
-    int64_t s_step;
-    int s_voff = kFp8OutOfRange;
-    if (s_tok) {
-      s_base = WG ? g.a_s + static_cast<int64_t>(start / kFp8Blk) * g.P + t0 : g.a_s + start + t0;
-      s_step = WG ? g.P : g.M_cap;
-      if (s_i < BT && s_i < rows_a) s_voff = 4 * s_i;
-    } else if constexpr (WG) {
-      s_base = g.b_s + static_cast<int64_t>(start / kFp8Blk) * g.N + n0;
-      s_step = g.N;
-      if (s_i < rows_b) s_voff = 4 * s_i;
-    } else {
-      s_base = g.b_s + e * g.b_s_stride + static_cast<int64_t>(n0 / kFp8Blk) * steps;
-      s_step = 1;
-      if (s_i < 2 && s_i * kFp8Blk < rows_b) s_voff = 4 * s_i * steps;
-    }
-    // A stage's loads in the order they go out: the tokens and the weights of
-    // tiles 0 .. 3 (early: their room is free half a step before the rest's),
-    // the other weights, the scales.  Each is issued by itself between two
-    // MFMAs: a wave that issues several in a row waits for the memory pipe,
-    // 16 cycles a load and eight waves at it, with its MFMAs behind.
-    constexpr int kTok = Fp8Loader<BT, false, F32>::kInstr, kEarly = kTok + 2;
-    auto issue_early = [&](auto l, uint8_t* sT, uint8_t* sWa, int kt) {
-      const int k_left = kt < steps ? K : 0;   // past the end: zeros
-      if constexpr (l < kTok) lt.template issue<l, l + 1>(sT, kt, wave_s, k_left);
-      else lw.template issue<l - kTok, l - kTok + 1>(sWa, kt, wave_s, k_left);
-    };
-    auto issue_late = [&](auto l, uint8_t* sWb, int kt) {
-      lw.template issue<2 + l, 3 + l>(sWb, kt, wave_s, kt < steps ? K : 0);
-    };
-    auto issue_scales = [&](uint8_t* sWb, int kt) {
-      fp8_dma4(fp8_rsrc(s_base + (kt < steps ? kt : 0) * s_step, 0x7ffffffeu), scales(sWb) + wave_s * 64,
-               kt < steps ? s_voff : kFp8OutOfRange, 0);
-    };
-
-    f32x4 acc[8][J];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < J; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    // Registers of the pipeline: the weight tile in use and the next one, the
-    // step's tokens, and their scales for this step and the next.
-    struct Raw {
-      i32x4 x, y;
-    };
-    Raw wr[2], tr[J];
-    float fr[2][J];
-    f32x4 wf[2];
-    auto read_w = [&](auto i, const uint8_t* sW, const float* sS) {   // sW: the half with tile i
-      const uint8_t* r = sW + (w_row + w_off(i)) * kFp8Blk;
-      wr[i & 1].x = *reinterpret_cast<const i32x4*>(r + 16 * (g4 ^ w_sw));
-      wr[i & 1].y = *reinterpret_cast<const i32x4*>(r + 16 * ((g4 + 4) ^ w_sw));
-      if constexpr (WG)
-        wf[i & 1] = *reinterpret_cast<const f32x4*>(sS + 256 + 128 * wn + 64 * (i / 4) + w_off(i) +
-                                                    (F32 ? 4 : 8) * g4);
-    };
-    auto read_t = [&](auto par, auto j, const uint8_t* sT, const float* sS) {
-      const uint8_t* r = sT + (t_row + 16 * j) * kFp8Blk;
-      tr[j].x = *reinterpret_cast<const i32x4*>(r + 16 * (g4 ^ t_sw));
-      tr[j].y = *reinterpret_cast<const i32x4*>(r + 16 * ((g4 + 4) ^ t_sw));
-      fr[par][j] = sS[t_row + 16 * j];
-      if constexpr (!WG) fr[par][j] *= sS[256 + wn];
-    };
-    // One step on the stage in (sT, sWa, sWb), par: which registers hold its
-    // token scales.  Weight tile i + 1 is read while tile i's MFMAs run, and an
-    // MFMA's sums are added three MFMAs later, when they are there (held in that
-    // order, else the compiler adds them at once, behind wait states).  Half way every wave is done with
-    // the stage's tokens and the first half of its weights (a barrier), so the
-    // loads of stage kt + 2 into that room go out; before the last weight tile
-    // all of the stage is read and the next one has landed (the other
-    // barrier), so the other weights go out (the scales follow in the next
-    // step), and the next step's tokens are read into the registers that the
-    // last MFMAs leave.
-    auto step = [&](auto par, uint8_t* sT, uint8_t* sWa, uint8_t* sWb,
-                    const uint8_t* nT, const uint8_t* nWa, uint8_t* nWb, int kt) {
-      const float* sS = scales(sWb);
-      const float* nS = scales(nWb);
-      constexpr int P = decltype(par)::value;
-      Fp8Frag<F32> t[J];
-#pragma unroll
-      for (int j = 0; j < J; ++j) t[j].set(tr[j].x, tr[j].y);
-      constexpr int kLag = 3, kRing = 4;
-      f32x4 p[kRing];
-      constexpr int kW = J >= kLag ? 2 : 4;   // weight tiles whose sums are outstanding
-      f32x4 wfm[kW];
-      auto add = [&](auto m) {   // the sums of MFMA m
-        constexpr int i = m / J, j = m % J;
-#pragma unroll
-        for (int r4 = 0; r4 < 4; ++r4) {
-          const float s = WG ? fr[P][j] * wfm[i % kW][r4] : fr[P][j];
-          acc[i][j][r4] = __builtin_fmaf(p[m % kRing][r4], s, acc[i][j][r4]);
-        }
+    // The tile with 64 JT tokens, JT the least that covers its rows: the last
+    // rows of a group cost what they are, not a whole tile.
+    auto run = [&](auto jt) {
+      constexpr int J = decltype(jt)::value, BT = 64 * J;
+      // opaque, so that the variants' addresses are made here and not held in
+      // registers (and spilled, and read back behind the stores) over all tiles
+      int lane = tid & 63;
+      asm volatile("" : "+v"(lane));
+      // operand reads: the lane's rows; their swizzles are unchanged by + 16 j
+      // and + w_off(i)
+      const int l16 = lane & 15, g4 = lane >> 4;
+      const int t_row = 16 * J * wt + l16, w_row = 64 * wn + (F32 ? l16 : 8 * (l16 >> 2) + (l16 & 3));
+      auto w_off = [](int i) { return F32 ? 16 * (i % 4) : 32 * (i % 4 / 2) + 4 * (i % 2); };
+      const int t_sw = fp8_swz_t(l16), w_sw = fp8_swz_w<F32>(w_row);
+      const int K = WG ? (n_e + kFp8Blk - 1) / kFp8Blk * kFp8Blk : g.K;
+      const int steps = (K + kFp8Blk - 1) / kFp8Blk;
+      const int rows_a = rows_t - t0, rows_b = g.N - n0;
+      Fp8Loader<BT, false, F32> lt;
+      Fp8Loader<kFp8BN, true, F32> lw;
+      const uint8_t* b_e = static_cast<const uint8_t*>(g.b) + (WG ? start : e * g.b_stride);
+      lt.init(g.a + (WG ? static_cast<int64_t>(t0) * g.M_cap + start
+                        : static_cast<int64_t>(start + t0) * g.K),
+              rows_a, WG ? g.M_cap : g.K, K, wave_s, lane);
+      const int64_t ld_b = WG ? g.M_cap : g.K;
+      lw.init(b_e + n0 * ld_b, rows_b, ld_b, K, wave_s, lane);
+      // this wave's 64 scales of a stage: waves 0 .. 3 tokens, 4 .. 7 weights
+      const bool s_tok = wave_s < 4;
+      const int s_i = (wave_s & 3) * 64 + lane;
+      const float* s_base;
+      int64_t s_step;
+      int s_voff = kFp8OutOfRange;
+      if (s_tok) {
+        s_base = WG ? g.a_s + static_cast<int64_t>(start / kFp8Blk) * g.P + t0 : g.a_s + start + t0;
+        s_step = WG ? g.P : g.M_cap;
+        if (s_i < BT && s_i < rows_a) s_voff = 4 * s_i;
+      } else if constexpr (WG) {
+        s_base = g.b_s + static_cast<int64_t>(start / kFp8Blk) * g.N + n0;
+        s_step = g.N;
+        if (s_i < rows_b) s_voff = 4 * s_i;
+      } else {
+        s_base = g.b_s + e * g.b_s_stride + static_cast<int64_t>(n0 / kFp8Blk) * steps;
+        s_step = 1;
+        if (s_i < 2 && s_i * kFp8Blk < rows_b) s_voff = 4 * s_i * steps;
+      }
+      // A stage's loads in the order they go out: the tokens and the weights of
+      // tiles 0 .. 3 (early: their room is free half a step before the rest's),
+      // the other weights, the scales.  Each is issued by itself between two
+      // MFMAs: a wave that issues several in a row waits for the memory pipe,
+      // 16 cycles a load and eight waves at it, with its MFMAs behind.
+      constexpr int kTok = Fp8Loader<BT, false, F32>::kInstr, kEarly = kTok + 2;
+      auto issue_early = [&](auto l, uint8_t* sT, uint8_t* sWa, int kt) {
+        const int k_left = kt < steps ? K : 0;   // past the end: zeros
+        if constexpr (l < kTok) lt.template issue<l, l + 1>(sT, kt, wave_s, k_left);
+        else lw.template issue<l - kTok, l - kTok + 1>(sWa, kt, wave_s, k_left);
       };
-      fp8_for<8>([&](auto i) {
-        if constexpr (i == 4) {
-          asm volatile("" ::: "memory");
-          __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-          __builtin_amdgcn_s_barrier();
-          asm volatile("" ::: "memory");
-        }
-        if constexpr (i < 7) {
-          read_w(std::integral_constant<int, i + 1>{}, i < 3 ? sWa : sWb, sS);
-        } else {
-          asm volatile("" ::: "memory");
-          __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kEarly) & 0xC07F);   // and lgkmcnt(0)
-          __builtin_amdgcn_s_barrier();
-          asm volatile("" ::: "memory");
-          read_w(std::integral_constant<int, 0>{}, nWa, nS);
-        }
-        Fp8Frag<F32> w;
-        w.set(wr[i & 1].x, wr[i & 1].y);
-        if constexpr (WG) wfm[i % kW] = wf[i & 1];
-        fp8_for<J>([&](auto j) {
-          constexpr int m = i * J + j;
-          p[m % kRing] = fp8_block_mfma(w, t[j]);
-          if constexpr (m >= kLag) add(std::integral_constant<int, m - kLag>{});
-          if constexpr (i == 7) read_t(std::integral_constant<int, 1 - P>{}, j, nT, nS);
-          if constexpr (i == 0 && j == J - 1) issue_scales(nWb, kt + 1);
-          if constexpr (i == 7)
-            fp8_for<2>([&](auto l) {
-              if constexpr (j == (J == 4 ? 1 + 2 * l : J - 1)) issue_late(l, sWb, kt + 2);
-            });
-          fp8_for<kEarly>([&](auto l) {   // two for each of tiles 4, 5 and 6
-            if constexpr (i == 4 + l / 2 && j == (l % 2 ? J - 1 : J / 2 - (J == 4))) issue_early(l, sT, sWa, kt + 2);
-          });
-          __builtin_amdgcn_sched_barrier(0);
-        });
-      });
-      fp8_for<kLag>([&](auto l) { add(std::integral_constant<int, 8 * J - kLag + l>{}); });
-    };
+      auto issue_late = [&](auto l, uint8_t* sWb, int kt) {
+        lw.template issue<2 + l, 3 + l>(sWb, kt, wave_s, kt < steps ? K : 0);
+      };
+      auto issue_scales = [&](uint8_t* sWb, int kt) {
+        fp8_dma4(fp8_rsrc(s_base + (kt < steps ? kt : 0) * s_step, 0x7ffffffeu), scales(sWb) + wave_s * 64,
+                 kt < steps ? s_voff : kFp8OutOfRange, 0);
+      };
 
-    if (steps > 0) {
-      fp8_for<kEarly>([&](auto l) { issue_early(l, sT0, sWa0, 0); });
-      fp8_for<2>([&](auto l) { issue_late(l, sWb0, 0); });
-      issue_scales(sWb0, 0);
-      fp8_for<kEarly>([&](auto l) { issue_early(l, sT1, sWa1, 1); });
-      fp8_for<2>([&](auto l) { issue_late(l, sWb1, 1); });
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kEarly + 2));   // stage 0 landed
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      fp8_for<J>([&](auto j) { read_t(std::integral_constant<int, 0>{}, j, sT0, scales(sWb0)); });
-      read_w(std::integral_constant<int, 0>{}, sWa0, scales(sWb0));
-      // (a loop with its exit in the middle would make the compiler wait for
-      // loads that only that way out leaves in flight)
-      int kt = 0;
-      for (; kt + 1 < steps; kt += 2) {
-        step(std::integral_constant<int, 0>{}, sT0, sWa0, sWb0, sT1, sWa1, sWb1, kt);
-        step(std::integral_constant<int, 1>{}, sT1, sWa1, sWb1, sT0, sWa0, sWb0, kt + 1);
-      }
-      if (kt < steps) step(std::integral_constant<int, 0>{}, sT0, sWa0, sWb0, sT1, sWa1, sWb1, kt);
-      // the zero fills past the end, and reads of the stage behind the last
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_waitcnt(0x0070);
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-    }
+      f32x4 acc[8][J];
+  #pragma unroll
+      for (int i = 0; i < 8; ++i)
+  #pragma unroll
+        for (int j = 0; j < J; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    // ---- store ----
-    // Straight from the accumulators a store would cover 64 bytes of 16 rows.
-    // Instead each wave passes its outputs, 16 tokens (4 or 8 KB) at a time,
-    // through LDS of its own (the stages are drained) and stores whole rows of
-    // its 128 columns: 235 -> 179 us where an output of 755 MB is all there is
-    // to do.  16-byte chunk c of row r lies at c ^ r, so that writes (16 rows,
-    // one chunk) and reads (one row) fall on different banks.
-    constexpr int kOut = F32 ? 4 : 2, kRow = 128 * kOut, kChunks = kRow / 16;
-    // token groups that have room at once: all of a 256-token tile's 128 KB
-    // and of smaller bf16 ones, else one
-    constexpr int kAtOnce = F32 ? 1 : J, kOwn = kAtOnce * 16 * kRow;
-    static_assert(kOwn <= (J == 4 ? 16384 : 8192), "a wave's room");
-    uint8_t* own = J == 4 ? (wave < 2   ? sT0 + (wave & 1) * kOwn
-                             : wave < 4 ? sT1 + (wave & 1) * kOwn
-                             : wave < 6 ? (wave & 1 ? sWa1 : sWa0)
-                                        : (wave & 1 ? sWb1 : sWb0))
-                          : (wave < 4 ? (wave < 2 ? sWa0 : sWa1) : (wave < 6 ? sWb0 : sWb1)) + (wave & 1) * 8192;
-    const int64_t c_row0 = WG ? static_cast<int64_t>(e) * g.P + t0 : static_cast<int64_t>(start) + t0;
-    // opaque, so that no address here is held in registers over the K loop
-    int ln = lane;
-    asm volatile("" : "+v"(ln));
-    const int r16 = ln & 15, q4 = ln >> 4;
-    const int chunk = ln % kChunks, n = 128 * wn + chunk * (16 / kOut);
-    char* c_tile = static_cast<char*>(g.c) + (c_row0 * g.ldc + n0 + n) * kOut;
-#pragma unroll
-    for (int j0 = 0; j0 < J; j0 += kAtOnce) {
-#pragma unroll
-      for (int jj = 0; jj < kAtOnce; ++jj) {
-        const int j = j0 + jj;
-#pragma unroll
-        for (int i = 0; i < 8; i += F32 ? 1 : 2) {
-          const int cw = (64 * (i / 4) + w_off(i)) * kOut / 16 + q4;
-          fp8_u32x4 w;
-          if constexpr (F32) {
-            w = __builtin_bit_cast(fp8_u32x4, acc[i][j]);
-          } else {
-            const f32x4 &x = acc[i][j], &y = acc[i + 1][j];
-            w = fp8_u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]),
-                          pack_bf16x2(y[2], y[3])};
+      // Registers of the pipeline: the weight tile in use and the next one, the
+      // step's tokens, and their scales for this step and the next.
+      struct Raw {
+        i32x4 x, y;
+      };
+      Raw wr[2], tr[J];
+      float fr[2][J];
+      f32x4 wf[2];
+      auto read_w = [&](auto i, const uint8_t* sW, const float* sS) {   // sW: the half with tile i
+        const uint8_t* r = sW + (w_row + w_off(i)) * kFp8Blk;
+        wr[i & 1].x = *reinterpret_cast<const i32x4*>(r + 16 * (g4 ^ w_sw));
+        wr[i & 1].y = *reinterpret_cast<const i32x4*>(r + 16 * ((g4 + 4) ^ w_sw));
+        if constexpr (WG)
+          wf[i & 1] = *reinterpret_cast<const f32x4*>(sS + 256 + 128 * wn + 64 * (i / 4) + w_off(i) +
+                                                      (F32 ? 4 : 8) * g4);
+      };
+      auto read_t = [&](auto par, auto j, const uint8_t* sT, const float* sS) {
+        const uint8_t* r = sT + (t_row + 16 * j) * kFp8Blk;
+        tr[j].x = *reinterpret_cast<const i32x4*>(r + 16 * (g4 ^ t_sw));
+        tr[j].y = *reinterpret_cast<const i32x4*>(r + 16 * ((g4 + 4) ^ t_sw));
+        fr[par][j] = sS[t_row + 16 * j];
+        if constexpr (!WG) fr[par][j] *= sS[256 + wn];
+      };
+      // One step on the stage in (sT, sWa, sWb), par: which registers hold its
+      // token scales.  Weight tile i + 1 is read while tile i's MFMAs run, and an
+      // MFMA's sums are added three MFMAs later, when they are there (held in that
+      // order, else the compiler adds them at once, behind wait states).  Half way every wave is done with
+      // the stage's tokens and the first half of its weights (a barrier), so the
+      // loads of stage kt + 2 into that room go out; before the last weight tile
+      // all of the stage is read and the next one has landed (the other
+      // barrier), so the other weights go out (the scales follow in the next
+      // step), and the next step's tokens are read into the registers that the
+      // last MFMAs leave.
+      auto step = [&](auto par, uint8_t* sT, uint8_t* sWa, uint8_t* sWb,
+                      const uint8_t* nT, const uint8_t* nWa, uint8_t* nWb, int kt) {
+        const float* sS = scales(sWb);
+        const float* nS = scales(nWb);
+        constexpr int P = decltype(par)::value;
+        Fp8Frag<F32> t[J];
+  #pragma unroll
+        for (int j = 0; j < J; ++j) t[j].set(tr[j].x, tr[j].y);
+        constexpr int kLag = 3, kRing = 4;
+        f32x4 p[kRing];
+        constexpr int kW = J >= kLag ? 2 : 4;   // weight tiles whose sums are outstanding
+        f32x4 wfm[kW];
+        auto add = [&](auto m) {   // the sums of MFMA m
+          constexpr int i = m / J, j = m % J;
+  #pragma unroll
+          for (int r4 = 0; r4 < 4; ++r4) {
+            const float s = WG ? fr[P][j] * wfm[i % kW][r4] : fr[P][j];
+            acc[i][j][r4] = __builtin_fmaf(p[m % kRing][r4], s, acc[i][j][r4]);
           }
-          *reinterpret_cast<fp8_u32x4*>(own + (16 * jj + r16) * kRow + 16 * (cw ^ r16)) = w;
+        };
+        fp8_for<8>([&](auto i) {
+          if constexpr (i == 4) {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+          }
+          if constexpr (i < 7) {
+            read_w(std::integral_constant<int, i + 1>{}, i < 3 ? sWa : sWb, sS);
+          } else {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kEarly) & 0xC07F);   // and lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            read_w(std::integral_constant<int, 0>{}, nWa, nS);
+          }
+          Fp8Frag<F32> w;
+          w.set(wr[i & 1].x, wr[i & 1].y);
+          if constexpr (WG) wfm[i % kW] = wf[i & 1];
+          fp8_for<J>([&](auto j) {
+            constexpr int m = i * J + j;
+            p[m % kRing] = fp8_block_mfma(w, t[j]);
+            if constexpr (m >= kLag) add(std::integral_constant<int, m - kLag>{});
+            if constexpr (i == 7) read_t(std::integral_constant<int, 1 - P>{}, j, nT, nS);
+            if constexpr (i == 0 && j == J - 1) issue_scales(nWb, kt + 1);
+            if constexpr (i == 7)
+              fp8_for<2>([&](auto l) {
+                if constexpr (j == (J == 4 ? 1 + 2 * l : J - 1)) issue_late(l, sWb, kt + 2);
+              });
+            fp8_for<kEarly>([&](auto l) {   // two for each of tiles 4, 5 and 6
+              if constexpr (i == 4 + l / 2 && j == (l % 2 ? J - 1 : J / 2 - (J == 4))) issue_early(l, sT, sWa, kt + 2);
+            });
+            __builtin_amdgcn_sched_barrier(0);
+          });
+        });
+        fp8_for<kLag>([&](auto l) { add(std::integral_constant<int, 8 * J - kLag + l>{}); });
+      };
+
+      if (steps > 0) {
+        fp8_for<kEarly>([&](auto l) { issue_early(l, sT0, sWa0, 0); });
+        fp8_for<2>([&](auto l) { issue_late(l, sWb0, 0); });
+        issue_scales(sWb0, 0);
+        fp8_for<kEarly>([&](auto l) { issue_early(l, sT1, sWa1, 1); });
+        fp8_for<2>([&](auto l) { issue_late(l, sWb1, 1); });
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(fp8_wait_vm(kEarly + 2));   // stage 0 landed
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        fp8_for<J>([&](auto j) { read_t(std::integral_constant<int, 0>{}, j, sT0, scales(sWb0)); });
+        read_w(std::integral_constant<int, 0>{}, sWa0, scales(sWb0));
+        // (a loop with its exit in the middle would make the compiler wait for
+        // loads that only that way out leaves in flight)
+        int kt = 0;
+        for (; kt + 1 < steps; kt += 2) {
+          step(std::integral_constant<int, 0>{}, sT0, sWa0, sWb0, sT1, sWa1, sWb1, kt);
+          step(std::integral_constant<int, 1>{}, sT1, sWa1, sWb1, sT0, sWa0, sWb0, kt + 1);
         }
+        if (kt < steps) step(std::integral_constant<int, 0>{}, sT0, sWa0, sWb0, sT1, sWa1, sWb1, kt);
+        // the zero fills past the end, and reads of the stage behind the last
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0x0070);
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
       }
-      // LDS operations of one wave complete in order
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int q = 0; q < kAtOnce * 16 * kChunks / kWave; ++q) {
-        const int r = ln / kChunks + q * (kWave / kChunks), tok = 16 * J * wt + 16 * j0 + r;
-        fp8_u32x4 w = *reinterpret_cast<const fp8_u32x4*>(own + r * kRow + 16 * (chunk ^ (r & 15)));
-        if (tok < rows_a && n < rows_b) {   // N % 16 == 0: the 16 bytes are inside or outside
-          auto* c = reinterpret_cast<fp8_u32x4*>(c_tile + static_cast<int64_t>(tok) * g.ldc * kOut);
-          if (F32 && WG && g.accumulate)
-            w = __builtin_bit_cast(fp8_u32x4, __builtin_bit_cast(f32x4, *c) + __builtin_bit_cast(f32x4, w));
-          *c = w;
+
+      // ---- store ----
+      // Straight from the accumulators a store would cover 64 bytes of 16 rows.
+      // Instead each wave passes its outputs, 16 tokens (4 or 8 KB) at a time,
+      // through LDS of its own (the stages are drained) and stores whole rows of
+      // its 128 columns: 235 -> 179 us where an output of 755 MB is all there is
+      // to do.  16-byte chunk c of row r lies at c ^ r, so that writes (16 rows,
+      // one chunk) and reads (one row) fall on different banks.
+      constexpr int kOut = F32 ? 4 : 2, kRow = 128 * kOut, kChunks = kRow / 16;
+      // token groups that have room at once: all (a bf16 tile, up to 128 KB), or one
+      constexpr int kAtOnce = F32 ? 1 : J, kOwn = kAtOnce * 16 * kRow;
+      static_assert(kOwn <= (JMAX == 4 ? 16384 : 8192), "a wave's room");
+      uint8_t* own = JMAX == 4 ? (wave < 2   ? sT0 + (wave & 1) * kOwn
+                               : wave < 4 ? sT1 + (wave & 1) * kOwn
+                               : wave < 6 ? (wave & 1 ? sWa1 : sWa0)
+                                          : (wave & 1 ? sWb1 : sWb0))
+                            : (wave < 4 ? (wave < 2 ? sWa0 : sWa1) : (wave < 6 ? sWb0 : sWb1)) + (wave & 1) * 8192;
+      const int64_t c_row0 = WG ? static_cast<int64_t>(e) * g.P + t0 : static_cast<int64_t>(start) + t0;
+      // opaque, so that no address here is held in registers over the K loop
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+      const int r16 = ln & 15, q4 = ln >> 4;
+      const int chunk = ln % kChunks, n = 128 * wn + chunk * (16 / kOut);
+      char* c_tile = static_cast<char*>(g.c) + (c_row0 * g.ldc + n0 + n) * kOut;
+  #pragma unroll
+      for (int j0 = 0; j0 < J; j0 += kAtOnce) {
+  #pragma unroll
+        for (int jj = 0; jj < kAtOnce; ++jj) {
+          const int j = j0 + jj;
+  #pragma unroll
+          for (int i = 0; i < 8; i += F32 ? 1 : 2) {
+            const int cw = (64 * (i / 4) + w_off(i)) * kOut / 16 + q4;
+            fp8_u32x4 w;
+            if constexpr (F32) {
+              w = __builtin_bit_cast(fp8_u32x4, acc[i][j]);
+            } else {
+              const f32x4 &x = acc[i][j], &y = acc[i + 1][j];
+              w = fp8_u32x4{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(y[0], y[1]),
+                            pack_bf16x2(y[2], y[3])};
+            }
+            *reinterpret_cast<fp8_u32x4*>(own + (16 * jj + r16) * kRow + 16 * (cw ^ r16)) = w;
+          }
         }
+        // LDS operations of one wave complete in order
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+  #pragma unroll
+        for (int q = 0; q < kAtOnce * 16 * kChunks / kWave; ++q) {
+          const int r = ln / kChunks + q * (kWave / kChunks), tok = 16 * J * wt + 16 * j0 + r;
+          fp8_u32x4 w = *reinterpret_cast<const fp8_u32x4*>(own + r * kRow + 16 * (chunk ^ (r & 15)));
+          if (tok < rows_a && n < rows_b) {   // N % 16 == 0: the 16 bytes are inside or outside
+            auto* c = reinterpret_cast<fp8_u32x4*>(c_tile + static_cast<int64_t>(tok) * g.ldc * kOut);
+            if (F32 && WG && g.accumulate)
+              w = __builtin_bit_cast(fp8_u32x4, __builtin_bit_cast(f32x4, *c) + __builtin_bit_cast(f32x4, w));
+            *c = w;
+          }
+        }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
       }
+      // every wave has read its rows: the next tile's loads may come
       asm volatile("" ::: "memory");
-      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    };
+    const int groups = (rows_t - t0 + 63) / 64;   // of 64 tokens
+    if constexpr (JMAX == 4) {
+      if (groups >= 4) run(std::integral_constant<int, 4>{});
+      else if (groups == 3) run(std::integral_constant<int, 3>{});
+      else if (groups == 2) run(std::integral_constant<int, 2>{});
+      else run(std::integral_constant<int, 1>{});
+    } else {
+      if (groups >= 2) run(std::integral_constant<int, 2>{});
+      else run(std::integral_constant<int, 1>{});
     }
-    // every wave has read its rows: the next tile's loads may come
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
   }
 }
 

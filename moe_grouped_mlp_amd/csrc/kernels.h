@@ -156,8 +156,9 @@ struct Fp8Args {
   int group_m;             // token tiles per band of the tile order
   int32_t* err;            // nullable
 };
-// tile_rows: 64, 128 or (bf16 output) 256 tokens per workgroup tile
-hipError_t launch_fp8_gemm(const Fp8Args& g, int tile_rows, bool f32, int grid, hipStream_t s);
+// tiles of fp8_tile_tokens(f32) tokens x 256 weight rows
+inline int fp8_tile_tokens(bool f32) { return f32 ? 128 : 256; }
+hipError_t launch_fp8_gemm(const Fp8Args& g, bool f32, int grid, hipStream_t s);
 // groups of few rows; tile_rows: 16 or 32 tokens at a time
 hipError_t launch_fp8_rows(const Fp8Args& g, int tile_rows, bool f32, hipStream_t s);
 hipError_t launch_fp8_wgrad(const Fp8Args& g, bool f32, int grid, hipStream_t s);
