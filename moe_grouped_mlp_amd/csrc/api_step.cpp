@@ -202,7 +202,7 @@ moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {
 // ------------------------------------------------------- router losses ------
 size_t moe_router_loss_workspace_size(int T, int E) {
   if (T < 0 || E < 1 || E > kMaxExperts) return 0;
-  return static_cast<size_t>(moe::router_loss_blocks(T, E)) * (8 + 8 * static_cast<size_t>(E));
+  return moe::router_loss_workspace_bytes(T, E);
 }
 
 moe_status moe_router_loss(const moe_router_loss_args* a, void* stream) {
@@ -212,7 +212,7 @@ moe_status moe_router_loss(const moe_router_loss_args* a, void* stream) {
       !std::isfinite(a->z_coef) || !a->counts || !a->n_tokens || !a->prob_mean || !a->loss)
     return MOE_ERR_INVALID_ARG;
   if (!a->workspace || a->workspace_bytes < moe_router_loss_workspace_size(a->T, a->E) ||
-      (reinterpret_cast<uintptr_t>(a->workspace) & 3))
+      (reinterpret_cast<uintptr_t>(a->workspace) & 7))
     return MOE_ERR_WORKSPACE;
   int cu = 0;
   if (moe_status st = moe::current_device(&cu)) return st;

@@ -164,7 +164,7 @@ hipError_t launch_fp8_rows(const Fp8Args& g, int tile_rows, bool f32, hipStream_
 hipError_t launch_fp8_wgrad(const Fp8Args& g, bool f32, int grid, hipStream_t s);
 
 // ---- router losses ----------------------------------------------------------
-int router_loss_blocks(int T, int E);   // workgroups of the loss kernel
+size_t router_loss_workspace_bytes(int T, int E);
 hipError_t launch_router_loss(const moe_router_loss_args& a, hipStream_t s);
 hipError_t launch_router_bwd(const moe_router_bwd_args& a, hipStream_t s);
 

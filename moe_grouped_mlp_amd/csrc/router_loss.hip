@@ -15,6 +15,7 @@
 // loss kernel keeps each lane's sums of p over its tokens in registers, adds
 // them over the workgroup in a fixed order and writes one fp32 partial per
 // expert and workgroup; a second launch of one workgroup adds these in fp64.
+// Bound by HBM for many tokens and by the two launches for few.
 #include <type_traits>
 
 #include "common.h"
@@ -39,6 +40,17 @@ MOE_DEV float group_sum(float v) {
 template <int L>
 MOE_DEV float group_max(float v) {
   return group_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// exp(x) for x <= 0 (or NaN), within 2 steps: x log2(e) in two parts, the
+// leading one through the hardware's exp2.  Below -200 it is 0.
+MOE_DEV float exp_neg(float x) {
+  x = x < -200.0f ? -200.0f : x;
+  constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925963033500011079e-8f;   // log2(e)
+  const float t = x * kHi;
+  const float r = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -t));   // what t left out
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, r * 0.693147182464599609375f, e);            // 2^r = 1 + r ln 2
 }
 
 // Expert of a lane's i-th logit.
@@ -79,7 +91,7 @@ MOE_DEV bool token_softmax(const float* __restrict__ row, int E, int g, float (&
   const float mm = m == kNegInf ? 0.0f : m;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    p[i] = expf(p[i] - mm);
+    p[i] = exp_neg(p[i] - mm);
     z += p[i];
     nan = p[i] != p[i] ? 1.0f : nan;
   }
@@ -92,22 +104,23 @@ MOE_DEV bool token_softmax(const float* __restrict__ row, int E, int g, float (&
   return true;
 }
 
-// Partials of one workgroup: prob [E], count [E], then {sum lse^2, n}.
+constexpr int kMaxLossBlocks = 256;   // workgroups of the loss kernel at most
+constexpr int kLossThreads = 1024;
+constexpr int kLossWaves = kLossThreads / kWave;
+
+// Partials of one workgroup: {sum of p, picks} per expert, {sum lse^2, n}.
 template <int L, bool VEC>
-__global__ __launch_bounds__(kThreads) void router_loss_kernel(
+__global__ __launch_bounds__(kLossThreads) void router_loss_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ idx,
-    const uint8_t* __restrict__ mask, int T, int E, int k, float* __restrict__ part_p,
-    int32_t* __restrict__ part_c, float* __restrict__ part_z, int32_t* __restrict__ part_n) {
-  constexpr int kTok = kThreads / L;   // tokens the workgroup covers at once
-  __shared__ float s_p[kMaxExperts];
-  __shared__ int32_t s_c[kMaxExperts];
-  __shared__ float s_z[kThreads / kWave];
-  __shared__ int32_t s_n[kThreads / kWave];
+    const uint8_t* __restrict__ mask, int T, int E, int k, float2* __restrict__ part,
+    float2* __restrict__ part_z, int32_t* done) {
+  constexpr int kTok = kLossThreads / L;   // tokens the workgroup covers at once
+  __shared__ float s_p[kLossWaves * L * kPer];   // the waves' sums, expert-major: at most 64 KB
+  __shared__ int32_t s_c[L * kPer];
+  __shared__ float s_z[kLossWaves];
+  __shared__ int32_t s_n[kLossWaves];
   const int tid = threadIdx.x, g = tid % L, wave = tid / kWave;
-  for (int e = tid; e < E; e += kThreads) {
-    s_p[e] = 0.0f;
-    s_c[e] = 0;
-  }
+  for (int e = tid; e < E; e += kLossThreads) s_c[e] = 0;
   __syncthreads();
   float sum[kPer] = {};
   float zsum = 0.0f;
@@ -132,7 +145,7 @@ __global__ __launch_bounds__(kThreads) void router_loss_kernel(
     }
   }
   // the lanes of a wave that hold the same experts (same g), then the waves
-  // one after the other
+  // in their order
 #pragma unroll
   for (int o = L; o < kWave; o <<= 1) {
 #pragma unroll
@@ -147,34 +160,33 @@ __global__ __launch_bounds__(kThreads) void router_loss_kernel(
     s_z[wave] = zsum;
     s_n[wave] = n;
   }
-  for (int w = 0; w < kThreads / kWave; ++w) {
-    if (wave == w && tid % kWave < L) {
+  if (tid % kWave < L) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int e = expert_at<L, VEC>(g, i);
-        if (e < E) s_p[e] += sum[i];
-      }
+    for (int i = 0; i < kPer; ++i) {
+      const int e = expert_at<L, VEC>(g, i);
+      if (e < E) s_p[wave * L * kPer + e] = sum[i];
     }
-    __syncthreads();
   }
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * E;
-  for (int e = tid; e < E; e += kThreads) {
-    part_p[at + e] = s_p[e];
-    part_c[at + e] = s_c[e];
+  __syncthreads();
+  for (int e = tid; e < E; e += kLossThreads) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kLossWaves; ++w) v += s_p[w * L * kPer + e];
+    part[static_cast<int64_t>(blockIdx.x) * E + e] = float2{v, __int_as_float(s_c[e])};
   }
   if (tid == 0) {
     float z = 0.0f;
     int32_t m = 0;
-    for (int w = 0; w < kThreads / kWave; ++w) {
+    for (int w = 0; w < kLossWaves; ++w) {
       z += s_z[w];
       m += s_n[w];
     }
-    part_z[blockIdx.x] = z;
-    part_n[blockIdx.x] = m;
+    part_z[blockIdx.x] = float2{z, __int_as_float(m)};
+    if (blockIdx.x == 0) *done = 0;
   }
 }
 
-constexpr int kSumThreads = 1024;
+constexpr int kSumExperts = 16;   // experts of a workgroup of the second launch
 
 MOE_DEV double sum_all(double v, double* s_wave) {
 #pragma unroll
@@ -183,53 +195,71 @@ MOE_DEV double sum_all(double v, double* s_wave) {
   if (threadIdx.x % kWave == 0) s_wave[threadIdx.x / kWave] = v;
   __syncthreads();
   double r = 0.0;
-  for (int i = 0; i < kSumThreads / kWave; ++i) r += s_wave[i];
+  for (int i = 0; i < kThreads / kWave; ++i) r += s_wave[i];
   return r;
 }
 
-// Adds the workgroups' partials: S threads share an expert (S the power of
-// two that fills the workgroup), each taking every S-th workgroup.
-__global__ __launch_bounds__(kSumThreads) void router_loss_sum_kernel(
-    const float* __restrict__ part_p, const int32_t* __restrict__ part_c,
-    const float* __restrict__ part_z, const int32_t* __restrict__ part_n, int blocks, int E, int k,
-    int S, float balance_coef, float z_coef, int32_t* __restrict__ counts,
-    int32_t* __restrict__ n_tokens, float* __restrict__ prob_mean, float* __restrict__ loss) {
-  __shared__ double s_wave[kSumThreads / kWave];
-  const int tid = threadIdx.x;
-  double z = 0.0, nd = 0.0;
-  for (int b = tid; b < blocks; b += kSumThreads) {
-    z += part_z[b];
-    nd += part_n[b];
+// Adds the workgroups' partials: 16 experts a workgroup, 16 threads each, all
+// loads of a thread in flight.  The last workgroup to end adds the balance
+// terms in their order; done was set to 0 by the first launch.
+__global__ __launch_bounds__(kThreads) void router_loss_sum_kernel(
+    const float2* __restrict__ part, const float2* __restrict__ part_z, int blocks, int E, int k,
+    float balance_coef, float z_coef, int32_t* __restrict__ counts, int32_t* __restrict__ n_tokens,
+    float* __restrict__ prob_mean, float* __restrict__ loss, int32_t* done, double* terms) {
+  __shared__ double s_wave[kThreads / kWave];
+  __shared__ double s_p[kThreads];
+  __shared__ int32_t s_c[kThreads];
+  __shared__ int s_last;
+  constexpr int kRows = kThreads / kSumExperts, U = kMaxLossBlocks / kRows;
+  const int tid = threadIdx.x, e = blockIdx.x * kSumExperts + tid % kSumExperts;
+  float2 v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int b = tid / kSumExperts + u * kRows;
+    v[u] = b < blocks && e < E ? part[static_cast<int64_t>(b) * E + e] : float2{0.0f, 0.0f};
   }
-  z = sum_all(z, s_wave);
-  nd = sum_all(nd, s_wave);   // an integer below 2^31: exact
-  const int sub = tid % S;
+  static_assert(kMaxLossBlocks == kThreads, "one partial a thread");
+  const float2 zn = tid < blocks ? part_z[tid] : float2{0.0f, 0.0f};
+  double p = 0.0;
+  int32_t c = 0;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    p += v[u].x;
+    c += __float_as_int(v[u].y);
+  }
+  s_p[tid] = p;
+  s_c[tid] = c;
+  const double z = sum_all(zn.x, s_wave);
+  const double nd = sum_all(__float_as_int(zn.y), s_wave);   // an integer below 2^31: exact
   double bal = 0.0;
-  for (int e0 = 0; e0 < E; e0 += kSumThreads / S) {
-    const int e = e0 + tid / S;
-    double p = 0.0;
-    int32_t c = 0;
-    if (e < E) {
-      for (int b = sub; b < blocks; b += S) {
-        p += part_p[static_cast<int64_t>(b) * E + e];
-        c += part_c[static_cast<int64_t>(b) * E + e];
-      }
+  if (tid < kSumExperts && e < E) {
+    p = 0.0;
+    c = 0;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      p += s_p[i * kSumExperts + tid];
+      c += s_c[i * kSumExperts + tid];
     }
-    for (int o = S / 2; o > 0; o >>= 1) {
-      p += __shfl_xor(p, o, kWave);
-      c += __shfl_xor(c, o, kWave);
-    }
-    if (e < E && sub == 0) {
-      const double mean = nd > 0.0 ? p / nd : 0.0;
-      counts[e] = c;
-      prob_mean[e] = static_cast<float>(mean);
-      bal += c * mean;
-    }
+    const double mean = nd > 0.0 ? p / nd : 0.0;
+    counts[e] = c;
+    prob_mean[e] = static_cast<float>(mean);
+    bal = c * mean;
   }
   bal = sum_all(bal, s_wave);
   if (tid == 0) {
+    __hip_atomic_store(&terms[blockIdx.x], bal, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int before = __hip_atomic_fetch_add(done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    s_last = before == static_cast<int>(gridDim.x) - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  const double t = tid < static_cast<int>(gridDim.x)
+                       ? __hip_atomic_load(&terms[tid], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                       : 0.0;
+  const double all = sum_all(t, s_wave);
+  if (tid == 0) {
     n_tokens[0] = static_cast<int32_t>(nd);
-    loss[0] = nd > 0.0 ? static_cast<float>(balance_coef * E * bal / (k * nd)) : 0.0f;
+    loss[0] = nd > 0.0 ? static_cast<float>(balance_coef * E * all / (k * nd)) : 0.0f;
     loss[1] = nd > 0.0 ? static_cast<float>(z_coef * z / nd) : 0.0f;
   }
 }
@@ -242,7 +272,13 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(
     const int32_t* __restrict__ n_tokens, int T, int E, int k, float balance_coef, float z_coef,
     float* __restrict__ dlogits) {
   constexpr int kTok = kThreads / L;
+  // the picks' gradients of a token, spread to the lanes of their experts
+  // through LDS: comparing every logit with every pick costs three times the
+  // rest of the kernel for 256 experts
+  constexpr bool kSpread = L >= kMaxTopK;
+  __shared__ __attribute__((aligned(16))) float s_d[kSpread ? kThreads * kPer : 4];
   const int tid = threadIdx.x, g = tid % L;
+  float* row_d = s_d + (kSpread ? tid / L * L * kPer : 0);
   const double n = n_tokens ? *n_tokens : 0;
   float cb[kPer] = {}, cz = 0.0f;   // the balance term of v, and 2 c_z / n
   if (n > 0.0) {
@@ -260,6 +296,17 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(
        t0 += static_cast<int64_t>(gridDim.x) * kTok) {
     const int64_t t = t0 + tid / L;
     if (t >= T) continue;   // whole groups: a token's lanes share t
+    // the picks: one a lane, or all in every lane of a small group
+    constexpr int kOwnPicks = L >= kMaxTopK ? 1 : kMaxTopK;
+    int32_t pe[kOwnPicks];
+    float pd[kOwnPicks];
+#pragma unroll
+    for (int s = 0; s < kOwnPicks; ++s) {
+      const int at = L >= kMaxTopK ? g : s;
+      const bool in = dprobs && at < k;
+      pe[s] = in ? idx[t * k + at] : -1;
+      pd[s] = in ? dprobs[t * k + at] : 0.0f;
+    }
     float p[kPer], lse = 0.0f;
     const bool any = token_softmax<L, VEC>(logits + t * E, E, g, p, lse);
     const bool kept = any && (!mask || mask[t]);
@@ -267,11 +314,40 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(
 #pragma unroll
     for (int i = 0; i < kPer; ++i) v[i] = kept ? cb[i] : 0.0f;
     if (dprobs) {
-      for (int s = 0; s < k; ++s) {
-        const int32_t e = idx[t * k + s];
-        const float d = dprobs[t * k + s];
+      if constexpr (kSpread) {
+        // lane s < k: the sum over the slots with its expert, written by the
+        // first of them (one wave: LDS operations complete in order)
+        float4* row4 = reinterpret_cast<float4*>(row_d);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] += expert_at<L, VEC>(g, i) == e ? d : 0.0f;
+        for (int q = 0; q < kPer / 4; ++q) row4[g + L * q] = float4{0.0f, 0.0f, 0.0f, 0.0f};
+        float d = 0.0f;
+        bool first = pe[0] >= 0 && pe[0] < E;
+#pragma unroll
+        for (int s = 0; s < kMaxTopK; ++s) {
+          const int32_t e = __shfl(pe[0], s, L);
+          const float ds = __shfl(pd[0], s, L);
+          if (e == pe[0]) {
+            d += ds;
+            first = first && s >= g;
+          }
+        }
+        asm volatile("" ::: "memory");
+        if (first) row_d[pe[0]] = d;
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) v[i] += row_d[expert_at<L, VEC>(g, i)];
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+      } else {
+#pragma unroll
+        for (int s = 0; s < kMaxTopK; ++s) {
+          if (s < k) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              v[i] += expert_at<L, VEC>(g, i) == pe[s % kOwnPicks] ? pd[s % kOwnPicks] : 0.0f;
+          }
+        }
       }
     }
     float dot = 0.0f;
@@ -319,28 +395,34 @@ void with_lanes(int E, bool vec, F&& f) {
 
 // Workgroups of the loss kernel: one per pass of tokens, at most 256 (their
 // partials are what the second launch reads).
-int router_loss_blocks(int T, int E) {
-  const int tok = kThreads / lanes_of(E);
+static int loss_blocks(int T, int E) {
+  const int tok = kLossThreads / lanes_of(E);
   const int64_t b = (static_cast<int64_t>(T) + tok - 1) / tok;
-  return static_cast<int>(b < 1 ? 1 : b > 256 ? 256 : b);
+  return static_cast<int>(b < 1 ? 1 : b > kMaxLossBlocks ? kMaxLossBlocks : b);
+}
+static int sum_blocks(int E) { return (E + kSumExperts - 1) / kSumExperts; }
+
+// Workspace: the balance terms (fp64), the counter, {sum lse^2, n} and the
+// experts' partials of every workgroup.
+size_t router_loss_workspace_bytes(int T, int E) {
+  const size_t blocks = loss_blocks(T, E);
+  return 8 * (sum_blocks(E) + 1 + blocks + blocks * static_cast<size_t>(E));
 }
 
 hipError_t launch_router_loss(const moe_router_loss_args& a, hipStream_t s) {
-  const int blocks = router_loss_blocks(a.T, a.E);
-  float* part_z = static_cast<float*>(a.workspace);
-  int32_t* part_n = reinterpret_cast<int32_t*>(part_z + blocks);
-  float* part_p = reinterpret_cast<float*>(part_n + blocks);
-  int32_t* part_c = reinterpret_cast<int32_t*>(part_p + static_cast<int64_t>(blocks) * a.E);
+  const int blocks = loss_blocks(a.T, a.E), blocks2 = sum_blocks(a.E);
+  double* terms = static_cast<double*>(a.workspace);
+  int32_t* done = reinterpret_cast<int32_t*>(terms + blocks2);
+  float2* part_z = reinterpret_cast<float2*>(terms + blocks2 + 1);
+  float2* part = part_z + blocks;
   with_lanes(a.E, rows_vec(a.logits, a.E), [&](auto l, auto vec) {
-    router_loss_kernel<decltype(l)::value, decltype(vec)::value><<<blocks, kThreads, 0, s>>>(
-        a.logits, a.expert_idx, a.token_mask, a.T, a.E, a.k, part_p, part_c, part_z, part_n);
+    router_loss_kernel<decltype(l)::value, decltype(vec)::value><<<blocks, kLossThreads, 0, s>>>(
+        a.logits, a.expert_idx, a.token_mask, a.T, a.E, a.k, part, part_z, done);
   });
   if (hipError_t e = hipGetLastError()) return e;
-  int S = 1;
-  while (S < 64 && 2 * S * a.E <= kSumThreads) S *= 2;
-  router_loss_sum_kernel<<<1, kSumThreads, 0, s>>>(part_p, part_c, part_z, part_n, blocks, a.E, a.k,
-                                                   S, a.balance_coef, a.z_coef, a.counts,
-                                                   a.n_tokens, a.prob_mean, a.loss);
+  router_loss_sum_kernel<<<blocks2, kThreads, 0, s>>>(part, part_z, blocks, a.E, a.k,
+                                                      a.balance_coef, a.z_coef, a.counts, a.n_tokens,
+                                                      a.prob_mean, a.loss, done, terms);
   return hipGetLastError();
 }
 
