@@ -6,8 +6,10 @@ The functions only marshal arguments; all work runs in the HIP kernels.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import math
+import operator
 import os
 from ctypes import c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 
@@ -560,14 +562,16 @@ def _buf(fn, name, t, dtypes, n, dev):
 
 
 _F32 = None
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _setup():
     import torch
-    global _F32, _BF16, _U8, _I32, _F64, _CODES, _MASK, _GRADS, _current_device, _raw_stream
+    global _F32, _BF16, _U8, _I32, _F64, _CODES, _MASK, _GRADS, _Tensor, _current_device, _raw_stream
     _BF16, _U8, _I32 = (torch.bfloat16,), (torch.uint8,), (torch.int32,)
     _F64, _CODES, _MASK = (torch.float64,), (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.bool)
     _GRADS = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
+    _Tensor = torch.Tensor
     _current_device = torch.cuda.current_device
     # the current stream's handle without the Stream object around it
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -683,26 +687,31 @@ def moe_grad_workspace_size(n_tensors) -> int:
 
 
 def _tensor_list(fn, tensors, out, dev):
-    """The host array of moe_tensor (four 8-byte words each: data, out, numel,
-    type)."""
-    if out is None:
-        out = (None,) * len(tensors)
-    elif len(out) != len(tensors):
-        raise ValueError(f"{fn}: out must have as many tensors as the list")
-    words = []
-    for t, o in zip(tensors, out):
-        dt = getattr(t, "dtype", None)
-        if dt not in _GRADS:
-            raise ValueError(f"{fn}: tensor {len(words) // 4} must be a bfloat16 or float32 tensor")
-        n = t.numel()
-        if o is not None and (o.dtype is not dt or o.numel() != n):
-            raise ValueError(f"{fn}: out {len(words) // 4} must have its tensor's type and size")
-        if (t.get_device() != dev or not t.is_contiguous()
-                or o is not None and (o.get_device() != dev or not o.is_contiguous())):
-            raise ValueError(f"{fn}: tensor {len(words) // 4} and its out must be contiguous and "
-                             f"on the current device (cuda:{dev})")
-        words += (t.data_ptr(), 0 if o is None else o.data_ptr(), n, _GRADS[dt])
-    return ctypes.cast((c_int64 * max(1, len(words)))(*words), ctypes.POINTER(Tensor))
+    """The host array of moe_tensor: four 8-byte words each (data, out, numel,
+    type), filled column by column, as lists may be long."""
+    T, n = _Tensor, len(tensors)
+    try:
+        types = [_GRADS.get(d) for d in map(_dtype_of, tensors)]
+        if None in types:
+            raise ValueError(f"{fn}: tensor {types.index(None)} must be bfloat16 or float32")
+        numels = list(map(T.numel, tensors))
+        every = tensors
+        words = array.array("q", bytes(32 * max(1, n)))
+        if out is not None:
+            if (len(out) != n or list(map(_dtype_of, out)) != list(map(_dtype_of, tensors))
+                    or list(map(T.numel, out)) != numels):
+                raise ValueError(f"{fn}: out must have a tensor of each one's type and size")
+            words[1:4 * n:4] = array.array("q", map(T.data_ptr, out))
+            every = [*tensors, *out]
+        if not all(map(T.is_contiguous, every)) or any(map(dev.__ne__, map(T.get_device, every))):
+            raise ValueError(f"{fn}: the tensors must be contiguous and on the current device "
+                             f"(cuda:{dev})")
+        words[0:4 * n:4] = array.array("q", map(T.data_ptr, tensors))
+        words[2:4 * n:4] = array.array("q", numels)
+        words[3:4 * n:4] = array.array("q", types)
+    except (AttributeError, TypeError):
+        raise ValueError(f"{fn}: a list of tensors is needed") from None
+    return ctypes.cast((c_int64 * len(words)).from_buffer(words), ctypes.POINTER(Tensor))
 
 
 def moe_grad_sumsq(*, tensors, sumsq, workspace, stream=None):
