@@ -812,9 +812,12 @@ moe_status moe_quantize_fp8(const moe_quant_fp8_args* args, void* stream);
  *   max_rows: the most rows any group can hold if the caller knows it (a
  *   decoding step of T tokens: T), 0 if not.  It chooses among kernels;
  *   groups that turn out larger are computed all the same.
- *   workspace: optional, moe_grouped_gemm_fp8_workspace_size(...) bytes; its
- *   contents need no initialisation and calls that overlap in time must
- *   not share one.  Without it the last round of tiles is not split. */
+ *   workspace: optional, moe_grouped_gemm_fp8_workspace_size(...) bytes (0:
+ *   none would be used; a smaller one is not used), 16-byte aligned, no initialisation; calls that overlap in time must not
+ *   share one.  With it a product of so few tiles that they would leave more
+ *   than half of the device idle is cut along K, its parts added in a fixed
+ *   order: the same call gives the same bits, one without workspace sums in
+ *   another order. */
 typedef struct moe_gemm_fp8_args {
   int32_t E, N, K;
   int64_t M_cap;
@@ -889,8 +892,8 @@ moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* args, void* stream);
  *   zeros.  Sums over tokens are made in a fixed order (fp32 inside a
  *   workgroup, fp64 over workgroups): the same inputs give the same bits.
  *   Needs 0 <= T, 1 <= E <= 1024, 1 <= k <= min(E, 8), T * k < 2^31;
- *   workspace of moe_router_loss_workspace_size(T, E) bytes, no
- *   initialisation.
+ *   workspace of moe_router_loss_workspace_size(T, E) bytes, 8-byte aligned,
+ *   no initialisation; calls that overlap in time must not share one.
  *   Several processes: sum counts and n_tokens over them (and prob_mean
  *   weighted by n_tokens) before moe_router_bwd, whose gradients are then
  *   those of the joint loss. */
@@ -952,7 +955,8 @@ moe_status moe_router_bwd(const moe_router_bwd_args* args, void* stream);
  *   contiguous, aligned to its type, numel >= 0.  moe_grad_clip refuses
  *   lists in which a tensor to be written overlaps another one (the same
  *   tensor twice, say): MOE_ERR_INVALID_ARG.
- *   workspace: moe_grad_workspace_size(n_tensors) bytes, no initialisation.
+ *   workspace: moe_grad_workspace_size(n_tensors) bytes, 8-byte aligned, no
+ *   initialisation; calls that overlap in time must not share one.
  * ---------------------------------------------------------------------- */
 typedef struct moe_tensor {
   void* data;                     /* device */

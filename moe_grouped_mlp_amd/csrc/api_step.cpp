@@ -35,6 +35,15 @@ int tile_grid(int cu, int margin, int64_t tiles) {
   return g < 1 ? 1 : g;
 }
 
+// Whether the product may cut K: rows that take the tiled kernel, 24 scale
+// blocks at least, and a row buffer (less a group's padding each) that cannot
+// fill the device with tiles.  The second launch costs 7 us also where nothing
+// was cut (E=22 N=352 K=2080, 34 tiles of few rows: 14 us without it, 21 with).
+bool cuts_k(int E, int N, int K, int64_t M_cap, int64_t most_rows, int cu) {
+  const int64_t rows = std::max<int64_t>(1, M_cap - static_cast<int64_t>(E) * (MOE_GROUP_ALIGN - 1));
+  return most_rows > 32 && K > 23 * kBlk && ceil_div(rows, 256) * ceil_div(N, kTileN) < cu;
+}
+
 struct Range {
   uintptr_t lo, hi;
   bool write;
@@ -115,20 +124,21 @@ moe_status moe_quantize_fp8(const moe_quant_fp8_args* a, void* stream) {
   return launched(moe::launch_quantize_fp8(b, static_cast<hipStream_t>(stream)));
 }
 
+// One tile's fp32 sums for every workgroup of a full grid; nothing where K is
+// too short to be cut or the kernel for few rows runs, which needs none.
 size_t moe_grouped_gemm_fp8_workspace_size(int E, int N, int K, int64_t M_cap, int max_rows) {
-  (void)E;
-  (void)N;
-  (void)K;
-  (void)M_cap;
-  (void)max_rows;
-  return 0;
+  if (E < 1 || N < 1 || K < 1 || M_cap < 1 || max_rows < 0) return 0;
+  int cu = 0;
+  if (moe::current_device(&cu) != MOE_OK) cu = 256;
+  if (!cuts_k(E, N, K, M_cap, max_rows ? std::min<int64_t>(max_rows, M_cap) : M_cap, cu)) return 0;
+  return static_cast<size_t>(cu) * moe::kFp8PartFloats * sizeof(float);
 }
 
 moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
   if (!a || a->E < 1 || a->E > kMaxExperts || a->N < 16 || a->N % 16 != 0 || a->K < 16 ||
       a->K % 16 != 0 || a->K > (1 << 22) || a->M_cap < 1 || a->M_cap > INT32_MAX ||
       !a->split_sizes || !a->padded_offsets || !a->a || !a->a_s || !a->b || !a->b_s || !a->c ||
-      !type_ok(a->c_type) || a->max_rows < 0 || a->cu_margin < 0 || !aligned16(a->a) ||
+      !type_ok(a->c_type) || !aligned16(a->workspace) || a->max_rows < 0 || a->cu_margin < 0 || !aligned16(a->a) ||
       !aligned16(a->b) || !aligned16(a->c))
     return MOE_ERR_INVALID_ARG;
   const int64_t nk = static_cast<int64_t>(a->N) * a->K;
@@ -163,7 +173,14 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
   g.err = a->err_flag;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   if (most <= 32) return launched(moe::launch_fp8_rows(g, most <= 16 ? 16 : 32, f32, s));
-  return launched(moe::launch_fp8_gemm(g, f32, tile_grid(cu, a->cu_margin, tiles), s));
+  // K may be cut where there is room for its parts; the grid is a full one
+  // then, since the tiles' number is known on the device only
+  const int full = tile_grid(cu, a->cu_margin, INT32_MAX);
+  const bool cut = cuts_k(a->E, a->N, a->K, a->M_cap, most, cu) && a->workspace &&
+                   a->workspace_bytes >= static_cast<size_t>(full) * moe::kFp8PartFloats * sizeof(float);
+  if (cut) g.part = static_cast<moe::fp8_f32x4*>(a->workspace);
+  const int grid = cut ? full : tile_grid(cu, a->cu_margin, tiles);
+  return launched(moe::launch_fp8_gemm(g, f32, grid, s));
 }
 
 moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {

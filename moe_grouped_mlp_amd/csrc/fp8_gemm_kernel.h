@@ -198,6 +198,113 @@ struct Fp8Loader {
   }
 };
 
+// The tiles of all experts in their order, from the sizes on the device.
+struct Fp8Tables {
+  int start[kMaxExperts + 1];   // an expert's first tile
+  int rows[kMaxExperts];
+  int tmp[kFp8Waves];
+};
+template <int BT, bool WG>
+MOE_DEV int fp8_tile_prefix(const Fp8Args& g, Fp8Tables& s) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tiles_n = (g.N + kFp8BN - 1) / kFp8BN;
+  auto tiles_of = [&](int rows) { return (WG ? (g.P + BT - 1) / BT : (rows + BT - 1) / BT) * tiles_n; };
+  const int per = (g.E + kFp8Threads - 1) / kFp8Threads;   // 1 or 2
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    if (e < g.E) {
+      bool bad;
+      const int n = fp8_group_rows(g, e, WG, bad);
+      if (bad && blockIdx.x == 0) set_err(g.err, MOE_DEVERR_BAD_OFFSETS);
+      s.rows[e] = n;
+      mine += tiles_of(n);
+    }
+  }
+  int inc = mine;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int v = __shfl_up(inc, o, kWave);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 63) s.tmp[wave] = inc;
+  __syncthreads();
+  int run = inc - mine, total = 0;
+  for (int w = 0; w < kFp8Waves; ++w) {
+    if (w < wave) run += s.tmp[w];
+    total += s.tmp[w];
+  }
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    if (e < g.E) {
+      s.start[e] = run;
+      run += tiles_of(s.rows[e]);
+    }
+  }
+  if (tid == 0) s.start[g.E] = total;
+  __syncthreads();
+  return __builtin_amdgcn_readfirstlane(total);
+}
+
+struct Fp8Tile {
+  int e, n_e, start;   // the expert, its rows and the first of them
+  int rows_t, t0, n0;  // token rows of the expert; the tile's first token and weight row
+};
+template <int BT, bool WG>
+MOE_DEV Fp8Tile fp8_tile_at(const Fp8Args& g, const Fp8Tables& s, int id) {
+  int lo = 0, hi = g.E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s.start[mid] <= id) lo = mid; else hi = mid - 1;
+  }
+  Fp8Tile t;
+  t.e = __builtin_amdgcn_readfirstlane(lo);
+  const int in_e = __builtin_amdgcn_readfirstlane(id - s.start[lo]);
+  t.n_e = __builtin_amdgcn_readfirstlane(s.rows[lo]);
+  t.start = __builtin_amdgcn_readfirstlane(g.padded[lo]);
+  t.rows_t = WG ? g.P : t.n_e;
+  // bands of group_m token tiles, all weight tiles of a band in turn
+  const int tiles_n = (g.N + kFp8BN - 1) / kFp8BN;
+  const int tiles_t = (t.rows_t + BT - 1) / BT;
+  const int band = in_e / (g.group_m * tiles_n), in_b = in_e - band * g.group_m * tiles_n;
+  const int gm = tiles_t - band * g.group_m < g.group_m ? tiles_t - band * g.group_m : g.group_m;
+  t.t0 = (band * g.group_m + in_b % gm) * BT;
+  t.n0 = in_b / gm * kFp8BN;
+  return t;
+}
+// 64-token groups a tile with this many rows left runs with.
+template <int JMAX>
+MOE_DEV int fp8_tile_groups(int rows) {
+  const int n = (rows + 63) / 64;
+  return n < JMAX ? n : JMAX;
+}
+// Parts that K is cut into.  A step takes a tile 1.5 us; a part's sums, 256 KB,
+// cost 0.09 us of the device's time to write and read again, and the second
+// launch about 9 us.  So the best number is near sqrt(16 steps / tiles) (of
+// four steps each at least, and as many workgroups as there are), and it has
+// to save more steps than it costs.  E=2 N=112 K=4736: 50 us uncut, 28 cut
+// into 9; E=4 N=656 K=1168 (31 tiles, 10 steps): 23 us uncut, 41 cut into 2.
+MOE_DEV int fp8_parts(const Fp8Args& g, int total, int workgroups) {
+  if (!g.part || total < 1) return 1;
+  const int steps = (g.K + kFp8Blk - 1) / kFp8Blk;
+  const int room = workgroups / total;
+  int n = steps / 4 < room ? steps / 4 : room;
+  while (n > 1 && static_cast<int64_t>(n) * n * total > 16 * static_cast<int64_t>(steps)) --n;
+  return n > 1 && steps - steps / n >= 6 + total * n / 16 ? n : 1;
+}
+// Place of a workgroup in the order of tiles: contiguous runs for each XCD
+// (workgroup ids go round the XCDs).
+MOE_DEV int fp8_workgroup() {
+  const int G = gridDim.x;
+  if (G % kNumXcd != 0) return blockIdx.x;
+  return (blockIdx.x % kNumXcd) * (G / kNumXcd) + blockIdx.x / kNumXcd;
+}
+// Column of weight tile i's MFMA row 0 in its 64 columns.
+template <bool F32>
+MOE_DEV constexpr int fp8_w_off(int i) {
+  return F32 ? 16 * (i % 4) : 32 * (i % 4 / 2) + 4 * (i % 2);
+}
+
 // JMAX: MFMA token tiles per wave; WG: the weight gradient; F32: fp32 output,
 // summed from widened operands.
 template <int JMAX, bool WG, bool F32>
@@ -217,75 +324,23 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
     using F = std::conditional_t<std::is_const_v<std::remove_pointer_t<decltype(sWb)>>, const float, float>;
     return reinterpret_cast<F*>(sWb + kHalfW);
   };
-  __shared__ int s_start[kMaxExperts + 1], s_rows[kMaxExperts], s_tmp[kFp8Waves];
+  __shared__ Fp8Tables s_tab;
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, wave = tid >> 6;
   const int wave_s = __builtin_amdgcn_readfirstlane(wave);
   const int wn = wave & 1, wt = wave >> 1;
-  const int tiles_n = (g.N + kFp8BN - 1) / kFp8BN;
+  const int total = fp8_tile_prefix<BT, WG>(g, s_tab);
+  const int parts = WG ? 1 : fp8_parts(g, total, gridDim.x);
 
-  // ---- tile prefix over the experts ----
-  auto tiles_of = [&](int rows) { return (WG ? (g.P + BT - 1) / BT : (rows + BT - 1) / BT) * tiles_n; };
-  {
-    const int per = (g.E + kFp8Threads - 1) / kFp8Threads;   // 1 or 2
-    int mine = 0;
-    for (int i = 0; i < per; ++i) {
-      const int e = tid * per + i;
-      if (e < g.E) {
-        bool bad;
-        const int n = fp8_group_rows(g, e, WG, bad);
-        if (bad && blockIdx.x == 0) set_err(g.err, MOE_DEVERR_BAD_OFFSETS);
-        s_rows[e] = n;
-        mine += tiles_of(n);
-      }
-    }
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-      const int v = __shfl_up(inc, o, kWave);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 63) s_tmp[wave] = inc;
-    __syncthreads();
-    int run = inc - mine, total = 0;
-    for (int w = 0; w < kFp8Waves; ++w) {
-      if (w < wave) run += s_tmp[w];
-      total += s_tmp[w];
-    }
-    for (int i = 0; i < per; ++i) {
-      const int e = tid * per + i;
-      if (e < g.E) {
-        s_start[e] = run;
-        run += tiles_of(s_rows[e]);
-      }
-    }
-    if (tid == 0) s_start[g.E] = total;
-    __syncthreads();
-  }
-  const int total = s_start[g.E];
-
-  // contiguous runs of tiles for each XCD (workgroup ids go round the XCDs)
-  const int G = gridDim.x;
-  int vid = blockIdx.x;
-  if (G % kNumXcd == 0) vid = (blockIdx.x % kNumXcd) * (G / kNumXcd) + blockIdx.x / kNumXcd;
-
-  for (int id = vid; id < total; id += G) {
-    int lo = 0, hi = g.E - 1;   // the expert of the tile
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_start[mid] <= id) lo = mid; else hi = mid - 1;
-    }
-    const int e = __builtin_amdgcn_readfirstlane(lo);
-    const int in_e = __builtin_amdgcn_readfirstlane(id - s_start[lo]);
-    const int n_e = __builtin_amdgcn_readfirstlane(s_rows[lo]);
-    const int start = __builtin_amdgcn_readfirstlane(g.padded[lo]);
-    const int rows_t = WG ? g.P : n_e;   // token rows of the expert
-    // bands of group_m token tiles, all weight tiles of a band in turn
-    const int tiles_t = (rows_t + BT - 1) / BT;
-    const int band = in_e / (g.group_m * tiles_n), in_b = in_e - band * g.group_m * tiles_n;
-    const int gm = tiles_t - band * g.group_m < g.group_m ? tiles_t - band * g.group_m : g.group_m;
-    const int m_b = in_b % gm, t_n = in_b / gm;
-    const int t0 = (band * g.group_m + m_b) * BT, n0 = t_n * kFp8BN;
+  for (int item = fp8_workgroup(); item < total * parts; item += gridDim.x) {
+    const Fp8Tile tile = fp8_tile_at<BT, WG>(g, s_tab, item / parts);
+    const int e = tile.e, n_e = tile.n_e, start = tile.start, rows_t = tile.rows_t, t0 = tile.t0, n0 = tile.n0;
+    // the steps [k0, k1) of this part
+    const int all_K = WG ? (n_e + kFp8Blk - 1) / kFp8Blk * kFp8Blk : g.K;
+    const int all_steps = (all_K + kFp8Blk - 1) / kFp8Blk;
+    const int part = item % parts;
+    const int k0 = parts > 1 ? static_cast<int>(static_cast<int64_t>(all_steps) * part / parts) : 0;
+    const int k1 = parts > 1 ? static_cast<int>(static_cast<int64_t>(all_steps) * (part + 1) / parts) : all_steps;
 
     // The tile with 64 JT tokens, JT the least that covers its rows: the last
     // rows of a group cost what they are, not a whole tile.
@@ -299,16 +354,15 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
       // and + w_off(i)
       const int l16 = lane & 15, g4 = lane >> 4;
       const int t_row = 16 * J * wt + l16, w_row = 64 * wn + (F32 ? l16 : 8 * (l16 >> 2) + (l16 & 3));
-      auto w_off = [](int i) { return F32 ? 16 * (i % 4) : 32 * (i % 4 / 2) + 4 * (i % 2); };
+      auto w_off = [](int i) { return fp8_w_off<F32>(i); };
       const int t_sw = fp8_swz_t(l16), w_sw = fp8_swz_w<F32>(w_row);
-      const int K = WG ? (n_e + kFp8Blk - 1) / kFp8Blk * kFp8Blk : g.K;
-      const int steps = (K + kFp8Blk - 1) / kFp8Blk;
+      const int steps = k1 - k0, K = (k1 < all_steps ? k1 * kFp8Blk : all_K) - k0 * kFp8Blk;
       const int rows_a = rows_t - t0, rows_b = g.N - n0;
       Fp8Loader<BT, false, F32> lt;
       Fp8Loader<kFp8BN, true, F32> lw;
-      const uint8_t* b_e = static_cast<const uint8_t*>(g.b) + (WG ? start : e * g.b_stride);
+      const uint8_t* b_e = static_cast<const uint8_t*>(g.b) + (WG ? start : e * g.b_stride) + k0 * kFp8Blk;
       lt.init(g.a + (WG ? static_cast<int64_t>(t0) * g.M_cap + start
-                        : static_cast<int64_t>(start + t0) * g.K),
+                        : static_cast<int64_t>(start + t0) * g.K) + k0 * kFp8Blk,
               rows_a, WG ? g.M_cap : g.K, K, wave_s, lane);
       const int64_t ld_b = WG ? g.M_cap : g.K;
       lw.init(b_e + n0 * ld_b, rows_b, ld_b, K, wave_s, lane);
@@ -327,10 +381,11 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
         s_step = g.N;
         if (s_i < rows_b) s_voff = 4 * s_i;
       } else {
-        s_base = g.b_s + e * g.b_s_stride + static_cast<int64_t>(n0 / kFp8Blk) * steps;
+        s_base = g.b_s + e * g.b_s_stride + static_cast<int64_t>(n0 / kFp8Blk) * all_steps;
         s_step = 1;
-        if (s_i < 2 && s_i * kFp8Blk < rows_b) s_voff = 4 * s_i * steps;
+        if (s_i < 2 && s_i * kFp8Blk < rows_b) s_voff = 4 * s_i * all_steps;
       }
+      s_base += k0 * s_step;
       // A stage's loads in the order they go out: the tokens and the weights of
       // tiles 0 .. 3 (early: their room is free half a step before the rest's),
       // the other weights, the scales.  Each is issued by itself between two
@@ -474,6 +529,17 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
         asm volatile("" ::: "memory");
       }
 
+      if constexpr (!WG) {
+        if (parts > 1) {   // the accumulators as they are, for fp8_join_kernel
+          f32x4* out = g.part + static_cast<int64_t>(item) * kFp8PartFloats / 4 + tid;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < J; ++j) out[(i * J + j) * kFp8Threads] = acc[i][j];
+          return;
+        }
+      }
+
       // ---- store ----
       // Straight from the accumulators a store would cover 64 bytes of 16 rows.
       // Instead each wave passes its outputs, 16 tokens (4 or 8 KB) at a time,
@@ -539,15 +605,55 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
     };
-    const int groups = (rows_t - t0 + 63) / 64;   // of 64 tokens
+    const int groups = fp8_tile_groups<JMAX>(rows_t - t0);
     if constexpr (JMAX == 4) {
-      if (groups >= 4) run(std::integral_constant<int, 4>{});
+      if (groups == 4) run(std::integral_constant<int, 4>{});
       else if (groups == 3) run(std::integral_constant<int, 3>{});
       else if (groups == 2) run(std::integral_constant<int, 2>{});
       else run(std::integral_constant<int, 1>{});
     } else {
-      if (groups >= 2) run(std::integral_constant<int, 2>{});
+      if (groups == 2) run(std::integral_constant<int, 2>{});
       else run(std::integral_constant<int, 1>{});
+    }
+  }
+}
+
+// Second launch where fp8_gemm_kernel may have cut K: adds a tile's parts in
+// their order and stores it.  Workgroup q of a tile takes every parts-th
+// accumulator (bf16: pair of weight tiles, whose outputs are neighbours).
+template <int JMAX, bool F32>
+__global__ __launch_bounds__(kFp8Threads) void fp8_join_kernel(const Fp8Args g, int workgroups) {
+  constexpr int BT = 64 * JMAX, kStep = F32 ? 1 : 2;
+  __shared__ Fp8Tables s_tab;
+  const int total = fp8_tile_prefix<BT, false>(g, s_tab);
+  const int parts = fp8_parts(g, total, workgroups);
+  const int item = blockIdx.x;
+  if (parts == 1 || item >= total * parts) return;
+  const Fp8Tile tile = fp8_tile_at<BT, false>(g, s_tab, item / parts);
+  const int J = fp8_tile_groups<JMAX>(tile.rows_t - tile.t0);
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wn = wave & 1, wt = wave >> 1, l16 = lane & 15, g4 = lane >> 4;
+  const f32x4* in = g.part + static_cast<int64_t>(item / parts) * parts * (kFp8PartFloats / 4) + tid;
+  for (int f = item % parts; f < 8 / kStep * J; f += parts) {
+    const int i = f / J * kStep, j = f % J;
+    const int tok = 16 * J * wt + 16 * j + l16;
+    const int n = tile.n0 + 128 * wn + 64 * (i / 4) + fp8_w_off<F32>(i) + (F32 ? 4 : 8) * g4;
+    f32x4 v[kStep];
+#pragma unroll
+    for (int u = 0; u < kStep; ++u) v[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = 0; p < parts; ++p) {
+#pragma unroll
+      for (int u = 0; u < kStep; ++u)
+        v[u] += in[static_cast<int64_t>(p) * (kFp8PartFloats / 4) + ((i + u) * J + j) * kFp8Threads];
+    }
+    if (tile.t0 + tok >= tile.rows_t || n >= g.N) continue;
+    const int64_t at = (static_cast<int64_t>(tile.start) + tile.t0 + tok) * g.ldc + n;
+    if constexpr (F32) {
+      *reinterpret_cast<f32x4*>(static_cast<float*>(g.c) + at) = v[0];
+    } else {
+      *reinterpret_cast<fp8_u32x4*>(static_cast<uint16_t*>(g.c) + at) =
+          fp8_u32x4{pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]),
+                    pack_bf16x2(v[1][0], v[1][1]), pack_bf16x2(v[1][2], v[1][3])};
     }
   }
 }

@@ -136,6 +136,8 @@ hipError_t launch_dprobs_reduce(const float* part, int n_part, const int32_t* sp
 // ---- block-scaled FP8 -----------------------------------------------------
 hipError_t launch_quantize_fp8(const moe_quant_fp8_args& a, hipStream_t s);
 
+typedef float fp8_f32x4 __attribute__((ext_vector_type(4)));
+
 // A grouped product: tokens a (rows of the groups) against weights b.  The
 // weight gradient takes the same kernel with the transposed copies: tokens
 // are a's P rows, weights b's N = Q rows, K the group's routed rows.
@@ -155,9 +157,12 @@ struct Fp8Args {
   int accumulate;          // weight gradient, fp32: C +=
   int group_m;             // token tiles per band of the tile order
   int32_t* err;            // nullable
+  fp8_f32x4* part;         // product (nullable): one tile's fp32 sums per workgroup
 };
+constexpr int kFp8PartFloats = 256 * 256;
 // tiles of fp8_tile_tokens(f32) tokens x 256 weight rows
 inline int fp8_tile_tokens(bool f32) { return f32 ? 128 : 256; }
+// with g.part also the launch that joins the parts of tiles whose K was cut
 hipError_t launch_fp8_gemm(const Fp8Args& g, bool f32, int grid, hipStream_t s);
 // groups of few rows; tile_rows: 16 or 32 tokens at a time
 hipError_t launch_fp8_rows(const Fp8Args& g, int tile_rows, bool f32, hipStream_t s);

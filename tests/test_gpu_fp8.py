@@ -406,6 +406,36 @@ def test_product_same_bits_again_without_workspace_and_on_another_stream(hint):
     assert torch.equal(c, d)
 
 
+@pytest.mark.parametrize("c_type", [mg.TYPE_F32, mg.TYPE_BF16])
+@pytest.mark.parametrize("sizes,N,K", [([100], 48, 4112), ([33, 0, 260, 1], 272, 3152), ([200, 600], 528, 5136),
+                                       ([64], 1040, 16400)])
+def test_product_cut_along_k(sizes, N, K, c_type):
+    """Few tiles and a long K: with a workspace K is cut and the parts are
+    joined, without it is not; exact on integers, twice the same bits, and a
+    workspace that is too small changes nothing."""
+    rng = np.random.default_rng(N)
+    starts = _starts(sizes)
+    ops = _operands(rng, sizes, starts, starts[-1], N, K, exact=True)
+    # one scale for all, and so few bits that every sum is exact
+    ops = (nu.e4m3_encode(np.clip(np.nan_to_num(nu.e4m3_decode(ops[0])), -3, 3)), np.ones_like(ops[1]),
+           nu.e4m3_encode(np.clip(nu.e4m3_decode(ops[2]), -3, 3)), np.ones_like(ops[3]))
+    ref, _ = _reference(*ops, sizes, starts)
+    routed = ~np.isnan(ref)
+    want = ref[routed] if c_type == mg.TYPE_F32 else nu.round_bf16(ref[routed])
+    assert mg.moe_grouped_gemm_fp8_workspace_size(len(sizes), N, K, starts[-1], 0) > 0
+    got = [_product(*ops, sizes, starts, c_type) for _ in range(2)] + [_product(*ops, sizes, starts, c_type, workspace=False)]
+    for c in got:
+        assert torch.equal(c, got[0])   # exact sums: any order gives them
+        c = c.double().cpu().numpy()
+        np.testing.assert_array_equal(c[routed], want)
+        assert (c[~routed] == -77.0).all()
+    ops = _operands(rng, sizes, starts, starts[-1], N, K)
+    ref, mag = _reference(*ops, sizes, starts)
+    c = _product(*ops, sizes, starts, c_type)
+    _check(c, ref, mag, K, c_type == mg.TYPE_BF16)
+    assert torch.equal(c, _product(*ops, sizes, starts, c_type))
+
+
 # -------------------------------------------------------- weight gradient --
 def _wgrad_operands(rng, sizes, starts, M_cap, P, Q, exact=False):
     nb = M_cap // 128
