@@ -21,7 +21,7 @@ from .binding import (  # noqa: F401
     moe_grouped_gemm_workspace_size,
     moe_permute, moe_permute_workspace_size, moe_quantize_mxfp4, moe_quantize_mxfp8,
     moe_unpermute, moe_weight_repack_interleave, EXPORTED_SYMBOLS,
-    FP8_BLOCK, QUANT_TILE, TYPE_BF16, TYPE_F32, DEVERR_NONFINITE,
+    PREC_FP8, FP8_BLOCK, QUANT_TILE, TYPE_BF16, TYPE_F32, DEVERR_NONFINITE,
     moe_quantize_fp8, moe_grouped_gemm_fp8, moe_grouped_gemm_fp8_workspace_size,
     moe_grouped_wgrad_fp8, moe_router_loss, moe_router_loss_workspace_size, moe_router_bwd,
     moe_grad_sumsq, moe_grad_clip, moe_grad_workspace_size,

@@ -19,6 +19,7 @@ lib_path = os.path.join(HERE, "libmoe_gmlp.so")
 # ---- constants mirrored from include/moe_gmlp.h ---------------------------
 ACT_SWIGLU, ACT_GEGLU, ACT_SRELU = 0, 1, 2
 PREC_BF16, PREC_MXFP8, PREC_MXFP4 = 0, 1, 2
+PREC_FP8 = 3   # block-scaled FP8: a precision of ExpertBlock, not of moe_grouped_mlp_fwd / _bwd
 PERMUTE_BUILD_MAP, PERMUTE_GATHER, PERMUTE_WRITE_MX = 0x1, 0x2, 0x4
 PERMUTE_WRITE_MX4 = 0x8
 QUANT_ROW, QUANT_COL, QUANT_BOTH, QUANT_TILE = 0, 1, 2, 3

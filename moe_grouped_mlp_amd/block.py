@@ -36,6 +36,21 @@ as separate passes instead (bf16 permutes and activation passes,
 moe_quantize_mxfp4 before each of the four grouped GEMMs): the baseline the
 fused path is measured against, which needs the bf16 copies.
 
+With prec=PREC_FP8 the layer runs on block-scaled FP8 operands (E4M3 with one
+fp32 scale per 128 values, weights per 128 x 128 tile) as separate passes:
+bf16 permutes and activation passes, moe_quantize_fp8 before each product,
+moe_grouped_gemm_fp8 for FC1, FC2 and both dgrads (which read the transposed
+weight copies) and moe_grouped_wgrad_fp8 for the weight gradients, whose
+transposed operands are made in the same pass as the row ones.  Layers of
+few tokens (decoding) take the product's kernel for few rows by themselves.
+wgrad_type=TYPE_F32 keeps the weight gradients in fp32, to which
+weight_grads(accumulate=True) adds.  No bias and no recompute path.
+
+Around the experts, router_loss() gives the router's balance and z losses and
+per-expert counts, router_backward() the gradient of its logits from these
+and from the dprobs of backward(), and clip_grads() scales the weight
+gradients (and any others given) to a largest global norm.
+
 With recompute=True (activation recompute) the forward stores no z and the
 backward first rebuilds it with moe_grouped_gemm from the saved Xp and W1
 (recompute_z): z's write moves from the forward to the backward, at the cost
@@ -66,7 +81,8 @@ class ExpertBlock:
                  prec: int = B.PREC_BF16, transposed_copies: bool = True,
                  bf16_copies: Optional[bool] = None, wgrad: bool = False,
                  recompute: bool = False, z_scratch: Optional[torch.Tensor] = None,
-                 unfused: bool = False, device="cuda"):
+                 unfused: bool = False, wgrad_type: int = B.TYPE_BF16,
+                 device="cuda"):
         self.E, self.H, self.I, self.T, self.k = E, H, I, T, k
         self.act = act or B.act_params()
         self.gated = self.act.act != B.ACT_SRELU
@@ -85,11 +101,16 @@ class ExpertBlock:
         # through the *_unfused methods (bf16 copies needed), as separate
         # passes with every operand quantized by moe_quantize_mxfp4
         self.mx4 = prec == B.PREC_MXFP4
+        self.fp8 = prec == B.PREC_FP8
+        if self.fp8 and (recompute or unfused):
+            raise ValueError("the FP8 layer has no recompute path, and always runs as separate passes")
+        if wgrad_type != B.TYPE_BF16 and not self.fp8:
+            raise ValueError("fp32 weight gradients are of the FP8 layer (prec=PREC_FP8)")
         # forward() / backward() run the unfused passes (the baseline the
         # fused kernels are measured against; bf16 copies are then needed)
         self.unfused = unfused
         M_cap = M_cap if M_cap is not None else T * k + E * (B.GROUP_ALIGN - 1)
-        if self.mx or self.mx4:
+        if self.mx or self.mx4 or self.fp8:
             M_cap = -(-M_cap // B.GROUP_ALIGN) * B.GROUP_ALIGN
         self.M_cap = M_cap
         self.cu_margin = cu_margin
@@ -138,8 +159,9 @@ class ExpertBlock:
         self.dx = torch.empty(T, H, **bf)
         self.dprobs = torch.zeros(T, k, **f32)
         self.ws = torch.empty(
-            max(1, B.moe_grouped_mlp_workspace_size(E, H, I, M, prec,
-                                                    self.act.act)),
+            max(1, max(B.moe_grouped_gemm_fp8_workspace_size(E, n, k, M, T)
+                       for n, k in ((N1, H), (H, I), (I, H), (H, N1))) if self.fp8 else
+                B.moe_grouped_mlp_workspace_size(E, H, I, M, prec, self.act.act)),
             dtype=torch.uint8, device=dev)
         self.w1i = torch.empty(E, N1, H, **bf)
         self.w2 = torch.empty(E, H, I, **bf)
@@ -189,7 +211,28 @@ class ExpertBlock:
             self.w2_q4, self.w2_s4 = fp4_pair(E, H, I)      # along I
             self.w2t_q4, self.w2t_s4 = fp4_pair(E, I, H)    # along H
             self.w1t_q4, self.w1t_s4 = fp4_pair(E, H, N1)   # along N1
+        if self.fp8:
+            def fp8_rows(R, K):      # a row copy: codes and scales
+                return torch.empty(R, K, **u8), torch.empty(-(-K // B.FP8_BLOCK), R, **f32)
+
+            def fp8_tiles(R, K):     # every expert's tile copy
+                return (torch.empty(E, R, K, **u8),
+                        torch.empty(E, -(-R // B.FP8_BLOCK), -(-K // B.FP8_BLOCK), **f32))
+            self.da = torch.empty(M, I, **bf)
+            for name, n in (("xp", H), ("a", I), ("dyp", H), ("dz", N1)):
+                q, sc = fp8_rows(M, n)
+                setattr(self, name + "_q8", q)
+                setattr(self, name + "_s8", sc)
+                # the transposed copies, operands of the weight gradients
+                qT, sT = fp8_rows(n, M) if wgrad else (None, None)
+                setattr(self, name + "T_q8", qT)
+                setattr(self, name + "T_s8", sT)
+            self.w1_q8, self.w1_s8 = fp8_tiles(N1, H)
+            self.w1t_q8, self.w1t_s8 = fp8_tiles(H, N1)
+            self.w2_q8, self.w2_s8 = fp8_tiles(H, I)
+            self.w2t_q8, self.w2t_s8 = fp8_tiles(I, H)
         self.wgrad = wgrad
+        self.wgrad_type = wgrad_type
         if wgrad:
             if self.mx or self.mx4:
                 if not transposed_copies:
@@ -204,8 +247,9 @@ class ExpertBlock:
             elif self.mx4:
                 self.xpT_q4, self.xpT_s4 = fp4_pair(H, M)
                 self.dypT_q4, self.dypT_s4 = fp4_pair(H, M)
-            self.dw1 = torch.empty(E, N1, H, **bf)
-            self.dw2 = torch.empty(E, H, I, **bf)
+            dw = f32 if wgrad_type == B.TYPE_F32 else bf
+            self.dw1 = torch.empty(E, N1, H, **dw)
+            self.dw2 = torch.empty(E, H, I, **dw)
 
     # ------------------------------------------------------------ weights --
     def load_weights(self, w1: torch.Tensor, w2: torch.Tensor,
@@ -228,7 +272,7 @@ class ExpertBlock:
         else:
             self.w1i.copy_(w1)
         self.w2.copy_(w2)
-        if self.mx or self.mx4:
+        if self.mx or self.mx4 or self.fp8:
             self.quantize_weights()
 
     def quantize_weights(self, live_only: bool = False) -> None:
@@ -241,6 +285,14 @@ class ExpertBlock:
         step's GEMMs read none of their weights; their copies are left as
         they were)."""
         E, H, I, N1 = self.E, self.H, self.I, self.N1
+        if self.fp8:
+            for x, rows, cols, copy, copy_t in ((self.w1i, N1, H, "w1", "w1t"),
+                                                (self.w2, H, I, "w2", "w2t")):
+                B.moe_quantize_fp8(mode=B.QUANT_TILE, batch=E, rows=rows, cols=cols, x=x,
+                                   q=getattr(self, copy + "_q8"), s=getattr(self, copy + "_s8"),
+                                   qT=getattr(self, copy_t + "_q8"), sT=getattr(self, copy_t + "_s8"),
+                                   live=self.split_sizes if live_only else None)
+            return
         # one pass per weight writes both of its copies (ROW into q / s, COL
         # into qT / sT), reading the bf16 weight once
         if self.mx4:
@@ -391,7 +443,9 @@ class ExpertBlock:
 
     def forward(self, x, expert_idx, probs, timing_events=None):
         self.route(expert_idx, probs, x)
-        if self.unfused:
+        if self.fp8:
+            self.experts_forward_fp8()
+        elif self.unfused:
             self.experts_forward_unfused()
         else:
             self.experts_forward(timing_events)
@@ -428,7 +482,9 @@ class ExpertBlock:
 
     def backward(self, dout, timing_events=None):
         self.gather(dout, self.dyp, *self._mx_dst("dyp"))
-        if self.unfused:
+        if self.fp8:
+            self.experts_backward_fp8()
+        elif self.unfused:
             self.experts_backward_unfused()
         else:
             self.experts_backward(timing_events)
@@ -532,11 +588,120 @@ class ExpertBlock:
             self._gemm(self.H, self.N1, self.dz, self.w1i, self.dxp, b_kn=True)
         rec(3)
 
-    def weight_grads(self, timing_events=None):
-        """dW1 (rows in w1i's interleaved order) and dW2 of the last
-        forward + backward; needs wgrad=True."""
+    # ------------------------------------------- block-scaled FP8 layer --
+    def _quantize8(self, name, x, cols):
+        """Row copy of x (and, with wgrad, its transposed one in the same
+        pass), of the rows the groups' spans hold."""
+        qT = getattr(self, name + "T_q8")
+        B.moe_quantize_fp8(mode=B.QUANT_ROW if qT is None else B.QUANT_BOTH, batch=1,
+                           rows=self.M_cap, cols=cols, x=x, q=getattr(self, name + "_q8"),
+                           s=getattr(self, name + "_s8"), qT=qT, sT=getattr(self, name + "T_s8"),
+                           row_end=self.padded_offsets[self.E:])
+
+    def _gemm8(self, N, K, name, weight, c):
+        B.moe_grouped_gemm_fp8(E=self.E, N=N, K=K, M_cap=self.M_cap, split_sizes=self.split_sizes,
+                               padded_offsets=self.padded_offsets, a=getattr(self, name + "_q8"),
+                               a_s=getattr(self, name + "_s8"), b=getattr(self, weight + "_q8"),
+                               b_s=getattr(self, weight + "_s8"), c=c, max_rows=self.T,
+                               cu_margin=self.cu_margin, err_flag=self.err_flag, workspace=self.ws)
+
+    def experts_forward_fp8(self) -> None:
+        if self.bias1 is not None:
+            raise RuntimeError("the FC1 bias is applied by the fused path only")
+        self._quantize8("xp", self.xp, self.H)
+        self._gemm8(self.N1, self.H, "xp", "w1", self.z)
+        B.moe_glu_unfused(direction=0, E=self.E, I=self.I, M_cap=self.M_cap,
+                          split_sizes=self.split_sizes,
+                          padded_offsets=self.padded_offsets, probs_p=self.probs_p,
+                          z=self.z, a=self.a, amax=self.amax, act=self.act)
+        self._quantize8("a", self.a, self.I)
+        self._gemm8(self.H, self.I, "a", "w2", self.yp)
+
+    def experts_backward_fp8(self) -> None:
+        self._quantize8("dyp", self.dyp, self.H)
+        self._gemm8(self.I, self.H, "dyp", "w2t", self.da)
+        B.moe_glu_unfused(direction=1, E=self.E, I=self.I, M_cap=self.M_cap,
+                          split_sizes=self.split_sizes,
+                          padded_offsets=self.padded_offsets, probs_p=self.probs_p,
+                          z=self.z, da=self.da, dz=self.dz,
+                          dprobs_p=self.dprobs_p, act=self.act)
+        self._quantize8("dz", self.dz, self.N1)
+        self._gemm8(self.H, self.N1, "dz", "w1t", self.dxp)
+
+    # ------------------------------------------------- around the experts --
+    def router_loss(self, logits: torch.Tensor, *, balance_coef: float = 0.0,
+                    z_coef: float = 0.0, token_mask: Optional[torch.Tensor] = None,
+                    expert_idx: Optional[torch.Tensor] = None):
+        """[balance loss, z loss] (fp32 [2]) of the router's logits [T][E_total]
+        and the picks (route_logits()'s by default); token_mask [T] leaves
+        tokens with 0 out.  Also fills router_counts, router_tokens and
+        router_prob_mean, and keeps what router_backward() needs."""
+        T, E_all = logits.shape
+        idx = self.expert_idx if expert_idx is None else expert_idx
+        if getattr(self, "router_counts", None) is None or self.router_counts.numel() != E_all:
+            dev = logits.device
+            self.router_counts = torch.empty(E_all, dtype=torch.int32, device=dev)
+            self.router_tokens = torch.empty(1, dtype=torch.int32, device=dev)
+            self.router_prob_mean = torch.empty(E_all, dtype=torch.float32, device=dev)
+            self.router_losses = torch.empty(2, dtype=torch.float32, device=dev)
+            self.dlogits = torch.empty(T, E_all, dtype=torch.float32, device=dev)
+            self.ws_loss = torch.empty(B.moe_router_loss_workspace_size(T, E_all),
+                                       dtype=torch.uint8, device=dev)
+        self._router_args = dict(T=T, E=E_all, k=self.k, logits=logits, expert_idx=idx,
+                                 token_mask=token_mask, balance_coef=balance_coef, z_coef=z_coef,
+                                 counts=self.router_counts, n_tokens=self.router_tokens)
+        B.moe_router_loss(**self._router_args, prob_mean=self.router_prob_mean,
+                          loss=self.router_losses, workspace=self.ws_loss)
+        return self.router_losses
+
+    def router_backward(self, dloss: Optional[torch.Tensor] = None,
+                        dprobs: Optional[torch.Tensor] = None):
+        """Gradient of the logits given to router_loss(): of its two losses
+        (dloss fp32 [2], their upstream gradients; ones by default) and of the
+        kept probabilities (backward()'s dprobs by default)."""
+        if getattr(self, "_router_args", None) is None:
+            raise RuntimeError("router_backward() needs router_loss() first")
+        B.moe_router_bwd(**self._router_args, dloss=dloss,
+                         dprobs=self.dprobs if dprobs is None else dprobs, dlogits=self.dlogits)
+        return self.dlogits
+
+    def clip_grads(self, max_norm: float, extra=()):
+        """Scales dw1, dw2 and the extra gradients (bf16 or fp32, contiguous)
+        in place so that their global norm is at most max_norm; returns the
+        norm (fp32 [1])."""
         if not self.wgrad:
             raise RuntimeError("ExpertBlock was built without wgrad=True")
+        grads = [self.dw1, self.dw2, *extra]
+        need = B.moe_grad_workspace_size(len(grads))
+        if getattr(self, "ws_grad", None) is None or self.ws_grad.numel() < need:
+            dev = self.dw1.device
+            self.ws_grad = torch.empty(need, dtype=torch.uint8, device=dev)
+            self.grad_sumsq = torch.empty(1, dtype=torch.float64, device=dev)
+            self.grad_norm = torch.empty(1, dtype=torch.float32, device=dev)
+        B.moe_grad_sumsq(tensors=grads, sumsq=self.grad_sumsq, workspace=self.ws_grad)
+        B.moe_grad_clip(tensors=grads, sumsq=self.grad_sumsq, max_norm=max_norm,
+                        norm=self.grad_norm, err_flag=self.err_flag)
+        return self.grad_norm
+
+    def weight_grads(self, timing_events=None, accumulate: bool = False):
+        """dW1 (rows in w1i's interleaved order) and dW2 of the last
+        forward + backward; needs wgrad=True.  accumulate (fp32 gradients of
+        the FP8 layer): adds to what dw1 and dw2 hold."""
+        if not self.wgrad:
+            raise RuntimeError("ExpertBlock was built without wgrad=True")
+        if accumulate and self.wgrad_type != B.TYPE_F32:
+            raise RuntimeError("accumulation needs fp32 weight gradients (wgrad_type=TYPE_F32)")
+        if self.fp8:
+            for P, Q, left, right, c in ((self.N1, self.H, "dzT", "xpT", self.dw1),
+                                         (self.H, self.I, "dypT", "aT", self.dw2)):
+                B.moe_grouped_wgrad_fp8(E=self.E, P=P, Q=Q, M_cap=self.M_cap,
+                                        split_sizes=self.split_sizes,
+                                        padded_offsets=self.padded_offsets,
+                                        a=getattr(self, left + "_q8"), a_s=getattr(self, left + "_s8"),
+                                        b=getattr(self, right + "_q8"), b_s=getattr(self, right + "_s8"),
+                                        c=c, c_type=self.wgrad_type, accumulate=accumulate,
+                                        cu_margin=self.cu_margin, err_flag=self.err_flag)
+            return self.dw1, self.dw2
         kw = {}
         if self.mx:
             for src, q, s in ((self.xp, self.xpT_q, self.xpT_s),
