@@ -6,10 +6,8 @@ The functions only marshal arguments; all work runs in the HIP kernels.
 
 from __future__ import annotations
 
-import array
 import ctypes
 import math
-import operator
 import os
 from ctypes import c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
 
@@ -543,74 +541,46 @@ def moe_glu_unfused(*, direction, E, I, M_cap, split_sizes, padded_offsets,
 
 
 # ---- block-scaled FP8, router losses, gradient norm -----------------------
-# These check what the C ABI cannot see: that a tensor is contiguous device
-# memory of the type and at least the size the call reads or writes, on the
-# device the call runs on (torch's current one).  A small call is as long as
-# its marshalling, so the checks are few attribute reads, and what they need
-# of torch is looked up once.
-def _buf(fn, name, t, dtypes, n, dev):
-    if t is None:
-        return None
-    try:
-        if (t.dtype in dtypes and t.numel() >= n and t.get_device() == dev
-                and t.is_contiguous()):
-            return t.data_ptr()
-    except (AttributeError, TypeError):
-        pass
-    raise ValueError(f"{fn}: {name} must be a contiguous tensor of type "
-                     f"{' or '.join(map(str, dtypes))} with at least {n} elements "
-                     f"on the current device (cuda:{dev})")
-
-
-_F32 = None
-_dtype_of = operator.attrgetter("dtype")
+# A small call is as long as its marshalling, so these go through a compiled
+# module (csrc/py_call.cpp), which also checks what the C ABI cannot see: that
+# a tensor is contiguous device memory of the type and at least the size the
+# call reads or writes, on the device the call runs on (torch's current one).
+_call = None
+_get_device = None
 
 
 def _setup():
+    """Loads the compiled module; raises if it is not built."""
+    global _call, _get_device
+    lib()
     import torch
-    global _F32, _BF16, _U8, _I32, _F64, _CODES, _MASK, _GRADS, _Tensor, _current_device, _raw_stream
-    _BF16, _U8, _I32 = (torch.bfloat16,), (torch.uint8,), (torch.int32,)
-    _F64, _CODES, _MASK = (torch.float64,), (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.bool)
-    _GRADS = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32}
-    _Tensor = torch.Tensor
-    _current_device = torch.cuda.current_device
+    try:
+        from . import _call as c
+    except ImportError as e:
+        raise ImportError("moe_grouped_mlp_amd/_call.so is missing or of another torch: build it "
+                          "with `python -m moe_grouped_mlp_amd.build`") from e
     # the current stream's handle without the Stream object around it
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
-                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-    _F32 = (torch.float32,)
+    c.setup(_check, getattr(torch._C, "_cuda_getCurrentRawStream",
+                            lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+    _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _call = c
 
 
 def _device():
-    """The current device's index, for _buf and _stream_on."""
-    if _F32 is None:
+    """The current device's index."""
+    if _get_device is None:
+        import torch
+        torch.cuda.current_device()   # initialises CUDA, or says why it cannot
         _setup()
-    return _current_device()
-
-
-def _stream_on(dev, stream):
-    return _raw_stream(dev) if stream is None else _stream(stream)
-
-
-def _blocks(n):
-    return -(-n // FP8_BLOCK)
+    return _get_device()
 
 
 def moe_quantize_fp8(*, mode, batch, rows, cols, x, q, s, qT=None, sT=None, pow2=False,
                      x_stride=0, live=None, row_end=None, stream=None):
     """bf16 -> block-scaled FP8 (E4M3 codes with fp32 scales per 128)."""
-    f, d = "moe_quantize_fp8", _device()
-    n = batch * rows * cols
-    rb, cb = _blocks(rows), _blocks(cols)
-    ns = {QUANT_ROW: cb * rows, QUANT_COL: rb * cols, QUANT_BOTH: cb * rows,
-          QUANT_TILE: rb * cb}.get(mode, 0) * batch
-    nsT = (rb * cb if mode == QUANT_TILE else rb * cols) * batch
-    nx = (batch - 1) * x_stride + rows * cols if x_stride and batch else n
-    a = QuantFp8Args(mode, batch, rows, cols, x_stride, _buf(f, "x", x, _BF16, nx, d),
-                     _buf(f, "q", q, _CODES, n, d), _buf(f, "s", s, _F32, ns, d),
-                     _buf(f, "qT", qT, _CODES, n, d), _buf(f, "sT", sT, _F32, nsT, d),
-                     int(bool(pow2)), _buf(f, "live", live, _I32, batch, d),
-                     _buf(f, "row_end", row_end, _I32, 1, d))
-    _check(f, lib().moe_quantize_fp8(ctypes.byref(a), _stream_on(d, stream)))
+    d = _device()
+    _call.quantize_fp8(d, mode, batch, rows, cols, x_stride, x, q, s, qT, sT, pow2, live, row_end,
+                       stream)
 
 
 def moe_grouped_gemm_fp8_workspace_size(E, N, K, M_cap, max_rows=0) -> int:
@@ -621,33 +591,19 @@ def moe_grouped_gemm_fp8(*, E, N, K, M_cap, split_sizes, padded_offsets, a, a_s,
                          b_stride=0, b_s_stride=0, ldc=0, c_type=TYPE_BF16, max_rows=0,
                          cu_margin=0, err_flag=None, workspace=None, stream=None):
     """C[r] = A[r] . B_e^T on block-scaled FP8 operands for every group's rows."""
-    f, d = "moe_grouped_gemm_fp8", _device()
-    nk, ns = N * K, _blocks(N) * _blocks(K)
-    args = GemmFp8Args(
-        E, N, K, M_cap, _buf(f, "split_sizes", split_sizes, _I32, E, d),
-        _buf(f, "padded_offsets", padded_offsets, _I32, E + 1, d),
-        _buf(f, "a", a, _CODES, M_cap * K, d), _buf(f, "a_s", a_s, _F32, M_cap * _blocks(K), d),
-        _buf(f, "b", b, _CODES, (E - 1) * (b_stride or nk) + nk, d),
-        _buf(f, "b_s", b_s, _F32, (E - 1) * (b_s_stride or ns) + ns, d), b_stride, b_s_stride,
-        _buf(f, "c", c, _F32 if c_type == TYPE_F32 else _BF16, (M_cap - 1) * (ldc or N) + N, d),
-        ldc, c_type, max_rows, cu_margin, _buf(f, "err_flag", err_flag, _I32, 1, d),
-        _buf(f, "workspace", workspace, _U8, 0, d), _nbytes(workspace))
-    _check(f, lib().moe_grouped_gemm_fp8(ctypes.byref(args), _stream_on(d, stream)))
+    d = _device()
+    _call.grouped_gemm_fp8(d, E, N, K, M_cap, b_stride, b_s_stride, ldc, c_type, max_rows,
+                           cu_margin, split_sizes, padded_offsets, a, a_s, b, b_s, c, err_flag,
+                           workspace, stream)
 
 
 def moe_grouped_wgrad_fp8(*, E, P, Q, M_cap, split_sizes, padded_offsets, a, a_s, b, b_s, c,
                           c_type=TYPE_BF16, accumulate=False, cu_margin=0, err_flag=None,
                           stream=None):
     """C_e = A_e . B_e^T over each group's routed rows (transposed FP8 copies)."""
-    f, d = "moe_grouped_wgrad_fp8", _device()
-    args = WgradFp8Args(
-        E, P, Q, M_cap, _buf(f, "split_sizes", split_sizes, _I32, E, d),
-        _buf(f, "padded_offsets", padded_offsets, _I32, E + 1, d),
-        _buf(f, "a", a, _CODES, P * M_cap, d), _buf(f, "a_s", a_s, _F32, P * _blocks(M_cap), d),
-        _buf(f, "b", b, _CODES, Q * M_cap, d), _buf(f, "b_s", b_s, _F32, Q * _blocks(M_cap), d),
-        _buf(f, "c", c, _F32 if c_type == TYPE_F32 else _BF16, E * P * Q, d), c_type,
-        int(bool(accumulate)), cu_margin, _buf(f, "err_flag", err_flag, _I32, 1, d))
-    _check(f, lib().moe_grouped_wgrad_fp8(ctypes.byref(args), _stream_on(d, stream)))
+    d = _device()
+    _call.grouped_wgrad_fp8(d, E, P, Q, M_cap, c_type, accumulate, cu_margin, split_sizes,
+                            padded_offsets, a, a_s, b, b_s, c, err_flag, stream)
 
 
 def moe_router_loss_workspace_size(T, E) -> int:
@@ -657,79 +613,32 @@ def moe_router_loss_workspace_size(T, E) -> int:
 def moe_router_loss(*, T, E, k, logits, expert_idx, counts, n_tokens, prob_mean, loss, workspace,
                     balance_coef=0.0, z_coef=0.0, token_mask=None, stream=None):
     """Per-expert counts, mean probabilities and loss = [balance, z]."""
-    f, d = "moe_router_loss", _device()
-    args = RouterLossArgs(
-        T, E, k, _buf(f, "logits", logits, _F32, T * E, d),
-        _buf(f, "expert_idx", expert_idx, _I32, T * k, d),
-        _buf(f, "token_mask", token_mask, _MASK, T, d), balance_coef, z_coef,
-        _buf(f, "counts", counts, _I32, E, d), _buf(f, "n_tokens", n_tokens, _I32, 1, d),
-        _buf(f, "prob_mean", prob_mean, _F32, E, d), _buf(f, "loss", loss, _F32, 2, d),
-        _buf(f, "workspace", workspace, _U8, 0, d), _nbytes(workspace))
-    _check(f, lib().moe_router_loss(ctypes.byref(args), _stream_on(d, stream)))
+    d = _device()
+    _call.router_loss(d, T, E, k, balance_coef, z_coef, logits, expert_idx, token_mask, counts,
+                      n_tokens, prob_mean, loss, workspace, stream)
 
 
 def moe_router_bwd(*, T, E, k, logits, expert_idx, dlogits, dprobs=None, dloss=None, counts=None,
                    n_tokens=None, balance_coef=0.0, z_coef=0.0, token_mask=None, stream=None):
     """Gradient of the kept probabilities and of both losses with respect to
     the router's logits."""
-    f, d = "moe_router_bwd", _device()
-    args = RouterBwdArgs(
-        T, E, k, _buf(f, "logits", logits, _F32, T * E, d),
-        _buf(f, "expert_idx", expert_idx, _I32, T * k, d),
-        _buf(f, "token_mask", token_mask, _MASK, T, d),
-        _buf(f, "dprobs", dprobs, _F32, T * k, d), _buf(f, "dloss", dloss, _F32, 2, d),
-        balance_coef, z_coef, _buf(f, "counts", counts, _I32, E, d),
-        _buf(f, "n_tokens", n_tokens, _I32, 1, d), _buf(f, "dlogits", dlogits, _F32, T * E, d))
-    _check(f, lib().moe_router_bwd(ctypes.byref(args), _stream_on(d, stream)))
+    d = _device()
+    _call.router_bwd(d, T, E, k, balance_coef, z_coef, logits, expert_idx, token_mask, dprobs,
+                     dloss, counts, n_tokens, dlogits, stream)
 
 
 def moe_grad_workspace_size(n_tensors) -> int:
     return lib().moe_grad_workspace_size(n_tensors)
 
 
-def _tensor_list(fn, tensors, out, dev):
-    """The host array of moe_tensor: four 8-byte words each (data, out, numel,
-    type), filled column by column, as lists may be long."""
-    T, n = _Tensor, len(tensors)
-    try:
-        types = [_GRADS.get(d) for d in map(_dtype_of, tensors)]
-        if None in types:
-            raise ValueError(f"{fn}: tensor {types.index(None)} must be bfloat16 or float32")
-        numels = list(map(T.numel, tensors))
-        every = tensors
-        words = array.array("q", bytes(32 * max(1, n)))
-        if out is not None:
-            if (len(out) != n or list(map(_dtype_of, out)) != list(map(_dtype_of, tensors))
-                    or list(map(T.numel, out)) != numels):
-                raise ValueError(f"{fn}: out must have a tensor of each one's type and size")
-            words[1:4 * n:4] = array.array("q", map(T.data_ptr, out))
-            every = [*tensors, *out]
-        if not all(map(T.is_contiguous, every)) or any(map(dev.__ne__, map(T.get_device, every))):
-            raise ValueError(f"{fn}: the tensors must be contiguous and on the current device "
-                             f"(cuda:{dev})")
-        words[0:4 * n:4] = array.array("q", map(T.data_ptr, tensors))
-        words[2:4 * n:4] = array.array("q", numels)
-        words[3:4 * n:4] = array.array("q", types)
-    except (AttributeError, TypeError):
-        raise ValueError(f"{fn}: a list of tensors is needed") from None
-    return ctypes.cast((c_int64 * len(words)).from_buffer(words), ctypes.POINTER(Tensor))
-
-
 def moe_grad_sumsq(*, tensors, sumsq, workspace, stream=None):
     """sumsq (float64 [1]) = sum of squares over a list of gradients."""
-    f, d = "moe_grad_sumsq", _device()
-    arr = _tensor_list(f, tensors, None, d)
-    args = GradArgs(arr, len(tensors), 0.0, _buf(f, "sumsq", sumsq, _F64, 1, d), None, None,
-                    _buf(f, "workspace", workspace, _U8, 0, d), _nbytes(workspace))
-    _check(f, lib().moe_grad_sumsq(ctypes.byref(args), _stream_on(d, stream)))
+    d = _device()
+    _call.grad_sumsq(d, tensors, sumsq, workspace, stream)
 
 
 def moe_grad_clip(*, tensors, sumsq, max_norm, out=None, norm=None, err_flag=None, stream=None):
     """Scale the gradients (in place, or into out) so that their norm
     sqrt(sumsq) is at most max_norm."""
-    f, d = "moe_grad_clip", _device()
-    arr = _tensor_list(f, tensors, out, d)
-    args = GradArgs(arr, len(tensors), max_norm, _buf(f, "sumsq", sumsq, _F64, 1, d),
-                    _buf(f, "norm", norm, _F32, 1, d), _buf(f, "err_flag", err_flag, _I32, 1, d),
-                    None, 0)
-    _check(f, lib().moe_grad_clip(ctypes.byref(args), _stream_on(d, stream)))
+    d = _device()
+    _call.grad_clip(d, tensors, out, max_norm, sumsq, norm, err_flag, stream)

@@ -4,7 +4,8 @@
 
 Every HIP source is compiled for gfx950 only, with packed-fp32 instruction
 selection switched off, then linked into one shared library next to this
-file.  Objects go to moe_grouped_mlp_amd/_build/.
+file, and with it _call.so, the compiled part of the Python binding.  Objects
+go to moe_grouped_mlp_amd/_build/.
 """
 
 from __future__ import annotations
@@ -19,6 +20,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_gmlp.so")
+CALL = os.path.join(HERE, "_call.so")   # Python's way into the smaller calls
 
 SOURCES = ["api.cpp", "route.hip", "router.hip", "unfused.hip", "permute.hip", "quant.hip", "gemm.hip", "gemm_store.hip",
            "gemm_glu_bf16.hip", "gemm_glu_mx.hip", "gemm_dglu_bf16.hip", "gemm_dglu_mx.hip", "gemm_wgrad.hip",
@@ -52,12 +54,42 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_call() -> str:
+    """csrc/py_call.cpp, host code on CPython's and torch's headers."""
+    import sysconfig
+
+    from torch.utils import cpp_extension
+    obj = os.path.join(BUILD, "py_call.o")
+    cmd = [HIPCC, "-x", "c++", "-O2", "-fPIC", "-std=c++17", "-Wall", "-fvisibility=hidden",
+           *(f"-I{p}" for p in (sysconfig.get_paths()["include"], *cpp_extension.include_paths())),
+           "-c", os.path.join(CSRC, "py_call.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling py_call.cpp failed:\n{r.stderr}")
+    return obj
+
+
+def _link_call(obj: str) -> None:
+    from torch.utils import cpp_extension
+    libs = cpp_extension.library_paths()
+    tmp = CALL + ".tmp"
+    cmd = [HIPCC, "-no-hip-rt", "-shared", "-fPIC", "-o", tmp, obj, f"-L{HERE}",
+           f"-l:{os.path.basename(LIB)}", "-Wl,-rpath,$ORIGIN",
+           *(f"-L{p}" for p in libs), *(f"-Wl,-rpath,{p}" for p in libs),
+           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stderr}")
+    os.replace(tmp, CALL)
+
+
 def build(verbose: bool = True) -> str:
     if shutil.which(HIPCC) is None and not os.path.exists(HIPCC):
         raise RuntimeError(f"hipcc not found ({HIPCC})")
     os.makedirs(BUILD, exist_ok=True)
     jobs = min(len(SOURCES), int(os.environ.get("MAX_JOBS", "8")))
     with cf.ThreadPoolExecutor(jobs) as ex:
+        call = ex.submit(_compile_call)
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs]
@@ -65,8 +97,9 @@ def build(verbose: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_call(call.result())
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB}\nbuilt {CALL}")
     return LIB
 
 

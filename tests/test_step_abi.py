@@ -235,3 +235,33 @@ def test_binding_refuses_other_tensors():
             m.moe_grad_clip(tensors=[f32], out=[], sumsq=f32, max_norm=1.0)
         with pytest.raises(ValueError):
             m.moe_grad_clip(tensors=[f32], out=[f32.double()], sumsq=f32, max_norm=1.0)
+
+
+def test_binding_refuses_other_arguments():
+    """Numbers that do not fit, lists that are none, sizes whose product passes
+    64 bits: exceptions, never a wrapped number."""
+    import unittest.mock as mock
+    f32 = torch.zeros(4, 8)
+    idx = torch.zeros(4, 2, dtype=torch.int32)
+    bf = torch.zeros(16, 16, dtype=torch.bfloat16)
+    with mock.patch.object(B, "_device", lambda: (B._setup(), -1)[1]):   # -1: the CPU tensors' device
+        with pytest.raises(OverflowError):
+            m.moe_router_bwd(T=2 ** 32 + 4, E=8, k=2, expert_idx=idx, logits=f32, dlogits=f32)
+        with pytest.raises(OverflowError):
+            m.moe_router_bwd(T=2 ** 70, E=8, k=2, expert_idx=idx, logits=f32, dlogits=f32)
+        for T in ("4", 4.5, None):
+            with pytest.raises(TypeError):
+                m.moe_router_bwd(T=T, E=8, k=2, expert_idx=idx, logits=f32, dlogits=f32)
+        big = 2 ** 31 - 1
+        with pytest.raises(ValueError, match="x must be a contiguous tensor of type torch.bfloat16"):
+            m.moe_quantize_fp8(mode=m.QUANT_ROW, batch=big, rows=big, cols=big, x=bf, q=f32, s=f32)
+        for tensors in (None, 3, [None], ["x"], [f32, 1]):
+            with pytest.raises(ValueError):
+                m.moe_grad_sumsq(tensors=tensors, sumsq=torch.zeros(1, dtype=torch.float64),
+                                 workspace=torch.zeros(64, dtype=torch.uint8))
+        with pytest.raises(ValueError):   # a layout that is no strided one
+            m.moe_grad_clip(tensors=[f32.to_sparse()], sumsq=torch.zeros(1, dtype=torch.float64), max_norm=1.0)
+        with pytest.raises(m.MoeError):   # what the library itself refuses
+            m.moe_router_bwd(T=-1, E=8, k=2, expert_idx=idx, logits=f32, dlogits=f32, stream=0)
+        with pytest.raises(AttributeError):
+            m.moe_router_bwd(T=4, E=8, k=2, expert_idx=idx, logits=f32, dlogits=f32, stream="x")
