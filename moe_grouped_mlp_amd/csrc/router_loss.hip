@@ -7,15 +7,19 @@
 //   dx_j = p_j (v_j - sum_i p_i v_i + 2 c_z lse / n),
 //   v_j = c_b E counts_j / (k n^2) + sum of dprobs over the slots that name j
 //
-// A token takes L lanes of a wave, L a power of two that leaves a lane at
-// most 16 of the E logits, so the logits are read once and stay in
-// registers; a wave covers 64 / L tokens.  Lane g of a token holds experts
-// 4 (g + L i) + c (VEC: E % 4 == 0 and 16-byte aligned rows, one float4
-// each), else g + L i.  The
-// loss kernel keeps each lane's sums of p over its tokens in registers, adds
-// them over the workgroup in a fixed order and writes one fp32 partial per
-// expert and workgroup; a second launch of one workgroup adds these in fp64.
-// Bound by HBM for many tokens and by the two launches for few.
+// A token takes L lanes of a wave with P logits each (4, or 16 for more than 64
+// experts), so the logits are read once and stay in registers; a wave covers
+// 64 / L tokens.  Lane g of a token holds experts 4 (g + L i) + c (VEC:
+// E % 4 == 0 and 16-byte aligned rows, one float4 each), else g + L i.  The loss
+// kernel keeps each lane's sums of p over its tokens in registers, adds them
+// over the workgroup in a fixed order and writes one fp32 partial per expert and
+// workgroup; a second launch adds these in fp64, unless there is one workgroup
+// only, which then does all of it.
+//
+// Bound by latencies: a workgroup makes one or a few passes, so all it reads
+// goes out at once, before the first use.  16384 tokens of 256 experts: 8.2 us
+// for the partials (16.8 MB read), 4.7 for their sums, 11.7 for the gradient
+// (33.6 MB, 2.9 TB/s); 256 tokens of 4: 4.8 and 2.8 in one launch each.
 #include <type_traits>
 
 #include "common.h"
@@ -25,7 +29,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 16;   // logits a lane holds
 
 template <int L, typename T, typename F>
 MOE_DEV T group_reduce(T v, F f) {
@@ -59,18 +62,17 @@ MOE_DEV int expert_at(int g, int i) {
   return VEC ? 4 * (g + L * (i / 4)) + i % 4 : g + L * i;
 }
 
-// One token's softmax: p[i] of the lane's experts and lse; false (p zero)
-// if the logits are all -infinity.  Experts past E have p 0.
-template <int L, bool VEC>
-MOE_DEV bool token_softmax(const float* __restrict__ row, int E, int g, float (&p)[kPer],
-                           float& lse) {
-  constexpr float kNegInf = -__builtin_inff();
+constexpr float kNegInf = -__builtin_inff();
+
+// The lane's logits of a token; those past E are -infinity (loads are made from
+// a clamped place: one behind a condition is waited for before the next).
+template <int L, int P, bool VEC>
+MOE_DEV void token_load(const float* __restrict__ row, int E, int g, float (&p)[P]) {
   if constexpr (VEC) {
     const float4* r4 = reinterpret_cast<const float4*>(row);
 #pragma unroll
-    for (int q = 0; q < kPer / 4; ++q) {
-      float4 v = {kNegInf, kNegInf, kNegInf, kNegInf};
-      if (4 * (g + L * q) < E) v = r4[g + L * q];
+    for (int q = 0; q < P / 4; ++q) {
+      const float4 v = r4[min(g + L * q, E / 4 - 1)];
       p[4 * q] = v.x;
       p[4 * q + 1] = v.y;
       p[4 * q + 2] = v.z;
@@ -78,11 +80,20 @@ MOE_DEV bool token_softmax(const float* __restrict__ row, int E, int g, float (&
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) p[i] = g + L * i < E ? row[g + L * i] : kNegInf;
+    for (int i = 0; i < P; ++i) p[i] = row[min(g + L * i, E - 1)];
   }
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (expert_at<L, VEC>(g, i) >= E) p[i] = kNegInf;
+}
+
+// The token's softmax in place of its logits, and lse; false if the logits are
+// all -infinity.  Experts past E have p 0.
+template <int L, int P>
+MOE_DEV bool token_softmax(float (&p)[P], float& lse) {
   float m = kNegInf;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) m = fmaxf(m, p[i]);
+  for (int i = 0; i < P; ++i) m = fmaxf(m, p[i]);
   m = group_max<L>(m);
   // the maximum of NaN and a number is the number here; a token of NaN
   // alone keeps m at -infinity and is told from an empty one by its logits
@@ -90,7 +101,7 @@ MOE_DEV bool token_softmax(const float* __restrict__ row, int E, int g, float (&
   float z = 0.0f;
   const float mm = m == kNegInf ? 0.0f : m;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+  for (int i = 0; i < P; ++i) {
     p[i] = exp_neg(p[i] - mm);
     z += p[i];
     nan = p[i] != p[i] ? 1.0f : nan;
@@ -99,7 +110,7 @@ MOE_DEV bool token_softmax(const float* __restrict__ row, int E, int g, float (&
   if (m == kNegInf && group_max<L>(nan) == 0.0f) return false;
   const float inv = 1.0f / z;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) p[i] *= inv;
+  for (int i = 0; i < P; ++i) p[i] *= inv;
   lse = mm + logf(z);
   return true;
 }
@@ -108,40 +119,71 @@ constexpr int kMaxLossBlocks = 256;   // workgroups of the loss kernel at most
 constexpr int kLossThreads = 1024;
 constexpr int kLossWaves = kLossThreads / kWave;
 
+// Sum over the workgroup's THREADS, in every thread.
+template <int THREADS, typename T>
+MOE_DEV T sum_all(T v, T* s_wave) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
+  __syncthreads();
+  if (threadIdx.x % kWave == 0) s_wave[threadIdx.x / kWave] = v;
+  __syncthreads();
+  T r = 0;
+#pragma unroll
+  for (int i = 0; i < THREADS / kWave; ++i) r += s_wave[i];
+  return r;
+}
+
+struct LossOut {
+  float balance_coef, z_coef;
+  int32_t *counts, *n_tokens;
+  float *prob_mean, *loss;
+  // over n tokens: bal = sum of counts * mean p, z = sum of lse^2
+  MOE_DEV void write(int E, int k, double n, double bal, double z) const {
+    n_tokens[0] = static_cast<int32_t>(n);
+    loss[0] = n > 0.0 ? static_cast<float>(balance_coef * E * bal / (k * n)) : 0.0f;
+    loss[1] = n > 0.0 ? static_cast<float>(z_coef * z / n) : 0.0f;
+  }
+};
+
 // Partials of one workgroup: {sum of p, picks} per expert, {sum lse^2, n}.
-template <int L, bool VEC>
+template <int L, int P, bool VEC>
 __global__ __launch_bounds__(kLossThreads) void router_loss_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ idx,
     const uint8_t* __restrict__ mask, int T, int E, int k, float2* __restrict__ part,
-    float2* __restrict__ part_z, int32_t* done) {
+    float2* __restrict__ part_z, int32_t* done, LossOut out) {
   constexpr int kTok = kLossThreads / L;   // tokens the workgroup covers at once
-  __shared__ float s_p[kLossWaves * L * kPer];   // the waves' sums, expert-major: at most 64 KB
-  __shared__ int32_t s_c[L * kPer];
+  constexpr int kOwnPicks = (kMaxTopK + L - 1) / L;
+  __shared__ float s_p[kLossWaves * L * P];   // the waves' sums, expert-major: at most 64 KB
+  __shared__ int32_t s_c[L * P];
   __shared__ float s_z[kLossWaves];
   __shared__ int32_t s_n[kLossWaves];
+  __shared__ double s_wave[kLossWaves];
   const int tid = threadIdx.x, g = tid % L, wave = tid / kWave;
   for (int e = tid; e < E; e += kLossThreads) s_c[e] = 0;
   __syncthreads();
-  float sum[kPer] = {};
+  float sum[P] = {};
   float zsum = 0.0f;
   int32_t n = 0;
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok; t0 < T;
        t0 += static_cast<int64_t>(gridDim.x) * kTok) {
     const int64_t t = t0 + tid / L;
-    if (t < T && (!mask || mask[t])) {
-      float p[kPer], lse = 0.0f;
-      if (token_softmax<L, VEC>(logits + t * E, E, g, p, lse)) {
+    if (t >= T) continue;   // whole groups: a token's lanes share t
+    float p[P], lse = 0.0f;
+    int32_t pick[kOwnPicks];
+    token_load<L, P, VEC>(logits + t * E, E, g, p);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) sum[i] += p[i];
-        if (g == 0) {
-          zsum += lse * lse;
-          ++n;
-        }
-        for (int s = g; s < k; s += L) {
-          const int32_t e = idx[t * k + s];
-          if (e >= 0 && e < E) atomicAdd(&s_c[e], 1);   // integers: any order
-        }
+    for (int s = 0; s < kOwnPicks; ++s) pick[s] = idx[t * k + min(g + s * L, k - 1)];
+    const bool keep = !mask || mask[t];
+    if (token_softmax<L, P>(p, lse) && keep) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) sum[i] += p[i];
+      if (g == 0) {
+        zsum += lse * lse;
+        ++n;
       }
+#pragma unroll
+      for (int s = 0; s < kOwnPicks; ++s)
+        if (g + s * L < k && pick[s] >= 0 && pick[s] < E) atomicAdd(&s_c[pick[s]], 1);   // integers: any order
     }
   }
   // the lanes of a wave that hold the same experts (same g), then the waves
@@ -149,7 +191,7 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_kernel(
 #pragma unroll
   for (int o = L; o < kWave; o <<= 1) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum[i] += __shfl_xor(sum[i], o, kWave);
+    for (int i = 0; i < P; ++i) sum[i] += __shfl_xor(sum[i], o, kWave);
   }
 #pragma unroll
   for (int o = 1; o < kWave; o <<= 1) {
@@ -162,25 +204,37 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_kernel(
   }
   if (tid % kWave < L) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < P; ++i) {
       const int e = expert_at<L, VEC>(g, i);
-      if (e < E) s_p[wave * L * kPer + e] = sum[i];
+      if (e < E) s_p[wave * L * P + e] = sum[i];
     }
   }
   __syncthreads();
-  for (int e = tid; e < E; e += kLossThreads) {
-    float v = 0.0f;
+  float z = 0.0f;
+  int32_t m = 0;
 #pragma unroll
-    for (int w = 0; w < kLossWaves; ++w) v += s_p[w * L * kPer + e];
-    part[static_cast<int64_t>(blockIdx.x) * E + e] = float2{v, __int_as_float(s_c[e])};
+  for (int w = 0; w < kLossWaves; ++w) {
+    z += s_z[w];
+    m += s_n[w];
   }
-  if (tid == 0) {
-    float z = 0.0f;
-    int32_t m = 0;
-    for (int w = 0; w < kLossWaves; ++w) {
-      z += s_z[w];
-      m += s_n[w];
+  static_assert(kMaxExperts <= kLossThreads, "an expert a thread");
+  float v = 0.0f;
+  if (tid < E) {
+#pragma unroll
+    for (int w = 0; w < kLossWaves; ++w) v += s_p[w * L * P + tid];
+  }
+  if (gridDim.x == 1) {   // these are the whole sums
+    const double mean = m > 0 ? static_cast<double>(v) / m : 0.0;
+    if (tid < E) {
+      out.counts[tid] = s_c[tid];
+      out.prob_mean[tid] = static_cast<float>(mean);
     }
+    const double bal = sum_all<kLossThreads>(tid < E ? s_c[tid] * mean : 0.0, s_wave);
+    if (tid == 0) out.write(E, k, m, bal, z);
+    return;
+  }
+  if (tid < E) part[static_cast<int64_t>(blockIdx.x) * E + tid] = float2{v, __int_as_float(s_c[tid])};
+  if (tid == 0) {
     part_z[blockIdx.x] = float2{z, __int_as_float(m)};
     if (blockIdx.x == 0) *done = 0;
   }
@@ -188,38 +242,31 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_kernel(
 
 constexpr int kSumExperts = 16;   // experts of a workgroup of the second launch
 
-MOE_DEV double sum_all(double v, double* s_wave) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-  __syncthreads();
-  if (threadIdx.x % kWave == 0) s_wave[threadIdx.x / kWave] = v;
-  __syncthreads();
-  double r = 0.0;
-  for (int i = 0; i < kThreads / kWave; ++i) r += s_wave[i];
-  return r;
-}
-
 // Adds the workgroups' partials: 16 experts a workgroup, 16 threads each, all
 // loads of a thread in flight.  The last workgroup to end adds the balance
 // terms in their order; done was set to 0 by the first launch.
 __global__ __launch_bounds__(kThreads) void router_loss_sum_kernel(
     const float2* __restrict__ part, const float2* __restrict__ part_z, int blocks, int E, int k,
-    float balance_coef, float z_coef, int32_t* __restrict__ counts, int32_t* __restrict__ n_tokens,
-    float* __restrict__ prob_mean, float* __restrict__ loss, int32_t* done, double* terms) {
-  __shared__ double s_wave[kThreads / kWave];
+    LossOut out, int32_t* done, double* terms) {
+  constexpr int kWaves = kThreads / kWave;
+  __shared__ double s_z[kWaves];
+  __shared__ int32_t s_n[kWaves];
   __shared__ double s_p[kThreads];
   __shared__ int32_t s_c[kThreads];
-  __shared__ int s_last;
   constexpr int kRows = kThreads / kSumExperts, U = kMaxLossBlocks / kRows;
   const int tid = threadIdx.x, e = blockIdx.x * kSumExperts + tid % kSumExperts;
+  // (loads from a clamped place, the value dropped after: a load behind a
+  // condition is waited for before the next one, 9.8 us in all against 4.7)
   float2 v[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int b = tid / kSumExperts + u * kRows;
-    v[u] = b < blocks && e < E ? part[static_cast<int64_t>(b) * E + e] : float2{0.0f, 0.0f};
-  }
+  for (int u = 0; u < U; ++u)
+    v[u] = part[static_cast<int64_t>(min(tid / kSumExperts + u * kRows, blocks - 1)) * E + min(e, E - 1)];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (tid / kSumExperts + u * kRows >= blocks || e >= E) v[u] = float2{0.0f, 0.0f};
   static_assert(kMaxLossBlocks == kThreads, "one partial a thread");
-  const float2 zn = tid < blocks ? part_z[tid] : float2{0.0f, 0.0f};
+  float2 zn = part_z[min(tid, blocks - 1)];
+  if (tid >= blocks) zn = float2{0.0f, 0.0f};
   double p = 0.0;
   int32_t c = 0;
 #pragma unroll
@@ -227,10 +274,28 @@ __global__ __launch_bounds__(kThreads) void router_loss_sum_kernel(
     p += v[u].x;
     c += __float_as_int(v[u].y);
   }
+  double z = zn.x;
+  int32_t n = __float_as_int(zn.y);
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    z += __shfl_xor(z, o, kWave);
+    n += __shfl_xor(n, o, kWave);
+  }
   s_p[tid] = p;
   s_c[tid] = c;
-  const double z = sum_all(zn.x, s_wave);
-  const double nd = sum_all(__float_as_int(zn.y), s_wave);   // an integer below 2^31: exact
+  if (tid % kWave == 0) {
+    s_z[tid / kWave] = z;
+    s_n[tid / kWave] = n;
+  }
+  __syncthreads();
+  if (tid >= kWave) return;   // the first wave does the rest
+  z = 0.0;
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    z += s_z[w];
+    n += s_n[w];
+  }
   double bal = 0.0;
   if (tid < kSumExperts && e < E) {
     p = 0.0;
@@ -240,31 +305,30 @@ __global__ __launch_bounds__(kThreads) void router_loss_sum_kernel(
       p += s_p[i * kSumExperts + tid];
       c += s_c[i * kSumExperts + tid];
     }
-    const double mean = nd > 0.0 ? p / nd : 0.0;
-    counts[e] = c;
-    prob_mean[e] = static_cast<float>(mean);
+    const double mean = n > 0 ? p / n : 0.0;
+    out.counts[e] = c;
+    out.prob_mean[e] = static_cast<float>(mean);
     bal = c * mean;
   }
-  bal = sum_all(bal, s_wave);
+#pragma unroll
+  for (int o = kSumExperts / 2; o > 0; o >>= 1) bal += __shfl_xor(bal, o, kWave);
+  int last = 0;
   if (tid == 0) {
     __hip_atomic_store(&terms[blockIdx.x], bal, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     const int before = __hip_atomic_fetch_add(done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    s_last = before == static_cast<int>(gridDim.x) - 1;
+    last = before == static_cast<int>(gridDim.x) - 1;
   }
-  __syncthreads();
-  if (!s_last) return;
-  const double t = tid < static_cast<int>(gridDim.x)
-                       ? __hip_atomic_load(&terms[tid], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
-                       : 0.0;
-  const double all = sum_all(t, s_wave);
-  if (tid == 0) {
-    n_tokens[0] = static_cast<int32_t>(nd);
-    loss[0] = nd > 0.0 ? static_cast<float>(balance_coef * E * all / (k * nd)) : 0.0f;
-    loss[1] = nd > 0.0 ? static_cast<float>(z_coef * z / nd) : 0.0f;
-  }
+  if (!__shfl(last, 0, kWave)) return;
+  static_assert(kMaxExperts / kSumExperts <= kWave, "a workgroup's term a lane");
+  double all = tid < static_cast<int>(gridDim.x)
+                   ? __hip_atomic_load(&terms[tid], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                   : 0.0;
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o, kWave);
+  if (tid == 0) out.write(E, k, n, all, z);
 }
 
-template <int L, bool VEC>
+template <int L, int P, bool VEC>
 __global__ __launch_bounds__(kThreads) void router_bwd_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ idx,
     const uint8_t* __restrict__ mask, const float* __restrict__ dprobs,
@@ -276,22 +340,19 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(
   // through LDS: comparing every logit with every pick costs three times the
   // rest of the kernel for 256 experts
   constexpr bool kSpread = L >= kMaxTopK;
-  __shared__ __attribute__((aligned(16))) float s_d[kSpread ? kThreads * kPer : 4];
+  __shared__ __attribute__((aligned(16))) float s_d[kSpread ? kThreads * P : 4];
   const int tid = threadIdx.x, g = tid % L;
-  float* row_d = s_d + (kSpread ? tid / L * L * kPer : 0);
-  const double n = n_tokens ? *n_tokens : 0;
-  float cb[kPer] = {}, cz = 0.0f;   // the balance term of v, and 2 c_z / n
-  if (n > 0.0) {
-    const double b = balance_coef * (dloss ? static_cast<double>(dloss[0]) : 1.0) * E / (k * n * n);
-    cz = static_cast<float>(2.0 * z_coef * (dloss ? static_cast<double>(dloss[1]) : 1.0) / n);
-    if (counts) {
+  float* row_d = s_d + (kSpread ? tid / L * L * P : 0);
+  // what the loss terms take, read now and used when the first token is there
+  const int32_t n_read = n_tokens ? *n_tokens : 0;
+  const float dl0 = dloss ? dloss[0] : 1.0f, dl1 = dloss ? dloss[1] : 1.0f;
+  int32_t count[P] = {};
+  if (counts) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int e = expert_at<L, VEC>(g, i);
-        if (e < E) cb[i] = static_cast<float>(b * counts[e]);
-      }
-    }
+    for (int i = 0; i < P; ++i) count[i] = counts[min(expert_at<L, VEC>(g, i), E - 1)];   // (past E its p is 0)
   }
+  float cb[P] = {}, cz = 0.0f;   // the balance term of v, and 2 c_z / n
+  bool ready = false;
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok; t0 < T;
        t0 += static_cast<int64_t>(gridDim.x) * kTok) {
     const int64_t t = t0 + tid / L;
@@ -299,27 +360,41 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(
     // the picks: one a lane, or all in every lane of a small group
     constexpr int kOwnPicks = L >= kMaxTopK ? 1 : kMaxTopK;
     int32_t pe[kOwnPicks];
-    float pd[kOwnPicks];
+    float pd[kOwnPicks] = {};
 #pragma unroll
     for (int s = 0; s < kOwnPicks; ++s) {
       const int at = L >= kMaxTopK ? g : s;
-      const bool in = dprobs && at < k;
-      pe[s] = in ? idx[t * k + at] : -1;
-      pd[s] = in ? dprobs[t * k + at] : 0.0f;
+      pe[s] = idx[t * k + min(at, k - 1)];
+      if (at >= k || !dprobs) pe[s] = -1;
     }
-    float p[kPer], lse = 0.0f;
-    const bool any = token_softmax<L, VEC>(logits + t * E, E, g, p, lse);
-    const bool kept = any && (!mask || mask[t]);
-    float v[kPer];
+    if (dprobs) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = kept ? cb[i] : 0.0f;
+      for (int s = 0; s < kOwnPicks; ++s) pd[s] = dprobs[t * k + min(L >= kMaxTopK ? g : s, k - 1)];
+    }
+    float p[P], lse = 0.0f;
+    token_load<L, P, VEC>(logits + t * E, E, g, p);
+    const bool keep = !mask || mask[t];
+    const bool any = token_softmax<L, P>(p, lse);
+    const bool kept = any && keep;
+    if (!ready) {
+      ready = true;
+      if (n_read > 0) {
+        const double n = n_read, b = balance_coef * static_cast<double>(dl0) * E / (k * n * n);
+        cz = static_cast<float>(2.0 * z_coef * static_cast<double>(dl1) / n);
+#pragma unroll
+        for (int i = 0; i < P; ++i) cb[i] = static_cast<float>(b * count[i]);
+      }
+    }
+    float v[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = kept ? cb[i] : 0.0f;
     if (dprobs) {
       if constexpr (kSpread) {
         // lane s < k: the sum over the slots with its expert, written by the
         // first of them (one wave: LDS operations complete in order)
         float4* row4 = reinterpret_cast<float4*>(row_d);
 #pragma unroll
-        for (int q = 0; q < kPer / 4; ++q) row4[g + L * q] = float4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int q = 0; q < P / 4; ++q) row4[g + L * q] = float4{0.0f, 0.0f, 0.0f, 0.0f};
         float d = 0.0f;
         bool first = pe[0] >= 0 && pe[0] < E;
 #pragma unroll
@@ -336,7 +411,7 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(
         asm volatile("" ::: "memory");
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) v[i] += row_d[expert_at<L, VEC>(g, i)];
+        for (int i = 0; i < P; ++i) v[i] += row_d[expert_at<L, VEC>(g, i)];
         asm volatile("" ::: "memory");
         __builtin_amdgcn_wave_barrier();
       } else {
@@ -344,7 +419,7 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(
         for (int s = 0; s < kMaxTopK; ++s) {
           if (s < k) {
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
+            for (int i = 0; i < P; ++i)
               v[i] += expert_at<L, VEC>(g, i) == pe[s % kOwnPicks] ? pd[s % kOwnPicks] : 0.0f;
           }
         }
@@ -352,27 +427,27 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(
     }
     float dot = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) dot += p[i] * v[i];
+    for (int i = 0; i < P; ++i) dot += p[i] * v[i];
     dot = group_sum<L>(dot) - (kept ? cz * lse : 0.0f);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = any ? p[i] * (v[i] - dot) : 0.0f;
+    for (int i = 0; i < P; ++i) v[i] = any ? p[i] * (v[i] - dot) : 0.0f;
     float* out = dlogits + t * E;
     if constexpr (VEC) {
 #pragma unroll
-      for (int q = 0; q < kPer / 4; ++q)
+      for (int q = 0; q < P / 4; ++q)
         if (4 * (g + L * q) < E)
           reinterpret_cast<float4*>(out)[g + L * q] =
               float4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
     } else {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
+      for (int i = 0; i < P; ++i)
         if (g + L * i < E) out[g + L * i] = v[i];
     }
   }
 }
 
-// Lanes per token: at most kPer logits each.
-int lanes_of(int E) { return E <= kPer ? 1 : E <= 4 * kPer ? 4 : E <= 16 * kPer ? 16 : 64; }
+// Lanes per token.
+int lanes_of(int E) { return E <= 4 ? 1 : E <= 16 ? 4 : E <= 256 ? 16 : 64; }
 
 bool rows_vec(const void* p, int E) {
   return E % 4 == 0 && (reinterpret_cast<uintptr_t>(p) & 15) == 0;
@@ -380,14 +455,16 @@ bool rows_vec(const void* p, int E) {
 
 template <typename F>
 void with_lanes(int E, bool vec, F&& f) {
-  auto go = [&](auto l) {
-    if (vec) f(l, std::true_type{}); else f(l, std::false_type{});
+  auto go = [&](auto l, auto per) {
+    if (vec) f(l, per, std::true_type{}); else f(l, per, std::false_type{});
   };
+  std::integral_constant<int, 4> four;
+  std::integral_constant<int, 16> sixteen;
   switch (lanes_of(E)) {
-    case 1: go(std::integral_constant<int, 1>{}); break;
-    case 4: go(std::integral_constant<int, 4>{}); break;
-    case 16: go(std::integral_constant<int, 16>{}); break;
-    default: go(std::integral_constant<int, 64>{}); break;
+    case 1: go(std::integral_constant<int, 1>{}, four); break;
+    case 4: go(four, four); break;
+    case 16: if (E <= 64) go(sixteen, four); else go(sixteen, sixteen); break;
+    default: go(std::integral_constant<int, 64>{}, sixteen); break;
   }
 }
 
@@ -415,14 +492,14 @@ hipError_t launch_router_loss(const moe_router_loss_args& a, hipStream_t s) {
   int32_t* done = reinterpret_cast<int32_t*>(terms + blocks2);
   float2* part_z = reinterpret_cast<float2*>(terms + blocks2 + 1);
   float2* part = part_z + blocks;
-  with_lanes(a.E, rows_vec(a.logits, a.E), [&](auto l, auto vec) {
-    router_loss_kernel<decltype(l)::value, decltype(vec)::value><<<blocks, kLossThreads, 0, s>>>(
-        a.logits, a.expert_idx, a.token_mask, a.T, a.E, a.k, part, part_z, done);
+  const LossOut out{a.balance_coef, a.z_coef, a.counts, a.n_tokens, a.prob_mean, a.loss};
+  with_lanes(a.E, rows_vec(a.logits, a.E), [&](auto l, auto per, auto vec) {
+    router_loss_kernel<decltype(l)::value, decltype(per)::value, decltype(vec)::value>
+        <<<blocks, kLossThreads, 0, s>>>(a.logits, a.expert_idx, a.token_mask, a.T, a.E, a.k, part, part_z, done, out);
   });
+  if (blocks == 1) return hipGetLastError();
   if (hipError_t e = hipGetLastError()) return e;
-  router_loss_sum_kernel<<<blocks2, kThreads, 0, s>>>(part, part_z, blocks, a.E, a.k,
-                                                      a.balance_coef, a.z_coef, a.counts, a.n_tokens,
-                                                      a.prob_mean, a.loss, done, terms);
+  router_loss_sum_kernel<<<blocks2, kThreads, 0, s>>>(part, part_z, blocks, a.E, a.k, out, done, terms);
   return hipGetLastError();
 }
 
@@ -431,8 +508,8 @@ hipError_t launch_router_bwd(const moe_router_bwd_args& a, hipStream_t s) {
   int64_t blocks = (static_cast<int64_t>(a.T) + tok - 1) / tok;
   if (blocks > 2048) blocks = 2048;
   const bool vec = rows_vec(a.logits, a.E) && rows_vec(a.dlogits, a.E);
-  with_lanes(a.E, vec, [&](auto l, auto v) {
-    router_bwd_kernel<decltype(l)::value, decltype(v)::value>
+  with_lanes(a.E, vec, [&](auto l, auto per, auto v) {
+    router_bwd_kernel<decltype(l)::value, decltype(per)::value, decltype(v)::value>
         <<<static_cast<int>(blocks), kThreads, 0, s>>>(
             a.logits, a.expert_idx, a.token_mask, a.dprobs, a.dloss, a.counts, a.n_tokens, a.T, a.E,
             a.k, a.balance_coef, a.z_coef, a.dlogits);
