@@ -35,12 +35,27 @@ int tile_grid(int cu, int margin, int64_t tiles) {
   return g < 1 ? 1 : g;
 }
 
+// 64-token groups of a tile: as many as there may be, but half where that still
+// leaves a CU for every tile, as the wider tile takes twice as long (E=2 T=372
+// N=1824 K=1088: 18.4 us with 256 tokens, 10.4 with 64; where tiles are more than
+// CUs, narrow ones read the weights more often: E=22 N=7632 K=1296, 196 rows,
+// 45.7 us with 128, 55.6 with 64).  `tiles`: how many tiles of 64 g tokens.
+template <typename F>
+int tile_groups(bool f32, int cu, F&& tiles) {
+  int g = moe::fp8_most_groups(f32);
+  while (g > 1 && tiles(g / 2) <= cu) g /= 2;
+  return g;
+}
+
 // Whether the product may cut K: rows that take the tiled kernel, 24 scale
 // blocks at least, and a row buffer (less a group's padding each) that cannot
 // fill the device with tiles.  The second launch costs 7 us also where nothing
 // was cut (E=22 N=352 K=2080, 34 tiles of few rows: 14 us without it, 21 with).
+int64_t rows_estimate(int E, int64_t M_cap) {
+  return std::max<int64_t>(1, M_cap - static_cast<int64_t>(E) * (MOE_GROUP_ALIGN - 1));
+}
 bool cuts_k(int E, int N, int K, int64_t M_cap, int64_t most_rows, int cu) {
-  const int64_t rows = std::max<int64_t>(1, M_cap - static_cast<int64_t>(E) * (MOE_GROUP_ALIGN - 1));
+  const int64_t rows = rows_estimate(E, M_cap);
   return most_rows > 32 && K > 23 * kBlk && ceil_div(rows, 256) * ceil_div(N, kTileN) < cu;
 }
 
@@ -149,10 +164,14 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
     return MOE_ERR_INVALID_ARG;
   const int64_t most = a->max_rows ? std::min<int64_t>(a->max_rows, a->M_cap) : a->M_cap;
   const bool f32 = a->c_type == MOE_TYPE_F32;
-  const int64_t tiles = (ceil_div(a->M_cap, moe::fp8_tile_tokens(f32)) + a->E) * ceil_div(a->N, kTileN);
-  if (tiles > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  const int64_t rows = rows_estimate(a->E, a->M_cap), tiles_n = ceil_div(a->N, kTileN);
+  auto at_most = [&](int g) { return (ceil_div(a->M_cap, 64 * g) + a->E) * tiles_n; };
+  if (at_most(moe::fp8_most_groups(f32)) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   int cu = 0;
   if (moe_status st = moe::current_device(&cu)) return st;
+  // half a tile of every group is filled on average
+  const int groups = tile_groups(f32, cu - a->cu_margin, [&](int g) { return (ceil_div(rows, 64 * g) + a->E / 2) * tiles_n; });
+  const int64_t tiles = at_most(groups);
   if (a->cu_margin >= cu) return MOE_ERR_INVALID_ARG;
   moe::Fp8Args g{};
   g.E = a->E;
@@ -180,7 +199,7 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
                    a->workspace_bytes >= static_cast<size_t>(full) * moe::kFp8PartFloats * sizeof(float);
   if (cut) g.part = static_cast<moe::fp8_f32x4*>(a->workspace);
   const int grid = cut ? full : tile_grid(cu, a->cu_margin, tiles);
-  return launched(moe::launch_fp8_gemm(g, f32, grid, s));
+  return launched(moe::launch_fp8_gemm(g, f32, groups, grid, s));
 }
 
 moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {
@@ -191,10 +210,12 @@ moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {
       !aligned16(a->a) || !aligned16(a->b) || !aligned16(a->c))
     return MOE_ERR_INVALID_ARG;
   const bool f32 = a->c_type == MOE_TYPE_F32;
-  const int64_t tiles = a->E * ceil_div(a->P, moe::fp8_tile_tokens(f32)) * ceil_div(a->Q, kTileN);
-  if (tiles > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  auto count = [&](int g) { return a->E * ceil_div(a->P, 64 * g) * ceil_div(a->Q, kTileN); };
+  if (count(moe::fp8_most_groups(f32)) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   int cu = 0;
   if (moe_status st = moe::current_device(&cu)) return st;
+  const int groups = tile_groups(f32, cu - a->cu_margin, count);
+  const int64_t tiles = count(groups);
   if (a->cu_margin >= cu) return MOE_ERR_INVALID_ARG;
   moe::Fp8Args g{};
   g.E = a->E;
@@ -212,7 +233,7 @@ moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {
   g.accumulate = a->accumulate != 0;
   g.group_m = 4;
   g.err = a->err_flag;
-  return launched(moe::launch_fp8_wgrad(g, f32, tile_grid(cu, a->cu_margin, tiles),
+  return launched(moe::launch_fp8_wgrad(g, f32, groups, tile_grid(cu, a->cu_margin, tiles),
                                         static_cast<hipStream_t>(stream)));
 }
 

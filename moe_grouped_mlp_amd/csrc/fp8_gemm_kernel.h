@@ -609,12 +609,11 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
     if constexpr (JMAX == 4) {
       if (groups == 4) run(std::integral_constant<int, 4>{});
       else if (groups == 3) run(std::integral_constant<int, 3>{});
-      else if (groups == 2) run(std::integral_constant<int, 2>{});
-      else run(std::integral_constant<int, 1>{});
-    } else {
-      if (groups == 2) run(std::integral_constant<int, 2>{});
-      else run(std::integral_constant<int, 1>{});
     }
+    if constexpr (JMAX >= 2) {
+      if (groups == 2) run(std::integral_constant<int, 2>{});
+    }
+    if (groups == 1) run(std::integral_constant<int, 1>{});
   }
 }
 

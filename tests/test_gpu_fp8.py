@@ -27,7 +27,6 @@ from .gpu_util import dev_bf16
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda"
-NAN_BITS = 0x7FC1
 
 
 def setup_module(module):
@@ -436,6 +435,27 @@ def test_product_cut_along_k(sizes, N, K, c_type):
     assert torch.equal(c, _product(*ops, sizes, starts, c_type))
 
 
+def _margin(leave):
+    """All CUs but `leave`: the fewer are left, the wider the tiles."""
+    return torch.cuda.get_device_properties(0).multi_processor_count - leave
+
+
+@pytest.mark.parametrize("c_type", [mg.TYPE_F32, mg.TYPE_BF16])
+@pytest.mark.parametrize("leave", [1, 5, 9, 20])
+@pytest.mark.parametrize("name", ["around_16_32", "around_64_128", "around_256", "empty"])
+def test_product_every_tile_width(name, leave, c_type):
+    sizes, N, K = SIZES[name], 272, 400
+    rng = np.random.default_rng(leave)
+    starts = _starts(sizes)
+    ops = _operands(rng, sizes, starts, max(128, starts[-1]), N, K, exact=True)
+    ref, _ = _reference(*ops, sizes, starts)
+    want = ref if c_type == mg.TYPE_F32 else nu.round_bf16(ref)
+    for workspace in (False, True):
+        c = _product(*ops, sizes, starts, c_type, 0, workspace=workspace, cu_margin=_margin(leave)).double().cpu().numpy()
+        np.testing.assert_array_equal(c[~np.isnan(ref)], want[~np.isnan(ref)])
+        assert (c[np.isnan(ref)] == -77.0).all()
+
+
 # -------------------------------------------------------- weight gradient --
 def _wgrad_operands(rng, sizes, starts, M_cap, P, Q, exact=False):
     nb = M_cap // 128
@@ -511,6 +531,19 @@ def test_wgrad_random(name, c_type):
         tol = tol + 7 * 2.0 ** -13 * mag
         tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
     assert (np.abs(c - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("c_type", [mg.TYPE_F32, mg.TYPE_BF16])
+@pytest.mark.parametrize("leave", [1, 20, 40, 80])
+@pytest.mark.parametrize("name", WSIZES)
+def test_wgrad_every_tile_width(name, leave, c_type):
+    sizes, P, Q = WSIZES[name], 592, 272
+    starts = _starts(sizes)
+    rng = np.random.default_rng(leave)
+    ops = _wgrad_operands(rng, sizes, starts, max(256, starts[-1] + 128), P, Q, exact=True)
+    ref, _ = _wgrad_ref(*ops, sizes, starts)
+    c = _wgrad(*ops, sizes, starts, c_type, cu_margin=_margin(leave)).double().cpu().numpy()
+    np.testing.assert_array_equal(c, ref if c_type == mg.TYPE_F32 else nu.round_bf16(ref))
 
 
 @pytest.mark.parametrize("split,pad,M_cap,cut", [
