@@ -82,6 +82,10 @@ MOE_DEV Span span_of(const GradEntry& t, int64_t chunk, int64_t chunks) {
   return s;
 }
 
+// Loads past a chunk's end are made from its last group and dropped: one
+// behind a condition would be waited for before the next.
+MOE_DEV int64_t clamped(int64_t i, int64_t n) { return i < n ? i : n - 1; }
+
 template <typename T>
 MOE_DEV double chunk_sumsq(const GradEntry& t, int64_t chunk, int64_t chunks) {
   const T* p = static_cast<const T*>(t.data);
@@ -92,10 +96,10 @@ MOE_DEV double chunk_sumsq(const GradEntry& t, int64_t chunk, int64_t chunks) {
   for (int64_t i = threadIdx.x; i < vecs; i += kThreads * kVecs) {
     uint4 w[kVecs];
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-      w[j] = i + j * kThreads < vecs ? v[i + j * kThreads] : uint4{0, 0, 0, 0};
+    for (int j = 0; j < kVecs; ++j) w[j] = v[clamped(i + j * kThreads, vecs)];
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
+      if (i + j * kThreads >= vecs) w[j] = uint4{0, 0, 0, 0};
       float f[Vec<T>::n];
       Vec<T>::unpack(w[j], f);
 #pragma unroll
@@ -127,8 +131,7 @@ MOE_DEV void chunk_scale(const GradEntry& t, int64_t chunk, int64_t chunks, F f)
   for (int64_t i = threadIdx.x; i < vecs; i += kThreads * kVecs) {
     uint4 u[kVecs];
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-      if (i + j * kThreads < vecs) u[j] = v[i + j * kThreads];
+    for (int j = 0; j < kVecs; ++j) u[j] = v[clamped(i + j * kThreads, vecs)];
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       if (i + j * kThreads < vecs) {
