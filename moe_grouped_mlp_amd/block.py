@@ -635,10 +635,13 @@ class ExpertBlock:
         """[balance loss, z loss] (fp32 [2]) of the router's logits [T][E_total]
         and the picks (route_logits()'s by default); token_mask [T] leaves
         tokens with 0 out.  Also fills router_counts, router_tokens and
-        router_prob_mean, and keeps what router_backward() needs."""
+        router_prob_mean, and keeps references to its arguments for
+        router_backward()."""
         T, E_all = logits.shape
         idx = self.expert_idx if expert_idx is None else expert_idx
-        if getattr(self, "router_counts", None) is None or self.router_counts.numel() != E_all:
+        if tuple(idx.shape) != (T, self.k):
+            raise ValueError(f"expert_idx must be [{T}][{self.k}], one row for each of the logits'")
+        if getattr(self, "dlogits", None) is None or self.dlogits.shape != logits.shape:
             dev = logits.device
             self.router_counts = torch.empty(E_all, dtype=torch.int32, device=dev)
             self.router_tokens = torch.empty(1, dtype=torch.int32, device=dev)
@@ -661,8 +664,11 @@ class ExpertBlock:
         kept probabilities (backward()'s dprobs by default)."""
         if getattr(self, "_router_args", None) is None:
             raise RuntimeError("router_backward() needs router_loss() first")
+        dprobs = self.dprobs if dprobs is None else dprobs
+        if tuple(dprobs.shape) != (self._router_args["T"], self.k):
+            raise ValueError(f"dprobs must be [{self._router_args['T']}][{self.k}]")
         B.moe_router_bwd(**self._router_args, dloss=dloss,
-                         dprobs=self.dprobs if dprobs is None else dprobs, dlogits=self.dlogits)
+                         dprobs=dprobs, dlogits=self.dlogits)
         return self.dlogits
 
     def clip_grads(self, max_norm: float, extra=()):

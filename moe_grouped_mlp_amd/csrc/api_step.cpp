@@ -127,10 +127,9 @@ moe_status moe_quantize_fp8(const moe_quant_fp8_args* a, void* stream) {
   const int64_t n = static_cast<int64_t>(a->rows) * a->cols;
   if (a->x_stride != 0 && (a->x_stride < n || a->x_stride % 8 != 0)) return MOE_ERR_INVALID_ARG;
   const int64_t cb = ceil_div(a->cols, kBlk);
-  const int64_t units = a->mode == MOE_QUANT_ROW ? ceil_div(a->rows, 16) * cb
+  const int64_t units = a->mode == MOE_QUANT_ROW ? ceil_div(a->rows, 16) * ceil_div(cb, 8)
                                                  : ceil_div(a->rows, kBlk) * cb;
-  if (a->batch > 65535 || units >= kMaxGridX * (a->mode == MOE_QUANT_ROW ? 8 : 1))
-    return MOE_ERR_UNSUPPORTED;
+  if (a->batch > 65535 || units >= kMaxGridX) return MOE_ERR_UNSUPPORTED;
   int cu = 0;
   if (moe_status st = moe::current_device(&cu)) return st;
   if (a->batch == 0 || a->rows == 0) return MOE_OK;
@@ -191,7 +190,7 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
   g.group_m = 4;
   g.err = a->err_flag;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (most <= 32) return launched(moe::launch_fp8_rows(g, most <= 16 ? 16 : 32, f32, s));
+  if (most <= 32 && a->N / 32 < kMaxGridX - 1) return launched(moe::launch_fp8_rows(g, most <= 16 ? 16 : 32, f32, s));
   // K may be cut where there is room for its parts; the grid is a full one
   // then, since the tiles' number is known on the device only
   const int full = tile_grid(cu, a->cu_margin, INT32_MAX);

@@ -130,6 +130,14 @@ class Args {
   void* stream() {
     PyObject* s = next();
     if (PyLong_Check(s)) return pointer(s);
+    if (s != Py_None) {   // a Stream object: of the current device
+      PyObject* d = PyObject_GetAttrString(s, "device_index");
+      if (!d) throw Raised{};
+      const long on = PyLong_AsLong(d);
+      Py_DECREF(d);
+      if (on == -1 && PyErr_Occurred()) throw Raised{};
+      if (on != dev_) refuse("the stream is of another device (cuda:" + std::to_string(on) + ")");
+    }
     PyObject* h = s == Py_None ? PyObject_CallOneArg(g_raw_stream, a_[0]) : PyObject_GetAttrString(s, "cuda_stream");
     if (!h) throw Raised{};
     void* p = PyLong_AsVoidPtr(h);
@@ -139,7 +147,8 @@ class Args {
   }
 
  private:
-  bool here(const at::Tensor& t) const { return t.get_device() == dev_ && t.is_contiguous(); }
+  // (a view with a pending negation, say x.imag of a conjugate, is no plain memory)
+  bool here(const at::Tensor& t) const { return t.get_device() == dev_ && t.is_contiguous() && !t.is_neg(); }
   void at_home(const at::Tensor& t) const {
     if (!here(t))
       refuse("the tensors must be contiguous and on the current device (cuda:" + std::to_string(dev_) + ")");

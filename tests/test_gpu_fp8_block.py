@@ -192,6 +192,16 @@ def test_refusals():
     x, dout, w1, w2, logits = _inputs(4, 128, 256, 128, 16, 5)
     with pytest.raises(RuntimeError):
         blk.router_backward()
+    with pytest.raises(ValueError):   # picks of other tokens than the logits'
+        blk.router_loss(logits, expert_idx=torch.zeros(15, 2, dtype=torch.int32, device=DEV))
+    with pytest.raises(ValueError):
+        blk.router_loss(logits, expert_idx=torch.zeros(16, 4, dtype=torch.int32, device=DEV))
+    blk.router_loss(logits, expert_idx=torch.zeros(16, 2, dtype=torch.int32, device=DEV))
+    with pytest.raises(ValueError):
+        blk.router_backward(dprobs=torch.zeros(16, 4, device=DEV))
+    # logits of another batch: outputs of that size
+    blk.router_loss(logits[:5].clone(), expert_idx=torch.zeros(5, 2, dtype=torch.int32, device=DEV))
+    assert blk.router_backward(dprobs=torch.zeros(5, 2, device=DEV)).shape == (5, 4)
     for f in (blk.weight_grads, lambda: blk.clip_grads(1.0)):
         with pytest.raises(RuntimeError):
             f()

@@ -265,3 +265,29 @@ def test_binding_refuses_other_arguments():
             m.moe_router_bwd(T=-1, E=8, k=2, expert_idx=idx, logits=f32, dlogits=f32, stream=0)
         with pytest.raises(AttributeError):
             m.moe_router_bwd(T=4, E=8, k=2, expert_idx=idx, logits=f32, dlogits=f32, stream="x")
+
+
+@no_device
+def test_sizes_past_a_launch():
+    """Grids that a launch cannot hold are refused; the largest that fit are not."""
+    for mode, rows, cols, want in ((m.QUANT_ROW, 2 ** 31 - 1, 16, UNSUPPORTED),
+                                   (m.QUANT_ROW, 2 ** 28 - 16, 1024, DEVICE),
+                                   (m.QUANT_BOTH, 2 ** 31 - 128, 16, DEVICE),
+                                   (m.QUANT_BOTH, 2 ** 31 - 128, 144, UNSUPPORTED)):
+        a = B.QuantFp8Args(mode, 1, rows, cols, 0, 4096, 8192, 64, 4096, 64, 0, None, None)
+        assert _call("moe_quantize_fp8", a) == want, (mode, rows, cols)
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    import types
+    import unittest.mock as mock
+    f32, idx = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+    with mock.patch.object(B, "_device", lambda: (B._setup(), -1)[1]):
+        with pytest.raises(ValueError, match="another device"):
+            m.moe_router_bwd(T=4, E=8, k=2, expert_idx=idx, logits=f32, dlogits=f32,
+                             stream=types.SimpleNamespace(cuda_stream=0, device_index=3))
+        neg = torch.zeros(32, dtype=torch.complex64).conj().imag   # a pending negation
+        assert neg.is_neg()
+        with pytest.raises(ValueError):
+            m.moe_grad_sumsq(tensors=[neg], sumsq=torch.zeros(1, dtype=torch.float64),
+                             workspace=torch.zeros(64, dtype=torch.uint8))
