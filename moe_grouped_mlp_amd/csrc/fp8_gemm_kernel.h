@@ -216,7 +216,7 @@ struct Fp8Loader {
 // The tiles of all experts in their order, from the sizes on the device.
 struct Fp8Tables {
   int start[kMaxExperts + 1];   // an expert's first tile
-  int rows[kMaxExperts];
+  int rows[kMaxExperts], at[kMaxExperts];   // its rows and the first of them
   int tmp[kFp8Waves];
 };
 template <int BT, bool WG>
@@ -233,6 +233,7 @@ MOE_DEV int fp8_tile_prefix(const Fp8Args& g, Fp8Tables& s) {
       const int n = fp8_group_rows(g, e, WG, bad);
       if (bad && blockIdx.x == 0) set_err(g.err, MOE_DEVERR_BAD_OFFSETS);
       s.rows[e] = n;
+      s.at[e] = g.padded[e];
       mine += tiles_of(n);
     }
   }
@@ -267,16 +268,17 @@ struct Fp8Tile {
 };
 template <int BT, bool WG>
 MOE_DEV Fp8Tile fp8_tile_at(const Fp8Args& g, const Fp8Tables& s, int id) {
-  int lo = 0, hi = g.E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s.start[mid] <= id) lo = mid; else hi = mid - 1;
+  // the last expert that starts at id or before: 64 a comparison
+  int lo = -1;
+  for (int e0 = 0; e0 < g.E; e0 += kWave) {
+    const int e = e0 + (threadIdx.x & (kWave - 1));
+    lo += __popcll(__ballot(e < g.E && s.start[e < g.E ? e : 0] <= id));
   }
   Fp8Tile t;
   t.e = __builtin_amdgcn_readfirstlane(lo);
   const int in_e = __builtin_amdgcn_readfirstlane(id - s.start[lo]);
   t.n_e = __builtin_amdgcn_readfirstlane(s.rows[lo]);
-  t.start = __builtin_amdgcn_readfirstlane(g.padded[lo]);
+  t.start = __builtin_amdgcn_readfirstlane(s.at[lo]);
   t.rows_t = WG ? g.P : t.n_e;
   // bands of group_m token tiles, all weight tiles of a band in turn
   const int tiles_n = (g.N + kFp8BN - 1) / kFp8BN;
