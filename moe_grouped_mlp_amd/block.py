@@ -102,6 +102,7 @@ class ExpertBlock:
         # passes with every operand quantized by moe_quantize_mxfp4
         self.mx4 = prec == B.PREC_MXFP4
         self.fp8 = prec == B.PREC_FP8
+        self._router_bufs, self._ws_grad, self.grad_norm = {}, {}, None
         if self.fp8 and (recompute or unfused):
             raise ValueError("the FP8 layer has no recompute path, and always runs as separate passes")
         if wgrad_type != B.TYPE_BF16 and not self.fp8:
@@ -641,15 +642,20 @@ class ExpertBlock:
         idx = self.expert_idx if expert_idx is None else expert_idx
         if tuple(idx.shape) != (T, self.k):
             raise ValueError(f"expert_idx must be [{T}][{self.k}], one row for each of the logits'")
-        if getattr(self, "dlogits", None) is None or self.dlogits.shape != logits.shape:
+        # buffers of every shape stay as long as the block: a graph captured with
+        # one shape still writes them after a call with another
+        bufs = self._router_bufs.get((T, E_all))
+        if bufs is None:
             dev = logits.device
-            self.router_counts = torch.empty(E_all, dtype=torch.int32, device=dev)
-            self.router_tokens = torch.empty(1, dtype=torch.int32, device=dev)
-            self.router_prob_mean = torch.empty(E_all, dtype=torch.float32, device=dev)
-            self.router_losses = torch.empty(2, dtype=torch.float32, device=dev)
-            self.dlogits = torch.empty(T, E_all, dtype=torch.float32, device=dev)
-            self.ws_loss = torch.empty(B.moe_router_loss_workspace_size(T, E_all),
-                                       dtype=torch.uint8, device=dev)
+            bufs = self._router_bufs[T, E_all] = dict(
+                router_counts=torch.empty(E_all, dtype=torch.int32, device=dev),
+                router_tokens=torch.empty(1, dtype=torch.int32, device=dev),
+                router_prob_mean=torch.empty(E_all, dtype=torch.float32, device=dev),
+                router_losses=torch.empty(2, dtype=torch.float32, device=dev),
+                dlogits=torch.empty(T, E_all, dtype=torch.float32, device=dev),
+                ws_loss=torch.empty(B.moe_router_loss_workspace_size(T, E_all),
+                                    dtype=torch.uint8, device=dev))
+        self.__dict__.update(bufs)
         self._router_args = dict(T=T, E=E_all, k=self.k, logits=logits, expert_idx=idx,
                                  token_mask=token_mask, balance_coef=balance_coef, z_coef=z_coef,
                                  counts=self.router_counts, n_tokens=self.router_tokens)
@@ -679,12 +685,13 @@ class ExpertBlock:
             raise RuntimeError("ExpertBlock was built without wgrad=True")
         grads = [self.dw1, self.dw2, *extra]
         need = B.moe_grad_workspace_size(len(grads))
-        if getattr(self, "ws_grad", None) is None or self.ws_grad.numel() < need:
-            dev = self.dw1.device
-            self.ws_grad = torch.empty(need, dtype=torch.uint8, device=dev)
+        dev = self.dw1.device
+        if self.grad_norm is None:
             self.grad_sumsq = torch.empty(1, dtype=torch.float64, device=dev)
             self.grad_norm = torch.empty(1, dtype=torch.float32, device=dev)
-        B.moe_grad_sumsq(tensors=grads, sumsq=self.grad_sumsq, workspace=self.ws_grad)
+        if need not in self._ws_grad:   # (kept for captured graphs, as above)
+            self._ws_grad[need] = torch.empty(need, dtype=torch.uint8, device=dev)
+        B.moe_grad_sumsq(tensors=grads, sumsq=self.grad_sumsq, workspace=self._ws_grad[need])
         B.moe_grad_clip(tensors=grads, sumsq=self.grad_sumsq, max_norm=max_norm,
                         norm=self.grad_norm, err_flag=self.err_flag)
         return self.grad_norm

@@ -251,3 +251,44 @@ def test_whole_step_in_a_graph():
         torch.cuda.synchronize()
         for n, g in zip(names, got):
             assert torch.equal(g, getattr(blk, n)), n
+
+
+def test_buffers_of_a_captured_graph_survive_other_shapes():
+    """A graph captured with one shape of logits and list of gradients writes
+    the same buffers after eager calls with others."""
+    E, k, T, H, I = 8, 2, 96, 128, 128
+    blk = mg.ExpertBlock(E, H, I, T, k, prec=mg.PREC_FP8, wgrad=True)
+    x, dout, w1, w2, logits = _inputs(E, H, 2 * I, I, T, 7)
+    blk.load_weights(w1, w2)
+    blk.route_logits(logits)
+    blk.forward(x, blk.expert_idx, blk.probs)
+    blk.backward(dout)
+    blk.weight_grads()
+
+    def tail():
+        blk.router_loss(logits, balance_coef=0.1, z_coef=0.01)
+        blk.router_backward()
+        blk.clip_grads(1e9, extra=[blk.dlogits])
+
+    tail()
+    mine = [blk.dlogits, blk.router_losses, blk.grad_norm]
+    want = [t.clone() for t in mine]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        tail()
+    few = torch.randn(33, E, device=DEV)
+    many = [torch.ones(1000 + i, device=DEV) for i in range(200)]
+    blk.router_loss(few, expert_idx=torch.zeros(33, k, dtype=torch.int32, device=DEV))
+    blk.clip_grads(1e9, extra=many)
+    other = [torch.full((n,), 7.0, device=DEV) for n in (T * E, T * E, 2, 2, 64, 1024, 4096)]   # what a freed buffer would become
+    for t in mine:
+        t.fill_(-1.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(mine, want):
+        assert torch.equal(a, b)
+    assert all(bool((o == 7.0).all()) for o in other)
+    blk.router_loss(logits)
+    assert blk.dlogits is mine[0]
