@@ -157,9 +157,10 @@ MOE_DEV int fp8_swz_w(int row) {
 
 // A group's rows as the kernels see them: cut to what lies between its start,
 // the next start and the buffer's end.
-MOE_DEV int fp8_group_rows(const Fp8Args& g, int e, bool aligned, bool& bad) {
+template <typename A>
+MOE_DEV int fp8_group_rows(const A& g, int e, bool aligned, bool& bad) {
   const int64_t n = g.split[e], p0 = g.padded[e], p1 = g.padded[e + 1];
-  const int64_t end = p1 < g.M_cap ? p1 : g.M_cap;
+  const int64_t cap = g.M_cap, end = p1 < cap ? p1 : cap;
   const int64_t span = aligned ? (n + kFp8Blk - 1) / kFp8Blk * kFp8Blk : n;
   bad = n < 0 || p0 < 0 || p0 + span > end || (aligned && n > 0 && p0 % kFp8Blk != 0);
   if (!bad) return static_cast<int>(n);

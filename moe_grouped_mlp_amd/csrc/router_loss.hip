@@ -19,7 +19,7 @@
 // Bound by latencies: a workgroup makes one or a few passes, so all it reads
 // goes out at once, before the first use.  16384 tokens of 256 experts: 8.2 us
 // for the partials (16.8 MB read), 4.7 for their sums, 11.7 for the gradient
-// (33.6 MB, 2.9 TB/s); 256 tokens of 4: 4.8 and 2.8 in one launch each.
+// (33.6 MB, 2.9 TB/s); 256 tokens of 4: 3.4 and 2.8 in one launch each.
 #include <type_traits>
 
 #include "common.h"
@@ -117,7 +117,10 @@ MOE_DEV bool token_softmax(float (&p)[P], float& lse) {
 
 constexpr int kMaxLossBlocks = 256;   // workgroups of the loss kernel at most
 constexpr int kLossThreads = 1024;
-constexpr int kLossWaves = kLossThreads / kWave;
+// threads of a single workgroup that covers all tokens in one pass: starting
+// and joining 16 waves costs more than 4 (256 tokens of
+// 4 experts: 4.8 us with 16, 3.4 with 4)
+constexpr int kFewThreads = 256;
 
 // Sum over the workgroup's THREADS, in every thread.
 template <int THREADS, typename T>
@@ -133,6 +136,25 @@ MOE_DEV T sum_all(T v, T* s_wave) {
   return r;
 }
 
+constexpr int kSumExperts = 16;   // experts of a workgroup of the second launch
+__host__ __device__ constexpr int sum_blocks(int E) { return (E + kSumExperts - 1) / kSumExperts; }
+
+// The workspace: the balance terms (fp64) and the count of the second launch's
+// workgroups, then the loss kernel's partials.
+struct LossWs {
+  double* terms;
+  int32_t* done;
+  float2 *part_z, *part;   // {sum lse^2, n} of a workgroup; its {sum of p, picks} per expert
+  MOE_DEV LossWs(void* p, int E, int blocks)
+      : terms(static_cast<double*>(p)),
+        done(reinterpret_cast<int32_t*>(terms + sum_blocks(E))),
+        part_z(reinterpret_cast<float2*>(terms + sum_blocks(E) + 1)),
+        part(part_z + blocks) {}
+};
+
+// (Arguments past about 104 bytes, a kernel's own and those that reading the
+// grid's size adds, cost a launch 0.6 to 1 us of the host's time: hence one
+// workspace pointer, and `blocks` by value.)
 struct LossOut {
   float balance_coef, z_coef;
   int32_t *counts, *n_tokens;
@@ -146,26 +168,25 @@ struct LossOut {
 };
 
 // Partials of one workgroup: {sum of p, picks} per expert, {sum lse^2, n}.
-template <int L, int P, bool VEC>
-__global__ __launch_bounds__(kLossThreads) void router_loss_kernel(
+template <int THREADS, int L, int P, bool VEC>
+__global__ __launch_bounds__(THREADS) void router_loss_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ idx,
-    const uint8_t* __restrict__ mask, int T, int E, int k, float2* __restrict__ part,
-    float2* __restrict__ part_z, int32_t* done, LossOut out) {
-  constexpr int kTok = kLossThreads / L;   // tokens the workgroup covers at once
+    const uint8_t* __restrict__ mask, int T, int E, int k, int blocks, void* ws, LossOut out) {
+  constexpr int kWaves = THREADS / kWave, kTok = THREADS / L;   // tokens the workgroup covers at once
   constexpr int kOwnPicks = (kMaxTopK + L - 1) / L;
-  __shared__ float s_p[kLossWaves * L * P];   // the waves' sums, expert-major: at most 64 KB
+  __shared__ float s_p[kWaves * L * P];   // the waves' sums, expert-major: at most 64 KB
   __shared__ int32_t s_c[L * P];
-  __shared__ float s_z[kLossWaves];
-  __shared__ int32_t s_n[kLossWaves];
-  __shared__ double s_wave[kLossWaves];
+  __shared__ float s_z[kWaves];
+  __shared__ int32_t s_n[kWaves];
+  __shared__ double s_wave[kWaves];
   const int tid = threadIdx.x, g = tid % L, wave = tid / kWave;
-  for (int e = tid; e < E; e += kLossThreads) s_c[e] = 0;
+  for (int e = tid; e < E; e += THREADS) s_c[e] = 0;
   __syncthreads();
   float sum[P] = {};
   float zsum = 0.0f;
   int32_t n = 0;
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok; t0 < T;
-       t0 += static_cast<int64_t>(gridDim.x) * kTok) {
+       t0 += static_cast<int64_t>(blocks) * kTok) {
     const int64_t t = t0 + tid / L;
     if (t >= T) continue;   // whole groups: a token's lanes share t
     float p[P], lse = 0.0f;
@@ -213,41 +234,40 @@ __global__ __launch_bounds__(kLossThreads) void router_loss_kernel(
   float z = 0.0f;
   int32_t m = 0;
 #pragma unroll
-  for (int w = 0; w < kLossWaves; ++w) {
+  for (int w = 0; w < kWaves; ++w) {
     z += s_z[w];
     m += s_n[w];
   }
-  static_assert(kMaxExperts <= kLossThreads, "an expert a thread");
+  static_assert(L * P <= THREADS, "an expert a thread");
   float v = 0.0f;
   if (tid < E) {
 #pragma unroll
-    for (int w = 0; w < kLossWaves; ++w) v += s_p[w * L * P + tid];
+    for (int w = 0; w < kWaves; ++w) v += s_p[w * L * P + tid];
   }
-  if (gridDim.x == 1) {   // these are the whole sums
+  if (blocks == 1) {   // these are the whole sums
     const double mean = m > 0 ? static_cast<double>(v) / m : 0.0;
     if (tid < E) {
       out.counts[tid] = s_c[tid];
       out.prob_mean[tid] = static_cast<float>(mean);
     }
-    const double bal = sum_all<kLossThreads>(tid < E ? s_c[tid] * mean : 0.0, s_wave);
+    const double bal = sum_all<THREADS>(tid < E ? s_c[tid] * mean : 0.0, s_wave);
     if (tid == 0) out.write(E, k, m, bal, z);
     return;
   }
-  if (tid < E) part[static_cast<int64_t>(blockIdx.x) * E + tid] = float2{v, __int_as_float(s_c[tid])};
+  const LossWs w(ws, E, blocks);
+  if (tid < E) w.part[static_cast<int64_t>(blockIdx.x) * E + tid] = float2{v, __int_as_float(s_c[tid])};
   if (tid == 0) {
-    part_z[blockIdx.x] = float2{z, __int_as_float(m)};
-    if (blockIdx.x == 0) *done = 0;
+    w.part_z[blockIdx.x] = float2{z, __int_as_float(m)};
+    if (blockIdx.x == 0) *w.done = 0;
   }
 }
-
-constexpr int kSumExperts = 16;   // experts of a workgroup of the second launch
 
 // Adds the workgroups' partials: 16 experts a workgroup, 16 threads each, all
 // loads of a thread in flight.  The last workgroup to end adds the balance
 // terms in their order; done was set to 0 by the first launch.
-__global__ __launch_bounds__(kThreads) void router_loss_sum_kernel(
-    const float2* __restrict__ part, const float2* __restrict__ part_z, int blocks, int E, int k,
-    LossOut out, int32_t* done, double* terms) {
+__global__ __launch_bounds__(kThreads) void router_loss_sum_kernel(void* ws, int blocks, int E, int k,
+                                                                   LossOut out) {
+  const LossWs w(ws, E, blocks);
   constexpr int kWaves = kThreads / kWave;
   __shared__ double s_z[kWaves];
   __shared__ int32_t s_n[kWaves];
@@ -260,12 +280,12 @@ __global__ __launch_bounds__(kThreads) void router_loss_sum_kernel(
   float2 v[U];
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    v[u] = part[static_cast<int64_t>(min(tid / kSumExperts + u * kRows, blocks - 1)) * E + min(e, E - 1)];
+    v[u] = w.part[static_cast<int64_t>(min(tid / kSumExperts + u * kRows, blocks - 1)) * E + min(e, E - 1)];
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (tid / kSumExperts + u * kRows >= blocks || e >= E) v[u] = float2{0.0f, 0.0f};
   static_assert(kMaxLossBlocks == kThreads, "one partial a thread");
-  float2 zn = part_z[min(tid, blocks - 1)];
+  float2 zn = w.part_z[min(tid, blocks - 1)];
   if (tid >= blocks) zn = float2{0.0f, 0.0f};
   double p = 0.0;
   int32_t c = 0;
@@ -292,9 +312,9 @@ __global__ __launch_bounds__(kThreads) void router_loss_sum_kernel(
   z = 0.0;
   n = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    z += s_z[w];
-    n += s_n[w];
+  for (int i = 0; i < kWaves; ++i) {
+    z += s_z[i];
+    n += s_n[i];
   }
   double bal = 0.0;
   if (tid < kSumExperts && e < E) {
@@ -314,14 +334,14 @@ __global__ __launch_bounds__(kThreads) void router_loss_sum_kernel(
   for (int o = kSumExperts / 2; o > 0; o >>= 1) bal += __shfl_xor(bal, o, kWave);
   int last = 0;
   if (tid == 0) {
-    __hip_atomic_store(&terms[blockIdx.x], bal, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const int before = __hip_atomic_fetch_add(done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    last = before == static_cast<int>(gridDim.x) - 1;
+    __hip_atomic_store(&w.terms[blockIdx.x], bal, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const int before = __hip_atomic_fetch_add(w.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    last = before == sum_blocks(E) - 1;
   }
   if (!__shfl(last, 0, kWave)) return;
   static_assert(kMaxExperts / kSumExperts <= kWave, "a workgroup's term a lane");
-  double all = tid < static_cast<int>(gridDim.x)
-                   ? __hip_atomic_load(&terms[tid], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+  double all = tid < sum_blocks(E)
+                   ? __hip_atomic_load(&w.terms[tid], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
                    : 0.0;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o, kWave);
@@ -333,8 +353,8 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ idx,
     const uint8_t* __restrict__ mask, const float* __restrict__ dprobs,
     const float* __restrict__ dloss, const int32_t* __restrict__ counts,
-    const int32_t* __restrict__ n_tokens, int T, int E, int k, float balance_coef, float z_coef,
-    float* __restrict__ dlogits) {
+    const int32_t* __restrict__ n_tokens, int T, int E, int k, int blocks, float balance_coef,
+    float z_coef, float* __restrict__ dlogits) {
   constexpr int kTok = kThreads / L;
   // the picks' gradients of a token, spread to the lanes of their experts
   // through LDS: comparing every logit with every pick costs three times the
@@ -354,7 +374,7 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(
   float cb[P] = {}, cz = 0.0f;   // the balance term of v, and 2 c_z / n
   bool ready = false;
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok; t0 < T;
-       t0 += static_cast<int64_t>(gridDim.x) * kTok) {
+       t0 += static_cast<int64_t>(blocks) * kTok) {
     const int64_t t = t0 + tid / L;
     if (t >= T) continue;   // whole groups: a token's lanes share t
     // the picks: one a lane, or all in every lane of a small group
@@ -477,29 +497,30 @@ static int loss_blocks(int T, int E) {
   const int64_t b = (static_cast<int64_t>(T) + tok - 1) / tok;
   return static_cast<int>(b < 1 ? 1 : b > kMaxLossBlocks ? kMaxLossBlocks : b);
 }
-static int sum_blocks(int E) { return (E + kSumExperts - 1) / kSumExperts; }
 
-// Workspace: the balance terms (fp64), the counter, {sum lse^2, n} and the
-// experts' partials of every workgroup.
 size_t router_loss_workspace_bytes(int T, int E) {
   const size_t blocks = loss_blocks(T, E);
   return 8 * (sum_blocks(E) + 1 + blocks + blocks * static_cast<size_t>(E));
 }
 
 hipError_t launch_router_loss(const moe_router_loss_args& a, hipStream_t s) {
-  const int blocks = loss_blocks(a.T, a.E), blocks2 = sum_blocks(a.E);
-  double* terms = static_cast<double*>(a.workspace);
-  int32_t* done = reinterpret_cast<int32_t*>(terms + blocks2);
-  float2* part_z = reinterpret_cast<float2*>(terms + blocks2 + 1);
-  float2* part = part_z + blocks;
+  const int blocks = loss_blocks(a.T, a.E);
   const LossOut out{a.balance_coef, a.z_coef, a.counts, a.n_tokens, a.prob_mean, a.loss};
   with_lanes(a.E, rows_vec(a.logits, a.E), [&](auto l, auto per, auto vec) {
-    router_loss_kernel<decltype(l)::value, decltype(per)::value, decltype(vec)::value>
-        <<<blocks, kLossThreads, 0, s>>>(a.logits, a.expert_idx, a.token_mask, a.T, a.E, a.k, part, part_z, done, out);
+    constexpr int kL = decltype(l)::value, kP = decltype(per)::value;
+    auto go = [&](auto kernel, int threads) {
+      kernel<<<blocks, threads, 0, s>>>(a.logits, a.expert_idx, a.token_mask, a.T, a.E, a.k, blocks,
+                                        a.workspace, out);
+    };
+    if constexpr (kL * kP <= kFewThreads) {
+      if (static_cast<int64_t>(a.T) * kL <= kFewThreads)
+        return go(router_loss_kernel<kFewThreads, kL, kP, decltype(vec)::value>, kFewThreads);
+    }
+    go(router_loss_kernel<kLossThreads, kL, kP, decltype(vec)::value>, kLossThreads);
   });
   if (blocks == 1) return hipGetLastError();
   if (hipError_t e = hipGetLastError()) return e;
-  router_loss_sum_kernel<<<blocks2, kThreads, 0, s>>>(part, part_z, blocks, a.E, a.k, out, done, terms);
+  router_loss_sum_kernel<<<sum_blocks(a.E), kThreads, 0, s>>>(a.workspace, blocks, a.E, a.k, out);
   return hipGetLastError();
 }
 
@@ -512,7 +533,7 @@ hipError_t launch_router_bwd(const moe_router_bwd_args& a, hipStream_t s) {
     router_bwd_kernel<decltype(l)::value, decltype(per)::value, decltype(v)::value>
         <<<static_cast<int>(blocks), kThreads, 0, s>>>(
             a.logits, a.expert_idx, a.token_mask, a.dprobs, a.dloss, a.counts, a.n_tokens, a.T, a.E,
-            a.k, a.balance_coef, a.z_coef, a.dlogits);
+            a.k, static_cast<int>(blocks), a.balance_coef, a.z_coef, a.dlogits);
   });
   return hipGetLastError();
 }
