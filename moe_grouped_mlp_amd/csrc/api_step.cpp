@@ -26,6 +26,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool type_ok(int t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_F32; }
+int64_t type_bytes(int t) { return t == MOE_TYPE_BF16 ? 2 : 4; }
 
 // Workgroups of a persistent product over at most `tiles` tiles.
 int tile_grid(int cu, int margin, int64_t tiles) {
@@ -46,6 +47,10 @@ int tile_groups(bool f32, int cu, F&& tiles) {
   while (g > 1 && tiles(g / 2) <= cu) g /= 2;
   return g;
 }
+
+// Whether an output of `rows` rows of `row` bytes is stored past the caches: more
+// than they hold, in whole 128-byte lines.
+int streams(int64_t rows, int64_t row) { return rows * row > moe::kStreamBytes && row % 128 == 0; }
 
 // Whether the product may cut K: rows that take the tiled kernel, 24 scale
 // blocks at least, and a row buffer (less a group's padding each) that cannot
@@ -75,8 +80,6 @@ bool overlap(Range* r, int64_t n) {
   }
   return false;
 }
-
-int64_t type_bytes(int t) { return t == MOE_TYPE_BF16 ? 2 : 4; }
 
 // Checks of the tensor list that both calls share.
 moe_status list_check(const moe_grad_args* a) {
@@ -187,6 +190,7 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
   g.b_s_stride = a->b_s_stride ? a->b_s_stride : ns;
   g.c = a->c;
   g.ldc = a->ldc ? a->ldc : a->N;
+  g.stream = a->M_cap <= (int64_t(1) << 62) / 4 / g.ldc && streams(a->M_cap, g.ldc * type_bytes(a->c_type));
   g.group_m = 4;
   g.err = a->err_flag;
   const hipStream_t s = static_cast<hipStream_t>(stream);
@@ -230,6 +234,7 @@ moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {
   g.c = a->c;
   g.ldc = a->Q;
   g.accumulate = a->accumulate != 0;
+  g.stream = streams(static_cast<int64_t>(a->E) * a->P, static_cast<int64_t>(a->Q) * type_bytes(a->c_type));
   g.group_m = 4;
   g.err = a->err_flag;
   return launched(moe::launch_fp8_wgrad(g, f32, groups, tile_grid(cu, a->cu_margin, tiles),

@@ -54,7 +54,7 @@
 // a 16-cycle MFMA a SIMD issues two vector instructions for nothing, each
 // further one costs 4 cycles (measured with two waves); here they are 4.7 (2.5
 // to widen, 2 to scale), so the MFMAs are busy for a quarter to a third of the
-// time.  32 experts of 7168 x 2048 from 16384 rows (4.5 steps a tile): 860 us,
+// time.  32 experts of 7168 x 2048 from 16384 rows (4.5 steps a tile): 855 us,
 // of which 690 without the stores, 300 the stores (1.88 GB) alone.
 #include <type_traits>
 #include <utility>
@@ -564,7 +564,12 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
       // through LDS of its own (the stages are drained) and stores whole rows of
       // its 128 columns: 235 -> 179 us where an output of 755 MB is all there is
       // to do.  16-byte chunk c of row r lies at c ^ r, so that writes (16 rows,
-      // one chunk) and reads (one row) fall on different banks.
+      // one chunk) and reads (one row) fall on different banks.  Large outputs
+      // (g.stream) pass the caches by, which then hold more of the operands: fp32
+      // weight gradients of 1.88 GB 870 -> 856 us, 89 experts' outputs of 755 MB
+      // 1217 -> 1200.  Rows that are no whole 128-byte lines or outputs that fit in
+      // the last-level cache were slower so (59 MB in rows of 2592 bytes: 28.5 ->
+      // 31.3 us).
       constexpr int kOut = F32 ? 4 : 2, kRow = 128 * kOut, kChunks = kRow / 16;
       // token groups that have room at once: all (a bf16 tile, up to 128 KB), or one
       constexpr int kAtOnce = F32 ? 1 : J, kOwn = kAtOnce * 16 * kRow;
@@ -603,17 +608,22 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
         // LDS operations of one wave complete in order
         asm volatile("" ::: "memory");
         __builtin_amdgcn_wave_barrier();
+        auto rows_out = [&](auto stream) {   // (a branch at each store would part them)
   #pragma unroll
-        for (int q = 0; q < kAtOnce * 16 * kChunks / kWave; ++q) {
-          const int r = ln / kChunks + q * (kWave / kChunks), tok = 16 * J * wt + 16 * j0 + r;
-          fp8_u32x4 w = *reinterpret_cast<const fp8_u32x4*>(own + r * kRow + 16 * (chunk ^ (r & 15)));
-          if (tok < rows_a && n < rows_b) {   // N % 16 == 0: the 16 bytes are inside or outside
-            auto* c = reinterpret_cast<fp8_u32x4*>(c_tile + static_cast<int64_t>(tok) * g.ldc * kOut);
-            if (F32 && WG && g.accumulate)
-              w = __builtin_bit_cast(fp8_u32x4, __builtin_bit_cast(f32x4, *c) + __builtin_bit_cast(f32x4, w));
-            *c = w;
+          for (int q = 0; q < kAtOnce * 16 * kChunks / kWave; ++q) {
+            const int r = ln / kChunks + q * (kWave / kChunks), tok = 16 * J * wt + 16 * j0 + r;
+            fp8_u32x4 w = *reinterpret_cast<const fp8_u32x4*>(own + r * kRow + 16 * (chunk ^ (r & 15)));
+            if (tok < rows_a && n < rows_b) {   // N % 16 == 0: the 16 bytes are inside or outside
+              auto* c = reinterpret_cast<fp8_u32x4*>(c_tile + static_cast<int64_t>(tok) * g.ldc * kOut);
+              if (F32 && WG && g.accumulate)
+                w = __builtin_bit_cast(fp8_u32x4, __builtin_bit_cast(f32x4, *c) + __builtin_bit_cast(f32x4, w));
+              if constexpr (decltype(stream)::value) __builtin_nontemporal_store(w, c);
+              else *c = w;
+            }
           }
-        }
+        };
+        if (g.stream) rows_out(std::true_type{});
+        else rows_out(std::false_type{});
         asm volatile("" ::: "memory");
         __builtin_amdgcn_wave_barrier();
       }

@@ -13,8 +13,8 @@
 // through LDS), and the transposed codes leave through an LDS tile so that
 // their stores are whole 128-byte lines.
 //
-// 17408 x 14336, both copies: 197 us, 5.1 TB/s of reads and writes; 128 weights
-// of 2880 x 2880, both tile copies: 874 us, 4.9 TB/s, where a large copy reaches
+// 17408 x 14336, both copies: 187 us, 5.4 TB/s of reads and writes; 128 weights
+// of 2880 x 2880, both tile copies: 818 us, 5.2 TB/s, where a large copy reaches
 // 4.8.  16 rows of 4096: 3 us, the launch.
 #include <type_traits>
 
@@ -49,6 +49,26 @@ MOE_DEV Scale block_scale(float m) {
   } else {
     return {s, 448.0f / m};
   }
+}
+
+// STREAM: nontemporal stores, and loads of what row copies are made of.  Both
+// copies of 17408 x 14336 in 187 us (stores alone 191, neither 197), 128 weights'
+// tile copies in 818 (loads too 827, neither 871).  For operands that the
+// last-level cache does not hold, in rows of whole 64 bytes: 6224 x 8816, whose
+// transposed rows are not, takes 102 us so and 50 without.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <bool STREAM>
+MOE_DEV uint4 load16(const void* p) {
+  const u32x4* v = static_cast<const u32x4*>(p);
+  if constexpr (STREAM) return __builtin_bit_cast(uint4, __builtin_nontemporal_load(v));
+  else return __builtin_bit_cast(uint4, *v);
+}
+template <bool STREAM, typename T>
+MOE_DEV void store(void* p, const T& v) {
+  using V = std::conditional_t<sizeof(T) == 8, u32x2, u32x4>;
+  if constexpr (STREAM) __builtin_nontemporal_store(__builtin_bit_cast(V, v), static_cast<V*>(p));
+  else *static_cast<T*>(p) = v;
 }
 
 MOE_DEV float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
@@ -141,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const Q a, int uni
 
 // One 128 x 128 tile: row copies (ROW), transposed row copies (COL), or the
 // tile's copy (TILE) and its transpose (TILE with COL).
-template <bool ROW, bool COL, bool TILE, bool POW2>
+template <bool ROW, bool COL, bool TILE, bool POW2, bool STREAM>
 __global__ __launch_bounds__(kThreads) void quant_tile_kernel(const Q a) {
   // LDS image of the transposed tile: a column's 128 codes in 8-byte chunks,
   // chunk r of column c at r ^ 2 (c / 8 % 8).  With rows 144 bytes apart a
@@ -168,7 +188,7 @@ __global__ __launch_bounds__(kThreads) void quant_tile_kernel(const Q a) {
   for (int i = 0; i < 8; ++i) {
     v[i] = uint4{0, 0, 0, 0};
     if (col_ok && row0 + r8 + i < used)
-      v[i] = *reinterpret_cast<const uint4*>(x + (row0 + r8 + i) * a.cols + col0 + c8);
+      v[i] = load16<STREAM && !TILE>(x + (row0 + r8 + i) * a.cols + col0 + c8);
   }
   float tile_r = 0.0f;
   if constexpr (TILE) {
@@ -200,7 +220,7 @@ __global__ __launch_bounds__(kThreads) void quant_tile_kernel(const Q a) {
         if (c8 == 0 && row < used) s[row] = sc.s;
       }
       if (col_ok && row < used)
-        *reinterpret_cast<uint2*>(q + row * a.cols + col0 + c8) = codes8(v[i], r);
+        store<STREAM>(q + row * a.cols + col0 + c8, codes8(v[i], r));
     }
   }
   if constexpr (COL) {
@@ -265,8 +285,8 @@ __global__ __launch_bounds__(kThreads) void quant_tile_kernel(const Q a) {
     for (int p = 0; p < 4; ++p) {
       const int col = p * 32 + tid / 8, r = (tid & 7) * 16;
       if (col0 + col < a.cols && row0 + r < a.rows)
-        *reinterpret_cast<uint4*>(qT + static_cast<int64_t>(col0 + col) * a.rows + row0 + r) =
-            *reinterpret_cast<const uint4*>(s_t + col * kLd + 8 * ((r / 8) ^ (2 * ((col >> 3) & 7))));
+        store<STREAM>(qT + static_cast<int64_t>(col0 + col) * a.rows + row0 + r,
+                      *reinterpret_cast<const uint4*>(s_t + col * kLd + 8 * ((r / 8) ^ (2 * ((col >> 3) & 7)))));
     }
   }
 }
@@ -286,14 +306,20 @@ void launch(const moe_quant_fp8_args& m, const Q& a, hipStream_t s) {
     return;
   }
   const dim3 grid(static_cast<uint32_t>(a.n_rb * a.n_cb), m.batch);
-  if (m.mode == MOE_QUANT_BOTH)
-    quant_tile_kernel<true, true, false, POW2><<<grid, kThreads, 0, s>>>(a);
-  else if (m.mode == MOE_QUANT_COL)
-    quant_tile_kernel<false, true, false, POW2><<<grid, kThreads, 0, s>>>(a);
-  else if (a.qT)
-    quant_tile_kernel<false, true, true, POW2><<<grid, kThreads, 0, s>>>(a);
-  else
-    quant_tile_kernel<false, false, true, POW2><<<grid, kThreads, 0, s>>>(a);
+  const int64_t n = static_cast<int64_t>(m.batch) * a.rows * a.cols;
+  auto tiles = [&](auto stream) {
+    constexpr bool kS = decltype(stream)::value;
+    if (m.mode == MOE_QUANT_BOTH)
+      quant_tile_kernel<true, true, false, POW2, kS><<<grid, kThreads, 0, s>>>(a);
+    else if (m.mode == MOE_QUANT_COL)
+      quant_tile_kernel<false, true, false, POW2, kS><<<grid, kThreads, 0, s>>>(a);
+    else if (a.qT)
+      quant_tile_kernel<false, true, true, POW2, kS><<<grid, kThreads, 0, s>>>(a);
+    else
+      quant_tile_kernel<false, false, true, POW2, kS><<<grid, kThreads, 0, s>>>(a);
+  };
+  if (2 * n > kStreamBytes && a.rows % 64 == 0 && a.cols % 64 == 0) tiles(std::true_type{});
+  else tiles(std::false_type{});
 }
 
 }  // namespace

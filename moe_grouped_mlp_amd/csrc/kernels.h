@@ -155,6 +155,7 @@ struct Fp8Args {
   void* c;
   int64_t ldc;
   int accumulate;          // weight gradient, fp32: C +=
+  int stream;              // C in nontemporal stores
   int group_m;             // token tiles per band of the tile order
   int32_t* err;            // nullable
   fp8_f32x4* part;         // product (nullable): one tile's fp32 sums per workgroup
@@ -172,6 +173,10 @@ hipError_t launch_fp8_wgrad(const Fp8Args& g, bool f32, int groups, int grid, hi
 size_t router_loss_workspace_bytes(int T, int E);
 hipError_t launch_router_loss(const moe_router_loss_args& a, hipStream_t s);
 hipError_t launch_router_bwd(const moe_router_bwd_args& a, hipStream_t s);
+
+// Nontemporal loads and stores are for what passes this size in a call: less
+// stays in the last-level cache (256 MB) for whoever reads it next.
+constexpr int64_t kStreamBytes = int64_t(256) << 20;
 
 // ---- gradient norm and clipping -----------------------------------------------
 constexpr int kGradList = 96;         // tensors of one launch (3 KB of arguments)

@@ -635,3 +635,71 @@ def test_quantize_product_and_gradients_together_in_a_graph():
         ref, mag = st.grouped_weight_grad(st.dequantize_rows(*st.quantize_rows(hdy.T.copy())),
                                           st.dequantize_rows(*st.quantize_rows(hx.T.copy())), sizes, starts)
         assert (np.abs(got[2].double().cpu().numpy() - ref) <= 2 * (132 + nb(M)) * 2.0 ** -23 * mag).all()
+
+
+# ------------------------------------------- past the last-level cache --
+# Outputs of more than 256 MB in whole lines are stored nontemporally.
+@pytest.mark.parametrize("c_type", [mg.TYPE_F32, mg.TYPE_BF16])
+def test_product_of_a_large_buffer(c_type):
+    sizes, N, K = [300, 0, 77], 4096, 144
+    starts = _starts(sizes)
+    M_cap = 40960 if c_type == mg.TYPE_BF16 else 20480
+    rng = np.random.default_rng(21)
+    ops = _operands(rng, sizes, starts, starts[-1], N, K, exact=True)
+    ref, _ = _reference(*ops, sizes, starts)
+    a_q, a_s = np.zeros((M_cap, K), np.uint8), np.ones((ops[1].shape[0], M_cap), np.float32)
+    a_q[:starts[-1]], a_s[:, :starts[-1]] = ops[0], ops[1]
+    c = _product(a_q, a_s, *ops[2:], sizes, starts, c_type)
+    want = ref if c_type == mg.TYPE_F32 else nu.round_bf16(ref)
+    got = c[:starts[-1]].double().cpu().numpy()
+    np.testing.assert_array_equal(got[~np.isnan(ref)], want[~np.isnan(ref)])
+    assert (got[np.isnan(ref)] == -77.0).all() and bool((c[starts[-1]:] == -77.0).all())
+
+
+@pytest.mark.parametrize("c_type", [mg.TYPE_F32, mg.TYPE_BF16])
+def test_wgrad_of_large_experts(c_type):
+    E, P, Q = 40 if c_type == mg.TYPE_F32 else 72, 1024, 2048
+    sizes = [0] * E
+    sizes[1], sizes[-1] = 5, 130
+    starts = _starts(sizes)
+    rng = np.random.default_rng(22)
+    ops = _wgrad_operands(rng, sizes, starts, starts[-1], P, Q, exact=True)
+    c = _wgrad(*ops, sizes, starts, c_type)
+    live = [1, E - 1]
+    ref, _ = _wgrad_ref(*ops, [sizes[e] for e in live], [starts[e] for e in live])
+    want = ref if c_type == mg.TYPE_F32 else nu.round_bf16(ref)
+    np.testing.assert_array_equal(c[live].double().cpu().numpy(), want)
+    assert not bool(c[[e for e in range(E) if e not in live]].any())
+    if c_type == mg.TYPE_F32:
+        c.fill_(3.0)
+        _wgrad(*ops, sizes, starts, c=c, accumulate=True)
+        np.testing.assert_array_equal(c[live].double().cpu().numpy(), ref + 3.0)
+
+
+@pytest.mark.parametrize("mode", [mg.QUANT_BOTH, mg.QUANT_TILE])
+def test_quantize_large_operand(mode):
+    """Samples of rows and columns against the oracle, the others against the
+    copies' own transposes."""
+    R, C = 16384, 8256
+    x = torch.randn(R, C, device=DEV, generator=torch.Generator(DEV).manual_seed(5)).bfloat16()
+    tile = mode == mg.QUANT_TILE
+    rb, cb = R // 128, -(-C // 128)
+    q, qT = torch.empty(R, C, dtype=torch.uint8, device=DEV), torch.empty(C, R, dtype=torch.uint8, device=DEV)
+    s = torch.empty((rb, cb) if tile else (cb, R), device=DEV)
+    sT = torch.empty((cb, rb) if tile else (rb, C), device=DEV)
+    mg.moe_quantize_fp8(mode=mode, batch=1, rows=R, cols=C, x=x, q=q, s=s, qT=qT, sT=sT)
+    torch.cuda.synchronize()
+    if tile:
+        assert torch.equal(q, qT.t()) and torch.equal(s, sT.t())
+        for r in (0, R - 128):
+            rq, rs = st.quantize_tiles(x[r:r + 128].double().cpu().numpy())
+            np.testing.assert_array_equal(q[r:r + 128].cpu().numpy(), rq)
+            np.testing.assert_array_equal(s[r // 128:r // 128 + 1].cpu().numpy(), rs)
+        return
+    q1, s1 = torch.empty_like(q), torch.empty_like(s)   # the kernel of row copies alone
+    mg.moe_quantize_fp8(mode=mg.QUANT_ROW, batch=1, rows=R, cols=C, x=x, q=q1, s=s1)
+    assert torch.equal(q, q1) and torch.equal(s, s1)
+    for c in (0, 4096, C - 64):
+        cq, cs = st.quantize_rows(x[:, c:c + 64].double().cpu().numpy().T.copy())
+        np.testing.assert_array_equal(qT[c:c + 64].cpu().numpy(), cq)
+        np.testing.assert_array_equal(sT[:, c:c + 64].cpu().numpy(), cs)
