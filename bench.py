@@ -195,9 +195,9 @@ def cpu_baseline(cfg, seed, mx=False, target_s=15.0):
 def gemm_bench(args):
     """--gemm: the FC2-shaped plain grouped GEMM (A = a [M][I], B = W2
     [E][H][I], the config's routed group sizes) through moe_grouped_gemm in
-    bf16, MXFP8 and MXFP4, operands quantized before the timed region (the
-    weights once per update; a by moe_quantize_mxfp8 / _mxfp4, timed on its
-    own).  Prints one JSON line whose value is the MXFP4 rate."""
+    bf16, MXFP8 and MXFP4, and through moe_grouped_gemm_fp8 in block-scaled
+    FP8, operands quantized before the timed region (the weights once per
+    update; a by moe_quantize_mxfp8 / _mxfp4 / _fp8, timed on its own).  Prints one JSON line whose value is the MXFP4 rate."""
     import numpy as np
     import torch
     import moe_grouped_mlp_amd as mg
@@ -286,6 +286,27 @@ def gemm_bench(args):
                 100 * tf / (PEAK_TFLOPS[prec] * ck / 2.4), 2)
         log(f"  {ms:.3f} ms, {tf:.1f} TFLOP/s ({100 * tf / PEAK_TFLOPS[prec]:.1f}% of peak)"
             f"{f', clock {ck:.3f} GHz' if ck else ''}")
+    # block-scaled FP8 (one fp32 scale per 128 values, weights per 128 x 128)
+    log(f"grouped GEMM fp8: E={E} M={M} N={N} K={K}")
+    f32 = dict(dtype=torch.float32, device=dev)
+    a_q, a_s = torch.empty(M_cap * K, **u8), torch.empty(-(-K // 128) * M_cap, **f32)
+    b_q = torch.empty(E * N * K, **u8)
+    b_s = torch.empty(E * -(-N // 128) * -(-K // 128), **f32)
+    mg.moe_quantize_fp8(mode=mg.QUANT_TILE, batch=E, rows=N, cols=K, x=w, q=b_q, s=b_s)
+    qms = timed(lambda: mg.moe_quantize_fp8(mode=mg.QUANT_ROW, batch=1, rows=M_cap, cols=K, x=a,
+                                            q=a_q, s=a_s), args.steps)
+    kernels["quantize_a_fp8"] = {"ms": round(qms, 4), "unit": "GB/s",
+                                 "rate": round(M_cap * K * (3 + 1 / 32) / (qms * 1e-3) / 1e9, 1)}
+    ws8 = mg.moe_grouped_gemm_fp8_workspace_size(E, N, K, M_cap)
+    ws8 = torch.empty(ws8, **u8) if ws8 else None
+    ms = timed(lambda: mg.moe_grouped_gemm_fp8(E=E, N=N, K=K, M_cap=M_cap, split_sizes=split,
+                                               padded_offsets=padded, a=a_q, a_s=a_s, b=b_q,
+                                               b_s=b_s, c=out, workspace=ws8), args.steps)
+    tf = flops / (ms * 1e-3) / 1e12
+    kernels["gemm_fp8"] = {"ms": round(ms, 4), "unit": "TFLOP/s", "rate": round(tf, 2),
+                           "pct_peak": round(100 * tf / PEAK_TFLOPS["mxfp8"], 2)}
+    log(f"  {ms:.3f} ms, {tf:.1f} TFLOP/s ({100 * tf / PEAK_TFLOPS['mxfp8']:.1f}% of peak)")
+    del a_q, a_s, b_q, b_s, ws8
     # overlap with another kernel (the pages' reason for dynamic scheduling):
     # a kernel holds 64 of the CUs for the first 1 ms of the bf16 GEMM; with
     # the work counters the other workgroups take the busy CUs' tiles, with
