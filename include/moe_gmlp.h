@@ -813,11 +813,11 @@ moe_status moe_quantize_fp8(const moe_quant_fp8_args* args, void* stream);
  *   decoding step of T tokens: T), 0 if not.  It chooses among kernels;
  *   groups that turn out larger are computed all the same.
  *   workspace: optional, moe_grouped_gemm_fp8_workspace_size(...) bytes (0:
- *   none would be used; a smaller one is not used), 16-byte aligned, no initialisation; calls that overlap in time must not
- *   share one.  With it a product of so few tiles that they would leave more
- *   than half of the device idle is cut along K, its parts added in a fixed
- *   order: the same call gives the same bits, one without workspace sums in
- *   another order. */
+ *   none would be used; a smaller one is not used), 16-byte aligned, no
+ *   initialisation; calls that overlap in time must not share one.  With it a
+ *   product of so few tiles that they would leave more than half of the
+ *   device idle is cut along K, its parts added in a fixed order: the same
+ *   call gives the same bits, one without workspace sums in another order. */
 typedef struct moe_gemm_fp8_args {
   int32_t E, N, K;
   int64_t M_cap;
@@ -948,8 +948,8 @@ moe_status moe_router_bwd(const moe_router_bwd_args* args, void* stream);
  *     that hold different parameters add their sums before clipping.
  *   moe_grad_clip: norm = sqrt(*sumsq), f = min(1, max_norm / (norm +
  *     1e-6)) (fp64, rounded to fp32 unless that is below its normal range),
- *     out = g * f in fp32, one rounding to the tensor's type; *norm (optional) = norm.  out == data (or NULL)
- *     scales in place.  If norm is infinite or NaN, f = 1 and
+ *     out = g * f in fp32, one rounding to the tensor's type; *norm (optional)
+ *     = norm.  out == data (or NULL) scales in place.  If norm is infinite or NaN, f = 1 and
  *     MOE_DEVERR_NONFINITE is set: the caller decides about the step.
  *   tensors: host array, read before the call returns; n_tensors >= 0; data
  *   contiguous, aligned to its type, numel >= 0.  moe_grad_clip refuses
