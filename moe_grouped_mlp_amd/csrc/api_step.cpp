@@ -201,8 +201,8 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
   const bool cut = cuts_k(a->E, a->N, a->K, a->M_cap, most, cu) && a->workspace &&
                    a->workspace_bytes >= static_cast<size_t>(full) * moe::kFp8PartFloats * sizeof(float);
   if (cut) g.part = static_cast<moe::fp8_f32x4*>(a->workspace);
-  const int grid = cut ? full : tile_grid(cu, a->cu_margin, tiles);
-  return launched(moe::launch_fp8_gemm(g, f32, groups, grid, s));
+  g.grid = cut ? full : tile_grid(cu, a->cu_margin, tiles);
+  return launched(moe::launch_fp8_gemm(g, f32, groups, s));
 }
 
 moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {
@@ -237,8 +237,8 @@ moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {
   g.stream = streams(static_cast<int64_t>(a->E) * a->P, static_cast<int64_t>(a->Q) * type_bytes(a->c_type));
   g.group_m = 4;
   g.err = a->err_flag;
-  return launched(moe::launch_fp8_wgrad(g, f32, groups, tile_grid(cu, a->cu_margin, tiles),
-                                        static_cast<hipStream_t>(stream)));
+  g.grid = tile_grid(cu, a->cu_margin, tiles);
+  return launched(moe::launch_fp8_wgrad(g, f32, groups, static_cast<hipStream_t>(stream)));
 }
 
 // ------------------------------------------------------- router losses ------

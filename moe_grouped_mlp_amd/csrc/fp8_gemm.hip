@@ -5,19 +5,19 @@ namespace moe {
 namespace {
 
 template <int JMAX, bool F32>
-hipError_t launch(const Fp8Args& g, int grid, hipStream_t s) {
-  fp8_gemm_kernel<JMAX, false, F32><<<grid, kFp8Threads, 0, s>>>(g);
+hipError_t launch(const Fp8Args& g, hipStream_t s) {
+  fp8_gemm_kernel<JMAX, false, F32><<<g.grid, kFp8Threads, 0, s>>>(g);
   if (hipError_t e = hipGetLastError()) return e;
-  if (g.part) fp8_join_kernel<JMAX, F32><<<grid, kFp8Threads, 0, s>>>(g, grid);
+  if (g.part) fp8_join_kernel<JMAX, F32><<<g.grid, kFp8Threads, 0, s>>>(g);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_fp8_gemm(const Fp8Args& g, bool f32, int groups, int grid, hipStream_t s) {
-  if (f32) return groups == 1 ? launch<1, true>(g, grid, s) : launch<2, true>(g, grid, s);
-  if (groups == 1) return launch<1, false>(g, grid, s);
-  return groups == 2 ? launch<2, false>(g, grid, s) : launch<4, false>(g, grid, s);
+hipError_t launch_fp8_gemm(const Fp8Args& g, bool f32, int groups, hipStream_t s) {
+  if (f32) return groups == 1 ? launch<1, true>(g, s) : launch<2, true>(g, s);
+  if (groups == 1) return launch<1, false>(g, s);
+  return groups == 2 ? launch<2, false>(g, s) : launch<4, false>(g, s);
 }
 
 }  // namespace moe

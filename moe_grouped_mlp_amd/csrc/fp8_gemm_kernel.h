@@ -312,8 +312,8 @@ MOE_DEV int fp8_parts(const Fp8Args& g, int total, int workgroups) {
 }
 // Place of a workgroup in the order of tiles: contiguous runs for each XCD
 // (workgroup ids go round the XCDs).
-MOE_DEV int fp8_workgroup() {
-  const int G = gridDim.x;
+MOE_DEV int fp8_workgroup(const Fp8Args& g) {
+  const int G = g.grid;
   if (G % kNumXcd != 0) return blockIdx.x;
   return (blockIdx.x % kNumXcd) * (G / kNumXcd) + blockIdx.x / kNumXcd;
 }
@@ -348,9 +348,9 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
   const int wave_s = __builtin_amdgcn_readfirstlane(wave);
   const int wn = wave & 1, wt = wave >> 1;
   const int total = fp8_tile_prefix<BT, WG>(g, s_tab);
-  const int parts = WG ? 1 : fp8_parts(g, total, gridDim.x);
+  const int parts = WG ? 1 : fp8_parts(g, total, g.grid);
 
-  for (int item = fp8_workgroup(); item < total * parts; item += gridDim.x) {
+  for (int item = fp8_workgroup(g); item < total * parts; item += g.grid) {
     const Fp8Tile tile = fp8_tile_at<BT, WG>(g, s_tab, item / parts);
     const int e = tile.e, n_e = tile.n_e, start = tile.start, rows_t = tile.rows_t, t0 = tile.t0, n0 = tile.n0;
     // the steps [k0, k1) of this part
@@ -649,11 +649,11 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
 // their order and stores it.  Workgroup q of a tile takes every parts-th
 // accumulator (bf16: pair of weight tiles, whose outputs are neighbours).
 template <int JMAX, bool F32>
-__global__ __launch_bounds__(kFp8Threads) void fp8_join_kernel(const Fp8Args g, int workgroups) {
+__global__ __launch_bounds__(kFp8Threads) void fp8_join_kernel(const Fp8Args g) {
   constexpr int BT = 64 * JMAX, kStep = F32 ? 1 : 2;
   __shared__ Fp8Tables s_tab;
   const int total = fp8_tile_prefix<BT, false>(g, s_tab);
-  const int parts = fp8_parts(g, total, workgroups);
+  const int parts = fp8_parts(g, total, g.grid);
   const int item = blockIdx.x;
   if (parts == 1 || item >= total * parts) return;
   const Fp8Tile tile = fp8_tile_at<BT, false>(g, s_tab, item / parts);

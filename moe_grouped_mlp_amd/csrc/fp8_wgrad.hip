@@ -3,8 +3,8 @@
 
 namespace moe {
 
-hipError_t launch_fp8_wgrad(const Fp8Args& g, bool f32, int groups, int grid, hipStream_t s) {
-  auto go = [&](auto kernel) { kernel<<<grid, kFp8Threads, 0, s>>>(g); };
+hipError_t launch_fp8_wgrad(const Fp8Args& g, bool f32, int groups, hipStream_t s) {
+  auto go = [&](auto kernel) { kernel<<<g.grid, kFp8Threads, 0, s>>>(g); };
   if (f32) groups == 1 ? go(fp8_gemm_kernel<1, true, true>) : go(fp8_gemm_kernel<2, true, true>);
   else if (groups == 1) go(fp8_gemm_kernel<1, true, false>);
   else groups == 2 ? go(fp8_gemm_kernel<2, true, false>) : go(fp8_gemm_kernel<4, true, false>);

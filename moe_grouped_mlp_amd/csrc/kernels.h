@@ -156,6 +156,7 @@ struct Fp8Args {
   int64_t ldc;
   int accumulate;          // weight gradient, fp32: C +=
   int stream;              // C in nontemporal stores
+  int grid;                // workgroups (asking the hardware for it adds 256 bytes of arguments)
   int group_m;             // token tiles per band of the tile order
   int32_t* err;            // nullable
   fp8_f32x4* part;         // product (nullable): one tile's fp32 sums per workgroup
@@ -164,10 +165,10 @@ constexpr int kFp8PartFloats = 256 * 256;
 // Tiles are of 64 `groups` tokens (1, 2 or, bf16 output only, 4) x 256 weight rows.
 inline int fp8_most_groups(bool f32) { return f32 ? 2 : 4; }
 // with g.part also the launch that joins the parts of tiles whose K was cut
-hipError_t launch_fp8_gemm(const Fp8Args& g, bool f32, int groups, int grid, hipStream_t s);
+hipError_t launch_fp8_gemm(const Fp8Args& g, bool f32, int groups, hipStream_t s);
 // groups of few rows; tile_rows: 16 or 32 tokens at a time
 hipError_t launch_fp8_rows(const Fp8Args& g, int tile_rows, bool f32, hipStream_t s);
-hipError_t launch_fp8_wgrad(const Fp8Args& g, bool f32, int groups, int grid, hipStream_t s);
+hipError_t launch_fp8_wgrad(const Fp8Args& g, bool f32, int groups, hipStream_t s);
 
 // ---- router losses ----------------------------------------------------------
 size_t router_loss_workspace_bytes(int T, int E);
