@@ -53,7 +53,8 @@ MOE_DEV Scale block_scale(float m) {
 
 // STREAM: nontemporal stores, and loads of what row copies are made of.  Both
 // copies of 17408 x 14336 in 187 us (stores alone 191, neither 197), 128 weights'
-// tile copies in 818 (loads too 827, neither 871).  For operands that the
+// tile copies in 818 (loads too 827, neither 871), rows alone of 17408 x 14336 in
+// 121 (neither 138).  For operands that the
 // last-level cache does not hold, in rows of whole 64 bytes: 6224 x 8816, whose
 // transposed rows are not, takes 102 us so and 50 without.
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -130,13 +131,13 @@ MOE_DEV int rows_used(const Q& a) {
 // Row copies.  A workgroup takes 16 rows and kU column blocks (kU loads in
 // flight for each thread): 256-byte runs in, 128-byte runs out, the 16
 // scales of a column block side by side.
-template <int kU, bool POW2>
-__global__ __launch_bounds__(kThreads) void quant_rows_kernel(const Q a, int units_c) {
+template <int kU, bool POW2, bool STREAM>
+__global__ __launch_bounds__(kThreads) void quant_rows_kernel(const Q a, uint32_t units_c) {
   const int b = blockIdx.y;
   if (a.live && a.live[b] == 0) return;
-  const int64_t unit = blockIdx.x;
-  const int cb0 = static_cast<int>(unit % units_c) * kU;
-  const int64_t row = unit / units_c * 16 + threadIdx.x / 16;
+  const uint32_t unit = blockIdx.x, ru = unit / units_c;
+  const int cb0 = static_cast<int>(unit - ru * units_c) * kU;
+  const int64_t row = static_cast<int64_t>(ru) * 16 + threadIdx.x / 16;
   const int c8 = (threadIdx.x & 15) * 8;
   if (row >= rows_used(a)) return;   // whole 16-lane rows leave
   const uint16_t* x = a.x + b * a.x_stride + row * a.cols;
@@ -148,13 +149,13 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(const Q a, int uni
   for (int u = 0; u < kU; ++u) {
     const int c = (cb0 + u) * kBlock + c8;
     v[u] = uint4{0, 0, 0, 0};
-    if (c < a.cols) v[u] = *reinterpret_cast<const uint4*>(x + c);
+    if (c < a.cols) v[u] = load16<STREAM>(x + c);
   }
 #pragma unroll
   for (int u = 0; u < kU; ++u) {
     const int cb = cb0 + u, c = cb * kBlock + c8;
     const Scale sc = block_scale<POW2>(max16(amax8(v[u])));
-    if (c < a.cols) *reinterpret_cast<uint2*>(q + c) = codes8(v[u], sc.r);
+    if (c < a.cols) store<STREAM>(q + c, codes8(v[u], sc.r));
     if (c8 == 0 && cb < a.n_cb) s[static_cast<int64_t>(cb) * a.rows] = sc.s;
   }
 }
@@ -293,20 +294,22 @@ __global__ __launch_bounds__(kThreads) void quant_tile_kernel(const Q a) {
 
 template <bool POW2>
 void launch(const moe_quant_fp8_args& m, const Q& a, hipStream_t s) {
+  const int64_t n = static_cast<int64_t>(m.batch) * a.rows * a.cols;
+  const bool large = 2 * n > kStreamBytes && a.cols % 64 == 0;
   if (m.mode == MOE_QUANT_ROW) {
     const int64_t row_units = (static_cast<int64_t>(a.rows) + 15) / 16;
+    const uint32_t uc = (a.n_cb + 7) / 8;
+    auto rows = [&](auto kernel, uint32_t units_c) {
+      kernel<<<dim3(static_cast<uint32_t>(row_units * units_c), m.batch), kThreads, 0, s>>>(a, units_c);
+    };
     // eight blocks a thread in flight where that still leaves four
     // workgroups a CU, else one block each
-    if (row_units * ((a.n_cb + 7) / 8) * m.batch >= 1024) {
-      const int uc = (a.n_cb + 7) / 8;
-      quant_rows_kernel<8, POW2><<<dim3(static_cast<uint32_t>(row_units * uc), m.batch), kThreads, 0, s>>>(a, uc);
-    } else {
-      quant_rows_kernel<1, POW2><<<dim3(static_cast<uint32_t>(row_units * a.n_cb), m.batch), kThreads, 0, s>>>(a, a.n_cb);
-    }
+    if (row_units * uc * m.batch < 1024) rows(quant_rows_kernel<1, POW2, false>, a.n_cb);
+    else if (large) rows(quant_rows_kernel<8, POW2, true>, uc);
+    else rows(quant_rows_kernel<8, POW2, false>, uc);
     return;
   }
   const dim3 grid(static_cast<uint32_t>(a.n_rb * a.n_cb), m.batch);
-  const int64_t n = static_cast<int64_t>(m.batch) * a.rows * a.cols;
   auto tiles = [&](auto stream) {
     constexpr bool kS = decltype(stream)::value;
     if (m.mode == MOE_QUANT_BOTH)
@@ -318,7 +321,7 @@ void launch(const moe_quant_fp8_args& m, const Q& a, hipStream_t s) {
     else
       quant_tile_kernel<false, false, true, POW2, kS><<<grid, kThreads, 0, s>>>(a);
   };
-  if (2 * n > kStreamBytes && a.rows % 64 == 0 && a.cols % 64 == 0) tiles(std::true_type{});
+  if (large && a.rows % 64 == 0) tiles(std::true_type{});
   else tiles(std::false_type{});
 }
 

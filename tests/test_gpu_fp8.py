@@ -699,6 +699,10 @@ def test_quantize_large_operand(mode):
     q1, s1 = torch.empty_like(q), torch.empty_like(s)   # the kernel of row copies alone
     mg.moe_quantize_fp8(mode=mg.QUANT_ROW, batch=1, rows=R, cols=C, x=x, q=q1, s=s1)
     assert torch.equal(q, q1) and torch.equal(s, s1)
+    for r in (0, R - 16):
+        rq, rs = st.quantize_rows(x[r:r + 16].double().cpu().numpy())
+        np.testing.assert_array_equal(q1[r:r + 16].cpu().numpy(), rq)
+        np.testing.assert_array_equal(s1[:, r:r + 16].cpu().numpy(), rs)
     for c in (0, 4096, C - 64):
         cq, cs = st.quantize_rows(x[:, c:c + 64].double().cpu().numpy().T.copy())
         np.testing.assert_array_equal(qT[c:c + 64].cpu().numpy(), cq)
