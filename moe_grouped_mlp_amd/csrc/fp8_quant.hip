@@ -54,9 +54,9 @@ MOE_DEV Scale block_scale(float m) {
 // STREAM: nontemporal stores, and loads of what row copies are made of.  Both
 // copies of 17408 x 14336 in 187 us (stores alone 191, neither 197), 128 weights'
 // tile copies in 818 (loads too 827, neither 871), rows alone of 17408 x 14336 in
-// 121 (neither 138).  For operands that the
-// last-level cache does not hold, in rows of whole 64 bytes: 6224 x 8816, whose
-// transposed rows are not, takes 102 us so and 50 without.
+// 121 (neither 138).  For operands that the last-level cache does not hold, in
+// rows of whole 64 bytes: 6224 x 8816, whose transposed rows are not, takes 102
+// us so and 50 without.
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 template <bool STREAM>
