@@ -191,7 +191,7 @@ class GemmFp8Args(ctypes.Structure):
                 ("b_s_stride", c_int64), ("c", c_void_p), ("ldc", c_int64),
                 ("c_type", c_int32), ("max_rows", c_int32), ("cu_margin", c_int32),
                 ("err_flag", c_void_p), ("workspace", c_void_p),
-                ("workspace_bytes", c_size_t)]
+                ("workspace_bytes", c_size_t), ("fp8_sums", c_int32)]
 
 
 class WgradFp8Args(ctypes.Structure):
@@ -200,7 +200,7 @@ class WgradFp8Args(ctypes.Structure):
                 ("padded_offsets", c_void_p), ("a", c_void_p), ("a_s", c_void_p),
                 ("b", c_void_p), ("b_s", c_void_p), ("c", c_void_p),
                 ("c_type", c_int32), ("accumulate", c_int32), ("cu_margin", c_int32),
-                ("err_flag", c_void_p)]
+                ("err_flag", c_void_p), ("fp8_sums", c_int32)]
 
 
 class RouterLossArgs(ctypes.Structure):
@@ -589,20 +589,23 @@ def moe_grouped_gemm_fp8_workspace_size(E, N, K, M_cap, max_rows=0) -> int:
 
 def moe_grouped_gemm_fp8(*, E, N, K, M_cap, split_sizes, padded_offsets, a, a_s, b, b_s, c,
                          b_stride=0, b_s_stride=0, ldc=0, c_type=TYPE_BF16, max_rows=0,
-                         cu_margin=0, err_flag=None, workspace=None, stream=None):
-    """C[r] = A[r] . B_e^T on block-scaled FP8 operands for every group's rows."""
+                         cu_margin=0, fp8_sums=False, err_flag=None, workspace=None, stream=None):
+    """C[r] = A[r] . B_e^T on block-scaled FP8 operands for every group's rows,
+    summed in fp32; fp8_sums (bf16 C): the sums inside a block by the FP8 matrix
+    instructions, which keep fewer bits at up to twice the rate."""
     d = _device()
     _call.grouped_gemm_fp8(d, E, N, K, M_cap, b_stride, b_s_stride, ldc, c_type, max_rows,
-                           cu_margin, split_sizes, padded_offsets, a, a_s, b, b_s, c, err_flag,
+                           cu_margin, fp8_sums, split_sizes, padded_offsets, a, a_s, b, b_s, c, err_flag,
                            workspace, stream)
 
 
 def moe_grouped_wgrad_fp8(*, E, P, Q, M_cap, split_sizes, padded_offsets, a, a_s, b, b_s, c,
-                          c_type=TYPE_BF16, accumulate=False, cu_margin=0, err_flag=None,
-                          stream=None):
-    """C_e = A_e . B_e^T over each group's routed rows (transposed FP8 copies)."""
+                          c_type=TYPE_BF16, accumulate=False, cu_margin=0, fp8_sums=False,
+                          err_flag=None, stream=None):
+    """C_e = A_e . B_e^T over each group's routed rows (transposed FP8 copies);
+    fp8_sums as in moe_grouped_gemm_fp8."""
     d = _device()
-    _call.grouped_wgrad_fp8(d, E, P, Q, M_cap, c_type, accumulate, cu_margin, split_sizes,
+    _call.grouped_wgrad_fp8(d, E, P, Q, M_cap, c_type, accumulate, cu_margin, fp8_sums, split_sizes,
                             padded_offsets, a, a_s, b, b_s, c, err_flag, stream)
 
 

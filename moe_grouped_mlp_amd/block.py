@@ -44,7 +44,9 @@ weight copies) and moe_grouped_wgrad_fp8 for the weight gradients, whose
 transposed operands are made in the same pass as the row ones.  Layers of
 few tokens (decoding) take the product's kernel for few rows by themselves.
 wgrad_type=TYPE_F32 keeps the weight gradients in fp32, to which
-weight_grads(accumulate=True) adds.  No bias and no recompute path.
+weight_grads(accumulate=True) adds.  The products sum in fp32; fp8_sums=True
+lets the FP8 matrix instructions sum inside a block for the bf16 outputs, which
+keeps fewer bits at up to twice the rate.  No bias and no recompute path.
 
 Around the experts, router_loss() gives the router's balance and z losses and
 per-expert counts, router_backward() the gradient of its logits from these
@@ -82,7 +84,7 @@ class ExpertBlock:
                  bf16_copies: Optional[bool] = None, wgrad: bool = False,
                  recompute: bool = False, z_scratch: Optional[torch.Tensor] = None,
                  unfused: bool = False, wgrad_type: int = B.TYPE_BF16,
-                 device="cuda"):
+                 fp8_sums: bool = False, device="cuda"):
         self.E, self.H, self.I, self.T, self.k = E, H, I, T, k
         self.act = act or B.act_params()
         self.gated = self.act.act != B.ACT_SRELU
@@ -107,6 +109,9 @@ class ExpertBlock:
             raise ValueError("the FP8 layer has no recompute path, and always runs as separate passes")
         if wgrad_type != B.TYPE_BF16 and not self.fp8:
             raise ValueError("fp32 weight gradients are of the FP8 layer (prec=PREC_FP8)")
+        if fp8_sums and not self.fp8:
+            raise ValueError("fp8_sums is of the FP8 layer (prec=PREC_FP8)")
+        self.fp8_sums = fp8_sums
         # forward() / backward() run the unfused passes (the baseline the
         # fused kernels are measured against; bf16 copies are then needed)
         self.unfused = unfused
@@ -604,7 +609,8 @@ class ExpertBlock:
                                padded_offsets=self.padded_offsets, a=getattr(self, name + "_q8"),
                                a_s=getattr(self, name + "_s8"), b=getattr(self, weight + "_q8"),
                                b_s=getattr(self, weight + "_s8"), c=c, max_rows=self.T,
-                               cu_margin=self.cu_margin, err_flag=self.err_flag, workspace=self.ws)
+                               cu_margin=self.cu_margin, fp8_sums=self.fp8_sums,
+                               err_flag=self.err_flag, workspace=self.ws)
 
     def experts_forward_fp8(self) -> None:
         if self.bias1 is not None:
@@ -713,7 +719,9 @@ class ExpertBlock:
                                         a=getattr(self, left + "_q8"), a_s=getattr(self, left + "_s8"),
                                         b=getattr(self, right + "_q8"), b_s=getattr(self, right + "_s8"),
                                         c=c, c_type=self.wgrad_type, accumulate=accumulate,
-                                        cu_margin=self.cu_margin, err_flag=self.err_flag)
+                                        cu_margin=self.cu_margin,
+                                        fp8_sums=self.fp8_sums and self.wgrad_type == B.TYPE_BF16,
+                                        err_flag=self.err_flag)
             return self.dw1, self.dw2
         kw = {}
         if self.mx:

@@ -42,8 +42,8 @@ int tile_grid(int cu, int margin, int64_t tiles) {
 // CUs, narrow ones read the weights more often: E=22 N=7632 K=1296, 196 rows,
 // 45.7 us with 128, 55.6 with 64).  `tiles`: how many tiles of 64 g tokens.
 template <typename F>
-int tile_groups(bool f32, int cu, F&& tiles) {
-  int g = moe::fp8_most_groups(f32);
+int tile_groups(bool wide, int cu, F&& tiles) {
+  int g = moe::fp8_most_groups(wide);
   while (g > 1 && tiles(g / 2) <= cu) g /= 2;
   return g;
 }
@@ -155,7 +155,7 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
   if (!a || a->E < 1 || a->E > kMaxExperts || a->N < 16 || a->N % 16 != 0 || a->K < 16 ||
       a->K % 16 != 0 || a->K > (1 << 22) || a->M_cap < 1 || a->M_cap > INT32_MAX ||
       !a->split_sizes || !a->padded_offsets || !a->a || !a->a_s || !a->b || !a->b_s || !a->c ||
-      !type_ok(a->c_type) || !aligned16(a->workspace) || a->max_rows < 0 || a->cu_margin < 0 || !aligned16(a->a) ||
+      !type_ok(a->c_type) || (a->fp8_sums && a->c_type != MOE_TYPE_BF16) || !aligned16(a->workspace) || a->max_rows < 0 || a->cu_margin < 0 || !aligned16(a->a) ||
       !aligned16(a->b) || !aligned16(a->c))
     return MOE_ERR_INVALID_ARG;
   const int64_t nk = static_cast<int64_t>(a->N) * a->K;
@@ -165,14 +165,14 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
       (a->ldc != 0 && (a->ldc < a->N || a->ldc % 8 != 0)))
     return MOE_ERR_INVALID_ARG;
   const int64_t most = a->max_rows ? std::min<int64_t>(a->max_rows, a->M_cap) : a->M_cap;
-  const bool f32 = a->c_type == MOE_TYPE_F32;
+  const bool f32 = a->c_type == MOE_TYPE_F32, wide = !a->fp8_sums;
   const int64_t rows = rows_estimate(a->E, a->M_cap), tiles_n = ceil_div(a->N, kTileN);
   auto at_most = [&](int g) { return (ceil_div(a->M_cap, 64 * g) + a->E) * tiles_n; };
-  if (at_most(moe::fp8_most_groups(f32)) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (at_most(moe::fp8_most_groups(wide)) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   int cu = 0;
   if (moe_status st = moe::current_device(&cu)) return st;
   // half a tile of every group is filled on average
-  const int groups = tile_groups(f32, cu - a->cu_margin, [&](int g) { return (ceil_div(rows, 64 * g) + a->E / 2) * tiles_n; });
+  const int groups = tile_groups(wide, cu - a->cu_margin, [&](int g) { return (ceil_div(rows, 64 * g) + a->E / 2) * tiles_n; });
   const int64_t tiles = at_most(groups);
   if (a->cu_margin >= cu) return MOE_ERR_INVALID_ARG;
   moe::Fp8Args g{};
@@ -194,7 +194,7 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
   g.group_m = 4;
   g.err = a->err_flag;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (most <= 32 && a->N / 32 < kMaxGridX - 1) return launched(moe::launch_fp8_rows(g, most <= 16 ? 16 : 32, f32, s));
+  if (most <= 32 && a->N / 32 < kMaxGridX - 1) return launched(moe::launch_fp8_rows(g, most <= 16 ? 16 : 32, f32, wide, s));
   // K may be cut where there is room for its parts; the grid is a full one
   // then, since the tiles' number is known on the device only
   const int full = tile_grid(cu, a->cu_margin, INT32_MAX);
@@ -202,22 +202,23 @@ moe_status moe_grouped_gemm_fp8(const moe_gemm_fp8_args* a, void* stream) {
                    a->workspace_bytes >= static_cast<size_t>(full) * moe::kFp8PartFloats * sizeof(float);
   if (cut) g.part = static_cast<moe::fp8_f32x4*>(a->workspace);
   g.grid = cut ? full : tile_grid(cu, a->cu_margin, tiles);
-  return launched(moe::launch_fp8_gemm(g, f32, groups, s));
+  return launched(moe::launch_fp8_gemm(g, f32, wide, groups, s));
 }
 
 moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {
   if (!a || a->E < 1 || a->E > kMaxExperts || a->P < 16 || a->P % 16 != 0 || a->Q < 16 ||
       a->Q % 16 != 0 || a->M_cap < 128 || a->M_cap % 128 != 0 || a->M_cap > 4194304 ||
       !a->split_sizes || !a->padded_offsets || !a->a || !a->a_s || !a->b || !a->b_s || !a->c ||
-      !type_ok(a->c_type) || (a->accumulate && a->c_type != MOE_TYPE_F32) || a->cu_margin < 0 ||
+      !type_ok(a->c_type) || (a->accumulate && a->c_type != MOE_TYPE_F32) ||
+      (a->fp8_sums && a->c_type != MOE_TYPE_BF16) || a->cu_margin < 0 ||
       !aligned16(a->a) || !aligned16(a->b) || !aligned16(a->c))
     return MOE_ERR_INVALID_ARG;
-  const bool f32 = a->c_type == MOE_TYPE_F32;
+  const bool f32 = a->c_type == MOE_TYPE_F32, wide = !a->fp8_sums;
   auto count = [&](int g) { return a->E * ceil_div(a->P, 64 * g) * ceil_div(a->Q, kTileN); };
-  if (count(moe::fp8_most_groups(f32)) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (count(moe::fp8_most_groups(wide)) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   int cu = 0;
   if (moe_status st = moe::current_device(&cu)) return st;
-  const int groups = tile_groups(f32, cu - a->cu_margin, count);
+  const int groups = tile_groups(wide, cu - a->cu_margin, count);
   const int64_t tiles = count(groups);
   if (a->cu_margin >= cu) return MOE_ERR_INVALID_ARG;
   moe::Fp8Args g{};
@@ -238,7 +239,7 @@ moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {
   g.group_m = 4;
   g.err = a->err_flag;
   g.grid = tile_grid(cu, a->cu_margin, tiles);
-  return launched(moe::launch_fp8_wgrad(g, f32, groups, static_cast<hipStream_t>(stream)));
+  return launched(moe::launch_fp8_wgrad(g, f32, wide, groups, static_cast<hipStream_t>(stream)));
 }
 
 // ------------------------------------------------------- router losses ------

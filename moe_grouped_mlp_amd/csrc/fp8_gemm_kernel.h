@@ -5,19 +5,21 @@
 //
 //   C[t][n] = sum_b sa[b][t] sb[.][b] * sum_{k in block b} a[t][k] w[n][k]
 //
-// One v_mfma_f32_16x16x128_f8f6f4 covers a whole scale block of a 16 x 16
-// output tile, so the matrix core sums a block from zero and the vector ALU
-// adds it, scaled, to the fp32 accumulators: 4 fused multiply-adds (16
-// cycles) behind a 32-cycle MFMA, which the SIMD's other wave hides.  The
-// weight operand sits on the MFMA's rows and the tokens on its columns, so a
-// lane holds one token's outputs: the token's scale is one register per
-// column tile and the 128 x 128 weight scale is uniform.
+// The operands are widened to bf16, which holds every E4M3 value: four
+// v_mfma_f32_16x16x32_bf16 cover a whole scale block of a 16 x 16 output tile
+// and sum it from zero in fp32 (fp8_sums: one v_mfma_f32_16x16x128_f8f6f4 on the
+// codes as they are), and the vector ALU adds it, scaled, to the fp32
+// accumulators: 4 fused multiply-adds (16 cycles) behind 64 (32) cycles of MFMA,
+// which the SIMD's other wave hides.  The weight operand sits on the MFMA's rows
+// and the tokens on its columns, so a lane holds one token's outputs: the token's
+// scale is one register per column tile and the 128 x 128 weight scale is uniform.
 //
 // Work decomposition
-//   * Workgroup: 8 waves (two per SIMD), tile 256 tokens (fp32 output: 128) x
+//   * Workgroup: 8 waves (two per SIMD), tile 128 tokens (fp8_sums: 256) x
 //     256 weight rows, wave (wn, wt) = 128 weight rows x a quarter of the
-//     tokens (8 x 4 MFMA tiles); 64 or 128 tokens where tiles are few (JMAX).  A
-//     group's last tile runs with 64, 128 or 192 tokens if it holds no more.
+//     tokens (8 x 2 or 8 x 4 MFMA tiles); fewer tokens where tiles are few
+//     (JMAX).  A group's last tile runs with the fewest 64s of tokens that hold
+//     its rows.
 //   * Operands go from HBM straight into LDS (buffer loads with the LDS
 //     destination), two stages of one scale block (128 bytes of every row)
 //     each; their scales ride along.  16-byte chunk c of a row is stored at
@@ -30,32 +32,32 @@
 //   * Persistent workgroups walk the tiles of all experts, whose sizes are
 //     read from device memory.
 //
-// Eight experts, 16384 rows x 4096 x 14336: 780 us, 2.47 PFLOP/s.  Bound by
-// power: the clock falls to 1.5 .. 1.7 GHz while the MFMAs run, and a loop of
-// nothing but these MFMAs and their scaled sums makes 3.47 PFLOP/s (a product
-// with one scale for all, from a library: 2.71).  89 experts of 736 rows on
-// average x 5760 x 2880: 1200 us, 1.82 PFLOP/s, 10% of it in tiles that groups
-// and sides fill in part, the rest in tiles' starts and ends (23 steps each).
-//
 // Precision: the FP8 MFMAs add eight neighbouring products aligned to the
 // largest of them and keep 13 bits below it (seen with two products 2^-14
 // apart, in all four FP8 forms; products of different eights add exactly in
-// fp32).  On activations that is 2e-5 to 4e-5 of the result, a fiftieth of a
-// bf16 rounding, so bf16 outputs take it.  fp32 outputs would not be worth
-// their bits: there the codes are widened to bf16 in registers (16
-// conversions per 32 codes of a lane) and four 16x16x32 bf16 MFMAs, whose
-// sums are exact to 1e-8, stand for one FP8 MFMA, at half its peak rate.
+// fp32).  On activations that is 2e-5 to 4e-5 of the result, and moves a bf16
+// output by a step where it lies that near the border of two.  The bf16 MFMAs
+// lose nothing of that kind (sums exact to 1e-8), at half the peak rate and 16
+// conversions per 32 codes of a lane, so sums are theirs unless the caller asks
+// for the FP8 ones.
 //
 // The weight gradient is the same product with the routed rows as K: both
 // operands transposed copies with one scale per row and block, so its
 // accumulation multiplies by two scales.
 //
-// An fp32 output's codes are widened to bf16 (Fp8Frag), 4 MFMAs a block.  Beside
-// a 16-cycle MFMA a SIMD issues two vector instructions for nothing, each
-// further one costs 4 cycles (measured with two waves); here they are 4.7 (2.5
-// to widen, 2 to scale), so the MFMAs are busy for a quarter to a third of the
-// time.  32 experts of 7168 x 2048 from 16384 rows (4.5 steps a tile): 855 us,
-// of which 690 without the stores, 300 the stores (1.88 GB) alone.
+// Bound by the vector instructions beside the MFMAs: a SIMD issues two beside a
+// 16-cycle MFMA for nothing, each further one costs 4 cycles (measured with two
+// waves).  The product has 3.5 (2.5 to widen, 1 to scale): eight experts, 16384
+// rows x 4096 x 14336, 1617 us, 1.19 PFLOP/s; 89 experts of 736 rows on average x
+// 5760 x 2880, 2241 us, 970 TFLOP/s.  The weight gradient has 4.7 (2 to scale),
+// and its MFMAs are busy for a quarter to a third of the time: 32 experts of 7168
+// x 2048 from 16384 rows (4.5 steps a tile), fp32, 855 us, of which 690 without
+// the stores, 300 the stores (1.88 GB) alone.
+// With fp8_sums the first product takes 780 us on a cool device (2.47 PFLOP/s; a
+// product with one scale for all, from a library: 2.71) and about 920 in a long
+// run, where power bounds it: the clock falls to 1.5 .. 1.7 GHz while the MFMAs
+// run, and a loop of nothing but these MFMAs and their scaled sums makes 3.47
+// PFLOP/s.  The second takes 1200 and 1450.
 #include <type_traits>
 #include <utility>
 
@@ -323,11 +325,12 @@ MOE_DEV constexpr int fp8_w_off(int i) {
   return F32 ? 16 * (i % 4) : 32 * (i % 4 / 2) + 4 * (i % 2);
 }
 
-// JMAX: MFMA token tiles per wave; WG: the weight gradient; F32: fp32 output,
-// summed from widened operands.
-template <int JMAX, bool WG, bool F32>
+// JMAX: MFMA token tiles per wave; WG: the weight gradient; F32: fp32 output;
+// WIDE: summed in fp32 from widened operands.
+template <int JMAX, bool WG, bool F32, bool WIDE>
 __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 2))) void fp8_gemm_kernel(
     const Fp8Args g) {
+  static_assert(WIDE || !F32, "an fp32 output is worth fp32 sums");
   constexpr int BT = 64 * JMAX;   // tokens of a tile
   __shared__ __attribute__((aligned(1024))) uint8_t sT0[BT * kFp8Blk], sT1[BT * kFp8Blk];
   // weights: the rows of tiles 0 .. 3 (a) and 4 .. 7 (b) of both wave columns;
@@ -467,7 +470,7 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
         const float* sS = scales(sWb);
         const float* nS = scales(nWb);
         constexpr int P = decltype(par)::value;
-        Fp8Frag<F32> t[J];
+        Fp8Frag<WIDE> t[J];
   #pragma unroll
         for (int j = 0; j < J; ++j) t[j].set(tr[j].x, tr[j].y);
         constexpr int kLag = 3, kRing = 4;
@@ -498,7 +501,7 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
             asm volatile("" ::: "memory");
             read_w(std::integral_constant<int, 0>{}, nWa, nS);
           }
-          Fp8Frag<F32> w;
+          Fp8Frag<WIDE> w;
           w.set(wr[i & 1].x, wr[i & 1].y);
           if constexpr (WG) wfm[i % kW] = wf[i & 1];
           fp8_for<J>([&](auto j) {

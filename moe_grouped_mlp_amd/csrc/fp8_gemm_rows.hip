@@ -3,12 +3,12 @@
 //
 // A workgroup takes 32 weight rows of one expert; its four waves take scale
 // blocks 4 u + w of K, so one row's 512 consecutive bytes are in flight over
-// the workgroup, and kUnroll of those per wave.  Per block: two MFMAs
+// the workgroup, and kUnroll of those per wave.  Per block: two sums by MFMAs
 // (weights on the rows, 16 tokens on the columns) from zero, then the scaled
 // sum in fp32; the waves' sums are added in a fixed order through LDS.
 // MFMA row m of weight tile i is weight row 8 (m / 4) + 4 i + m % 4, so a
 // lane stores 8 consecutive outputs of its token.  Two rows for each of 8
-// experts of 28672 x 4096: 157 us, 6.0 TB/s (the tiled kernel, which waits at
+// experts of 28672 x 4096: 159 us, 5.9 TB/s (the tiled kernel, which waits at
 // two barriers a step, is for more).
 #include "fp8_gemm_kernel.h"
 
@@ -37,7 +37,7 @@ struct RowsArgs {
   int N, K, M_cap;
 };
 
-template <int J, bool F32>
+template <int J, bool F32, bool WIDE>
 __global__ __launch_bounds__(kRowsThreads) void fp8_rows_kernel(const RowsArgs g) {
   constexpr int kUnroll = J == 1 ? 4 : 2;
   __shared__ __attribute__((aligned(16))) f32x4 s_red[4][2 * J][kWave];
@@ -100,12 +100,12 @@ __global__ __launch_bounds__(kRowsThreads) void fp8_rows_kernel(const RowsArgs g
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        Fp8Frag<F32> ft[J];
+        Fp8Frag<WIDE> ft[J];
 #pragma unroll
         for (int j = 0; j < J; ++j) ft[j].set(t[u][j][0], t[u][j][1]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          Fp8Frag<F32> fw;
+          Fp8Frag<WIDE> fw;
           fw.set(w[u][i][0], w[u][i][1]);
 #pragma unroll
           for (int j = 0; j < J; ++j) {
@@ -150,13 +150,13 @@ __global__ __launch_bounds__(kRowsThreads) void fp8_rows_kernel(const RowsArgs g
 
 }  // namespace
 
-hipError_t launch_fp8_rows(const Fp8Args& g, int tile_rows, bool f32, hipStream_t s) {
+hipError_t launch_fp8_rows(const Fp8Args& g, int tile_rows, bool f32, bool wide, hipStream_t s) {
   const dim3 grid((g.N + kRowsBN - 1) / kRowsBN, g.E);
   const RowsArgs r{g.split, g.padded, g.a, g.a_s, g.b, g.b_s, g.b_stride, g.b_s_stride, g.c, g.ldc, g.err,
                    g.N, g.K, static_cast<int>(g.M_cap)};
   auto go = [&](auto kernel) { kernel<<<grid, kRowsThreads, 0, s>>>(r); };
-  if (tile_rows == 16) f32 ? go(fp8_rows_kernel<1, true>) : go(fp8_rows_kernel<1, false>);
-  else f32 ? go(fp8_rows_kernel<2, true>) : go(fp8_rows_kernel<2, false>);
+  if (tile_rows == 16) f32 ? go(fp8_rows_kernel<1, true, true>) : wide ? go(fp8_rows_kernel<1, false, true>) : go(fp8_rows_kernel<1, false, false>);
+  else f32 ? go(fp8_rows_kernel<2, true, true>) : wide ? go(fp8_rows_kernel<2, false, true>) : go(fp8_rows_kernel<2, false, false>);
   return hipGetLastError();
 }
 

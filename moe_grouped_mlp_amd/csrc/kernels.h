@@ -162,13 +162,15 @@ struct Fp8Args {
   fp8_f32x4* part;         // product (nullable): one tile's fp32 sums per workgroup
 };
 constexpr int kFp8PartFloats = 256 * 256;
-// Tiles are of 64 `groups` tokens (1, 2 or, bf16 output only, 4) x 256 weight rows.
-inline int fp8_most_groups(bool f32) { return f32 ? 2 : 4; }
+// f32: the output's type; wide: operands widened to bf16 and summed in fp32 (an
+// fp32 output's always).  Tiles are of 64 `groups` tokens (1, 2 or, not wide, 4)
+// x 256 weight rows.
+inline int fp8_most_groups(bool wide) { return wide ? 2 : 4; }
 // with g.part also the launch that joins the parts of tiles whose K was cut
-hipError_t launch_fp8_gemm(const Fp8Args& g, bool f32, int groups, hipStream_t s);
+hipError_t launch_fp8_gemm(const Fp8Args& g, bool f32, bool wide, int groups, hipStream_t s);
 // groups of few rows; tile_rows: 16 or 32 tokens at a time
-hipError_t launch_fp8_rows(const Fp8Args& g, int tile_rows, bool f32, hipStream_t s);
-hipError_t launch_fp8_wgrad(const Fp8Args& g, bool f32, int groups, hipStream_t s);
+hipError_t launch_fp8_rows(const Fp8Args& g, int tile_rows, bool f32, bool wide, hipStream_t s);
+hipError_t launch_fp8_wgrad(const Fp8Args& g, bool f32, bool wide, int groups, hipStream_t s);
 
 // ---- router losses ----------------------------------------------------------
 size_t router_loss_workspace_bytes(int T, int E);

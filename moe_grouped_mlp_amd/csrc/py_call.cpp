@@ -241,7 +241,7 @@ PyObject* quantize_fp8(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
 PyObject* grouped_gemm_fp8(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
   constexpr const char* fn = "moe_grouped_gemm_fp8";
   return guarded(fn, [&] {
-    Args p(fn, args, n_args, 21);
+    Args p(fn, args, n_args, 22);
     moe_gemm_fp8_args a{};
     a.E = p.i32();
     a.N = p.i32();
@@ -253,6 +253,7 @@ PyObject* grouped_gemm_fp8(PyObject*, PyObject* const* args, Py_ssize_t n_args) 
     a.c_type = p.i32();
     a.max_rows = p.i32();
     a.cu_margin = p.i32();
+    a.fp8_sums = p.truth();
     const Size E = a.E, N = a.N, K = a.K, M = a.M_cap, nk = N * K, ns = blocks(N) * blocks(K);
     a.split_sizes = p.buf<int32_t>("split_sizes", kI32, E);
     a.padded_offsets = p.buf<int32_t>("padded_offsets", kI32, E + 1);
@@ -270,7 +271,7 @@ PyObject* grouped_gemm_fp8(PyObject*, PyObject* const* args, Py_ssize_t n_args) 
 PyObject* grouped_wgrad_fp8(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
   constexpr const char* fn = "moe_grouped_wgrad_fp8";
   return guarded(fn, [&] {
-    Args p(fn, args, n_args, 17);
+    Args p(fn, args, n_args, 18);
     moe_wgrad_fp8_args a{};
     a.E = p.i32();
     a.P = p.i32();
@@ -279,6 +280,7 @@ PyObject* grouped_wgrad_fp8(PyObject*, PyObject* const* args, Py_ssize_t n_args)
     a.c_type = p.i32();
     a.accumulate = p.truth();
     a.cu_margin = p.i32();
+    a.fp8_sums = p.truth();
     const Size E = a.E, P = a.P, Q = a.Q, M = a.M_cap;
     a.split_sizes = p.buf<int32_t>("split_sizes", kI32, E);
     a.padded_offsets = p.buf<int32_t>("padded_offsets", kI32, E + 1);
