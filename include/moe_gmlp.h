@@ -891,8 +891,8 @@ moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* args, void* stream);
  *   An id outside [0, E) (a dropped pick) counts nowhere, one listed twice
  *   twice.  Logits may be -infinity (an expert ruled out); a token whose
  *   logits are all -infinity is left out as a masked one.  n == 0 gives
- *   zeros.  Sums over tokens are made in a fixed order (fp32 inside a
- *   workgroup, fp64 over workgroups): the same inputs give the same bits.
+ *   zeros.  Sums over tokens are made in fp64 and in a fixed order: the same
+ *   inputs give the same bits.
  *   Needs 0 <= T, 1 <= E <= 1024, 1 <= k <= min(E, 8), T * k < 2^31;
  *   workspace of moe_router_loss_workspace_size(T, E) bytes, 8-byte aligned,
  *   no initialisation; calls that overlap in time must not share one.

@@ -12,9 +12,10 @@
 // 64 / L tokens.  Lane g of a token holds experts 4 (g + L i) + c (VEC:
 // E % 4 == 0 and 16-byte aligned rows, one float4 each), else g + L i.  The loss
 // kernel keeps each lane's sums of p over its tokens in registers, adds them
-// over the workgroup in a fixed order and writes one fp32 partial per expert and
-// workgroup; a second launch adds these in fp64, unless there is one workgroup
-// only, which then does all of it.
+// over the workgroup in a fixed order and writes one partial per expert and
+// workgroup; a second launch adds these, unless there is one workgroup only,
+// which then does all of it.  Sums over tokens are fp64 throughout (a token's own
+// sums over its experts fp32).
 //
 // Bound by latencies: a workgroup makes one or a few passes, so all it reads
 // goes out at once, before the first use.  16384 tokens of 256 experts: 8.2 us
@@ -43,17 +44,6 @@ MOE_DEV float group_sum(float v) {
 template <int L>
 MOE_DEV float group_max(float v) {
   return group_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
-}
-
-// exp(x) for x <= 0 (or NaN), within 2 steps: x log2(e) in two parts, the
-// leading one through the hardware's exp2.  Below -200 it is 0.
-MOE_DEV float exp_neg(float x) {
-  x = x < -200.0f ? -200.0f : x;
-  constexpr float kHi = 1.44269502162933349609375f, kLo = 1.925963033500011079e-8f;   // log2(e)
-  const float t = x * kHi;
-  const float r = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -t));   // what t left out
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e, r * 0.693147182464599609375f, e);            // 2^r = 1 + r ln 2
 }
 
 // Expert of a lane's i-th logit.
@@ -102,7 +92,7 @@ MOE_DEV bool token_softmax(float (&p)[P], float& lse) {
   const float mm = m == kNegInf ? 0.0f : m;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    p[i] = exp_neg(p[i] - mm);
+    p[i] = expf(p[i] - mm);
     z += p[i];
     nan = p[i] != p[i] ? 1.0f : nan;
   }
@@ -140,16 +130,19 @@ constexpr int kSumExperts = 16;   // experts of a workgroup of the second launch
 __host__ __device__ constexpr int sum_blocks(int E) { return (E + kSumExperts - 1) / kSumExperts; }
 
 // The workspace: the balance terms (fp64) and the count of the second launch's
-// workgroups, then the loss kernel's partials.
+// workgroups, then the loss kernel's partials: sums, then counts.
 struct LossWs {
   double* terms;
   int32_t* done;
-  float2 *part_z, *part;   // {sum lse^2, n} of a workgroup; its {sum of p, picks} per expert
+  double *part_z, *part_p;    // a workgroup's sum of lse^2; its sum of p per expert
+  int32_t *part_n, *part_c;   // its tokens; its picks per expert
   MOE_DEV LossWs(void* p, int E, int blocks)
       : terms(static_cast<double*>(p)),
         done(reinterpret_cast<int32_t*>(terms + sum_blocks(E))),
-        part_z(reinterpret_cast<float2*>(terms + sum_blocks(E) + 1)),
-        part(part_z + blocks) {}
+        part_z(terms + sum_blocks(E) + 1),
+        part_p(part_z + blocks),
+        part_n(reinterpret_cast<int32_t*>(part_p + static_cast<int64_t>(blocks) * E)),
+        part_c(part_n + blocks) {}
 };
 
 // (Arguments past about 104 bytes, a kernel's own and those that reading the
@@ -174,16 +167,16 @@ __global__ __launch_bounds__(THREADS) void router_loss_kernel(
     const uint8_t* __restrict__ mask, int T, int E, int k, int blocks, void* ws, LossOut out) {
   constexpr int kWaves = THREADS / kWave, kTok = THREADS / L;   // tokens the workgroup covers at once
   constexpr int kOwnPicks = (kMaxTopK + L - 1) / L;
-  __shared__ float s_p[kWaves * L * P];   // the waves' sums, expert-major: at most 64 KB
+  __shared__ double s_p[kWaves * L * P];   // the waves' sums, expert-major: at most 128 KB
   __shared__ int32_t s_c[L * P];
-  __shared__ float s_z[kWaves];
+  __shared__ double s_z[kWaves];
   __shared__ int32_t s_n[kWaves];
   __shared__ double s_wave[kWaves];
   const int tid = threadIdx.x, g = tid % L, wave = tid / kWave;
   for (int e = tid; e < E; e += THREADS) s_c[e] = 0;
   __syncthreads();
-  float sum[P] = {};
-  float zsum = 0.0f;
+  double sum[P] = {};
+  double zsum = 0.0;
   int32_t n = 0;
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok; t0 < T;
        t0 += static_cast<int64_t>(blocks) * kTok) {
@@ -199,7 +192,7 @@ __global__ __launch_bounds__(THREADS) void router_loss_kernel(
 #pragma unroll
       for (int i = 0; i < P; ++i) sum[i] += p[i];
       if (g == 0) {
-        zsum += lse * lse;
+        zsum = __builtin_fma(static_cast<double>(lse), static_cast<double>(lse), zsum);
         ++n;
       }
 #pragma unroll
@@ -231,7 +224,7 @@ __global__ __launch_bounds__(THREADS) void router_loss_kernel(
     }
   }
   __syncthreads();
-  float z = 0.0f;
+  double z = 0.0;
   int32_t m = 0;
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
@@ -239,13 +232,13 @@ __global__ __launch_bounds__(THREADS) void router_loss_kernel(
     m += s_n[w];
   }
   static_assert(L * P <= THREADS, "an expert a thread");
-  float v = 0.0f;
+  double v = 0.0;
   if (tid < E) {
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) v += s_p[w * L * P + tid];
   }
   if (blocks == 1) {   // these are the whole sums
-    const double mean = m > 0 ? static_cast<double>(v) / m : 0.0;
+    const double mean = m > 0 ? v / m : 0.0;
     if (tid < E) {
       out.counts[tid] = s_c[tid];
       out.prob_mean[tid] = static_cast<float>(mean);
@@ -255,9 +248,13 @@ __global__ __launch_bounds__(THREADS) void router_loss_kernel(
     return;
   }
   const LossWs w(ws, E, blocks);
-  if (tid < E) w.part[static_cast<int64_t>(blockIdx.x) * E + tid] = float2{v, __int_as_float(s_c[tid])};
+  if (tid < E) {
+    w.part_p[static_cast<int64_t>(blockIdx.x) * E + tid] = v;
+    w.part_c[static_cast<int64_t>(blockIdx.x) * E + tid] = s_c[tid];
+  }
   if (tid == 0) {
-    w.part_z[blockIdx.x] = float2{z, __int_as_float(m)};
+    w.part_z[blockIdx.x] = z;
+    w.part_n[blockIdx.x] = m;
     if (blockIdx.x == 0) *w.done = 0;
   }
 }
@@ -277,25 +274,26 @@ __global__ __launch_bounds__(kThreads) void router_loss_sum_kernel(void* ws, int
   const int tid = threadIdx.x, e = blockIdx.x * kSumExperts + tid % kSumExperts;
   // (loads from a clamped place, the value dropped after: a load behind a
   // condition is waited for before the next one, 9.8 us in all against 4.7)
-  float2 v[U];
+  double vp[U];
+  int32_t vc[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    v[u] = w.part[static_cast<int64_t>(min(tid / kSumExperts + u * kRows, blocks - 1)) * E + min(e, E - 1)];
-#pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (tid / kSumExperts + u * kRows >= blocks || e >= E) v[u] = float2{0.0f, 0.0f};
+  for (int u = 0; u < U; ++u) {
+    const int64_t at = static_cast<int64_t>(min(tid / kSumExperts + u * kRows, blocks - 1)) * E + min(e, E - 1);
+    vp[u] = w.part_p[at];
+    vc[u] = w.part_c[at];
+  }
   static_assert(kMaxLossBlocks == kThreads, "one partial a thread");
-  float2 zn = w.part_z[min(tid, blocks - 1)];
-  if (tid >= blocks) zn = float2{0.0f, 0.0f};
+  double z = w.part_z[min(tid, blocks - 1)];
+  int32_t n = w.part_n[min(tid, blocks - 1)];
+  if (tid >= blocks) z = 0.0, n = 0;
   double p = 0.0;
   int32_t c = 0;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    p += v[u].x;
-    c += __float_as_int(v[u].y);
+    if (tid / kSumExperts + u * kRows >= blocks || e >= E) vp[u] = 0.0, vc[u] = 0;
+    p += vp[u];
+    c += vc[u];
   }
-  double z = zn.x;
-  int32_t n = __float_as_int(zn.y);
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     z += __shfl_xor(z, o, kWave);
@@ -499,8 +497,8 @@ static int loss_blocks(int T, int E) {
 }
 
 size_t router_loss_workspace_bytes(int T, int E) {
-  const size_t blocks = loss_blocks(T, E);
-  return 8 * (sum_blocks(E) + 1 + blocks + blocks * static_cast<size_t>(E));
+  const size_t blocks = loss_blocks(T, E), parts = blocks + blocks * static_cast<size_t>(E);
+  return 8 * (sum_blocks(E) + 1 + parts) + 4 * parts;
 }
 
 hipError_t launch_router_loss(const moe_router_loss_args& a, hipStream_t s) {
