@@ -925,8 +925,10 @@ moe_status moe_router_loss(const moe_router_loss_args* args, void* stream);
  *               + kept(t) * dloss[1] * 2 z_coef * lse[t] / n)
  *   with counts and n = n_tokens[0] as moe_router_loss wrote them (n == 0: no
  *   loss terms).  The mask leaves a token out of the losses only; its dprobs
- *   act as any other's.  A token whose logits are all -infinity gets zeros.
- *   counts and n_tokens may be NULL if both coefficients are 0. */
+ *   act as any other's.  Without any (none given, or zeros) it gets zeros, also
+ *   where its logits are NaN or infinite.  A token whose logits are all
+ *   -infinity gets zeros.  counts and n_tokens may be NULL if both
+ *   coefficients are 0. */
 typedef struct moe_router_bwd_args {
   int32_t T, E, k;
   const float* logits;            /* [T][E] device */

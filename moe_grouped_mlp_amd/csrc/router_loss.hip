@@ -443,12 +443,22 @@ __global__ __launch_bounds__(kThreads) void router_bwd_kernel(
         }
       }
     }
+    // a token that is left out and has no gradient of its own gets zeros, whatever
+    // its logits are: padding may hold NaN
+    bool zero = !any;
+    if (!keep) {
+      float own = 0.0f;
+#pragma unroll
+      for (int i = 0; i < P; ++i)
+        if (expert_at<L, VEC>(g, i) < E && v[i] != 0.0f) own = 1.0f;   // (also for NaN)
+      zero = zero || group_max<L>(own) == 0.0f;
+    }
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < P; ++i) dot += p[i] * v[i];
     dot = group_sum<L>(dot) - (kept ? cz * lse : 0.0f);
 #pragma unroll
-    for (int i = 0; i < P; ++i) v[i] = any ? p[i] * (v[i] - dot) : 0.0f;
+    for (int i = 0; i < P; ++i) v[i] = zero ? 0.0f : p[i] * (v[i] - dot);
     float* out = dlogits + t * E;
     if constexpr (VEC) {
 #pragma unroll
