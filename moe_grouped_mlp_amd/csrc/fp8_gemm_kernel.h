@@ -356,6 +356,7 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
   for (int item = fp8_workgroup(g); item < total * parts; item += g.grid) {
     const Fp8Tile tile = fp8_tile_at<BT, WG>(g, s_tab, item / parts);
     const int e = tile.e, n_e = tile.n_e, start = tile.start, rows_t = tile.rows_t, t0 = tile.t0, n0 = tile.n0;
+    if (WG && g.accumulate && n_e == 0) continue;   // nothing to add: C stays as it is
     // the steps [k0, k1) of this part
     const int all_K = WG ? (n_e + kFp8Blk - 1) / kFp8Blk * kFp8Blk : g.K;
     const int all_steps = (all_K + kFp8Blk - 1) / kFp8Blk;

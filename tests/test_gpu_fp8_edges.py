@@ -1,0 +1,35 @@
+"""Calls of the block-scaled FP8 products at their edges."""
+
+import numpy as np
+import pytest
+import torch
+
+import moe_grouped_mlp_amd as mg
+
+from .test_gpu_fp8 import DEV, _starts, _wgrad, _wgrad_operands, _wgrad_ref
+
+pytestmark = pytest.mark.gpu
+
+
+def setup_module(module):
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    mg.lib()
+
+
+def test_accumulation_leaves_empty_experts_as_they_are():
+    """An expert with no rows adds nothing: not even the sign of a zero or a
+    NaN's bits change."""
+    sizes, P, Q = [0, 130, 0, 1, 0], 272, 144
+    starts = _starts(sizes)
+    ops = _wgrad_operands(np.random.default_rng(1), sizes, starts, starts[-1] + 128, P, Q, exact=True)
+    ref, _ = _wgrad_ref(*ops, sizes, starts)
+    bits = torch.randint(-2 ** 31, 2 ** 31 - 1, (5, P, Q), dtype=torch.int32, device=DEV,
+                         generator=torch.Generator(DEV).manual_seed(1))
+    bits[0] = -2 ** 31      # -0
+    bits[2, 0] = 0x7F800001  # a signalling NaN
+    c = bits.view(torch.float32).clone()
+    c[[1, 3]] = 3.0
+    _wgrad(*ops, sizes, starts, c=c, accumulate=True)
+    for e in (0, 2, 4):
+        assert torch.equal(c[e].view(torch.int32), bits[e]), e
+    np.testing.assert_array_equal(c[[1, 3]].double().cpu().numpy(), ref[[1, 3]] + 3.0)
