@@ -812,6 +812,8 @@ moe_status moe_quantize_fp8(const moe_quant_fp8_args* args, void* stream);
  *   max_rows: the most rows any group can hold if the caller knows it (a
  *   decoding step of T tokens: T), 0 if not.  It chooses among kernels;
  *   groups that turn out larger are computed all the same.
+ *   cu_margin: CUs to leave free for concurrent kernels (the kernel for at
+ *   most 32 rows a group, which runs on all of them, is then not taken).
  *   workspace: optional, moe_grouped_gemm_fp8_workspace_size(...) bytes (0:
  *   none would be used; a smaller one is not used), 16-byte aligned, no
  *   initialisation; calls that overlap in time must not share one.  With it a

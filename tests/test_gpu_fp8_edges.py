@@ -6,7 +6,7 @@ import torch
 
 import moe_grouped_mlp_amd as mg
 
-from .test_gpu_fp8 import DEV, _starts, _wgrad, _wgrad_operands, _wgrad_ref
+from .test_gpu_fp8 import DEV, _margin, _operands, _product, _starts, _wgrad, _wgrad_operands, _wgrad_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,16 @@ def test_accumulation_leaves_empty_experts_as_they_are():
     for e in (0, 2, 4):
         assert torch.equal(c[e].view(torch.int32), bits[e]), e
     np.testing.assert_array_equal(c[[1, 3]].double().cpu().numpy(), ref[[1, 3]] + 3.0)
+
+
+@pytest.mark.parametrize("hint", [1, 16, 20, 32])
+def test_few_rows_leave_the_margin_free(hint):
+    """With a cu_margin products of few rows run on one workgroup a CU, as all
+    others do: the tiled kernel, whose sums over K are in its own order."""
+    sizes, N, K = [3, 0, 16, 1, 20], 272, 1168
+    starts = _starts(sizes)
+    ops = _operands(np.random.default_rng(2), sizes, starts, starts[-1], N, K)
+    tiled = _product(*ops, sizes, starts, cu_margin=_margin(40))
+    assert torch.equal(_product(*ops, sizes, starts, max_rows=hint, cu_margin=_margin(40)), tiled)
+    few = _product(*ops, sizes, starts, max_rows=hint)
+    assert not torch.equal(few, tiled)   # the other kernel, or this test shows nothing
