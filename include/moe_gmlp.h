@@ -761,13 +761,13 @@ typedef enum moe_type { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type;
  *     values: qT [batch][cols][rows], sT
  *     [batch][ceil(cols/128)][ceil(rows/128)] (the input-gradient operand).
  *   Needs cols % 16 == 0 and, but for ROW, rows % 16 == 0; rows or batch 0
- *   is a call with nothing to do.  live (optional, [batch], say the split
- *   sizes): entries with live[b] == 0 are skipped, as in
- *   moe_quantize_mxfp8.  row_end (optional, device int32, say
- *   padded_offsets + E): rows at or past *row_end are not read and not
- *   written in the copies that have rows as rows; a block of 128 rows that
- *   starts there is not written in the others, and one that contains
- *   *row_end has zeros for the rows past it. */
+ *   is a call with nothing to do, whose pointers may be NULL.  live
+ *   (optional, [batch], say the split sizes): entries with live[b] == 0
+ *   are skipped, as in moe_quantize_mxfp8.  row_end (optional, device
+ *   int32, say padded_offsets + E): rows at or past *row_end are not read
+ *   and not written in the copies that have rows as rows; a block of 128
+ *   rows that starts there is not written in the others, and one that
+ *   contains row_end has zeros for the rows past it. */
 #define MOE_QUANT_TILE 3
 
 typedef struct moe_quant_fp8_args {

@@ -123,19 +123,21 @@ extern "C" {
 moe_status moe_quantize_fp8(const moe_quant_fp8_args* a, void* stream) {
   if (!a || a->mode < MOE_QUANT_ROW || a->mode > MOE_QUANT_TILE || a->batch < 0 || a->rows < 0 ||
       a->cols < 16 || a->cols % 16 != 0 || (a->mode != MOE_QUANT_ROW && a->rows % 16 != 0) ||
-      !a->x || !a->q || !a->s || (a->mode == MOE_QUANT_BOTH && (!a->qT || !a->sT)) ||
-      (a->mode == MOE_QUANT_TILE && (a->qT != nullptr) != (a->sT != nullptr)) ||
       !aligned16(a->x) || !aligned16(a->q) || !aligned16(a->qT))
     return MOE_ERR_INVALID_ARG;
   const int64_t n = static_cast<int64_t>(a->rows) * a->cols;
   if (a->x_stride != 0 && (a->x_stride < n || a->x_stride % 8 != 0)) return MOE_ERR_INVALID_ARG;
+  const bool nothing = a->batch == 0 || a->rows == 0;   // empty tensors may have no address
+  if (!nothing && (!a->x || !a->q || !a->s || (a->mode == MOE_QUANT_BOTH && (!a->qT || !a->sT)) ||
+                   (a->mode == MOE_QUANT_TILE && (a->qT != nullptr) != (a->sT != nullptr))))
+    return MOE_ERR_INVALID_ARG;
   const int64_t cb = ceil_div(a->cols, kBlk);
   const int64_t units = a->mode == MOE_QUANT_ROW ? ceil_div(a->rows, 16) * ceil_div(cb, 8)
                                                  : ceil_div(a->rows, kBlk) * cb;
   if (a->batch > 65535 || units >= kMaxGridX) return MOE_ERR_UNSUPPORTED;
   int cu = 0;
   if (moe_status st = moe::current_device(&cu)) return st;
-  if (a->batch == 0 || a->rows == 0) return MOE_OK;
+  if (nothing) return MOE_OK;
   moe_quant_fp8_args b = *a;
   if (b.x_stride == 0) b.x_stride = n;
   return launched(moe::launch_quantize_fp8(b, static_cast<hipStream_t>(stream)));

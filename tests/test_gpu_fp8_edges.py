@@ -46,3 +46,13 @@ def test_few_rows_leave_the_margin_free(hint):
     assert torch.equal(_product(*ops, sizes, starts, max_rows=hint, cu_margin=_margin(40)), tiled)
     few = _product(*ops, sizes, starts, max_rows=hint)
     assert not torch.equal(few, tiled)   # the other kernel, or this test shows nothing
+
+
+@pytest.mark.parametrize("mode", [mg.QUANT_ROW, mg.QUANT_COL, mg.QUANT_BOTH, mg.QUANT_TILE])
+def test_quantize_of_empty_tensors(mode):
+    u8 = dict(dtype=torch.uint8, device=DEV)
+    x = torch.empty(0, 48, dtype=torch.bfloat16, device=DEV)
+    s = torch.empty(1, 0, device=DEV)
+    mg.moe_quantize_fp8(mode=mode, batch=1, rows=0, cols=48, x=x, q=torch.empty(0, 48, **u8), s=s,
+                        qT=torch.empty(48, 0, **u8), sT=torch.empty(0, 48, device=DEV))
+    torch.cuda.synchronize()
