@@ -767,7 +767,7 @@ typedef enum moe_type { MOE_TYPE_BF16 = 0, MOE_TYPE_F32 = 1 } moe_type;
  *   int32, say padded_offsets + E): rows at or past *row_end are not read
  *   and not written in the copies that have rows as rows; a block of 128
  *   rows that starts there is not written in the others, and one that
- *   contains row_end has zeros for the rows past it. */
+ *   contains *row_end has zeros for the rows past it. */
 #define MOE_QUANT_TILE 3
 
 typedef struct moe_quant_fp8_args {

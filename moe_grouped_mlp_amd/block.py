@@ -105,6 +105,7 @@ class ExpertBlock:
         self.mx4 = prec == B.PREC_MXFP4
         self.fp8 = prec == B.PREC_FP8
         self._router_bufs, self._ws_grad, self.grad_norm = {}, {}, None
+        self._dprobs_valid = False   # whether dprobs are of the rows last routed
         if self.fp8 and (recompute or unfused):
             raise ValueError("the FP8 layer has no recompute path, and always runs as separate passes")
         if wgrad_type != B.TYPE_BF16 and not self.fp8:
@@ -315,6 +316,7 @@ class ExpertBlock:
     # ------------------------------------------------------------ forward --
     def route(self, expert_idx: torch.Tensor, probs: torch.Tensor,
               x: Optional[torch.Tensor] = None) -> None:
+        self._dprobs_valid = False
         flags = B.PERMUTE_BUILD_MAP
         xq, xs = self._mx_dst("xp")
         if x is not None:
@@ -359,6 +361,7 @@ class ExpertBlock:
                               expert_idx=self.expert_idx, probs=self.probs)
             self.route(self.expert_idx, self.probs, x)
             return
+        self._dprobs_valid = False
         if getattr(self, "ws_router", None) is None:
             # its counters start at zero; every call leaves them at zero
             self.ws_router = torch.zeros(B.moe_router_route_workspace_size(T, E_all, self.E),
@@ -446,6 +449,7 @@ class ExpertBlock:
                         row_id_map=self.row_id_map, yp=yp, out=out,
                         dprobs_p=self.dprobs_p if dprobs else None,
                         dprobs=self.dprobs if dprobs else None)
+        self._dprobs_valid = self._dprobs_valid or dprobs
 
     def forward(self, x, expert_idx, probs, timing_events=None):
         self.route(expert_idx, probs, x)
@@ -673,9 +677,14 @@ class ExpertBlock:
                         dprobs: Optional[torch.Tensor] = None):
         """Gradient of the logits given to router_loss(): of its two losses
         (dloss fp32 [2], their upstream gradients; ones by default) and of the
-        kept probabilities (backward()'s dprobs by default)."""
+        kept probabilities (by default the dprobs of the backward() since the
+        last route(); zeros if only the losses count).  Several shares of one
+        layer (first_expert) each add both losses' gradient: before their
+        dlogits are summed, all but one are given a dloss of zeros."""
         if getattr(self, "_router_args", None) is None:
             raise RuntimeError("router_backward() needs router_loss() first")
+        if dprobs is None and not self._dprobs_valid:
+            raise RuntimeError("router_backward() needs the backward() of the rows last routed, or dprobs")
         dprobs = self.dprobs if dprobs is None else dprobs
         if tuple(dprobs.shape) != (self._router_args["T"], self.k):
             raise ValueError(f"dprobs must be [{self._router_args['T']}][{self.k}]")

@@ -1,12 +1,14 @@
-"""Calls of the block-scaled FP8 products at their edges."""
+"""Calls of the block-scaled FP8 layer at their edges."""
 
 import numpy as np
 import pytest
 import torch
 
 import moe_grouped_mlp_amd as mg
+from oracle import step as st
 
 from .test_gpu_fp8 import DEV, _margin, _operands, _product, _starts, _wgrad, _wgrad_operands, _wgrad_ref
+from .test_gpu_fp8_block import _inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +58,31 @@ def test_quantize_of_empty_tensors(mode):
     mg.moe_quantize_fp8(mode=mode, batch=1, rows=0, cols=48, x=x, q=torch.empty(0, 48, **u8), s=s,
                         qT=torch.empty(48, 0, **u8), sT=torch.empty(0, 48, device=DEV))
     torch.cuda.synchronize()
+
+
+def test_router_gradient_of_two_shares():
+    """Two shares of a layer, the losses' gradient taken in one of them: their
+    dlogits add up to the whole layer's, each off by its roundings."""
+    E, k, T, H, I = 8, 2, 120, 128, 128
+    x, dout, w1, w2, logits = _inputs(E, H, 2 * I, I, T, 4)
+    whole = mg.ExpertBlock(E, H, I, T, k, prec=mg.PREC_FP8)
+    whole.load_weights(w1, w2)
+    whole.route_logits(logits)
+    idx, probs = whole.expert_idx, whole.probs
+
+    def step(b, dloss=None):
+        b.forward(x, idx, probs)
+        b.backward(dout)
+        b.router_loss(logits, expert_idx=idx, balance_coef=0.5, z_coef=0.1)
+        return b.router_backward(dloss).double().cpu().numpy()
+
+    want = step(whole)
+    parts = []
+    for first, dloss in ((0, None), (4, torch.zeros(2, device=DEV))):
+        b = mg.ExpertBlock(4, H, I, T, k, first_expert=first, prec=mg.PREC_FP8)
+        b.load_weights(w1[first:first + 4].contiguous(), w2[first:first + 4].contiguous())
+        parts.append(step(b, dloss))
+    _, scale = st.router_bwd(logits.cpu().numpy(), idx.cpu().numpy(), whole.dprobs.double().cpu().numpy(), None,
+                             whole.router_counts.cpu().numpy(), T, None, 0.5, 0.1)
+    # 400 half steps of the terms' magnitudes for each of the three
+    assert (np.abs(parts[0] + parts[1] - want) <= 3 * 400 * 2.0 ** -24 * scale).all()
