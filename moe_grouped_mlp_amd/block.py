@@ -76,6 +76,26 @@ import torch
 from . import binding as B
 
 
+def _capturing(t: torch.Tensor) -> bool:
+    """Whether the current stream of t's device is being captured."""
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _stream_of(t: torch.Tensor) -> int:
+    """The current stream of t's device."""
+    return _raw_stream(t.get_device()) if t.is_cuda else 0
+
+
+def _record(t: torch.Tensor) -> None:
+    """t's memory, once it is given up, waits for the current stream."""
+    if t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+
+
 class ExpertBlock:
     def __init__(self, E: int, H: int, I: int, T: int, k: int, *,
                  act: Optional[B.ActParams] = None, first_expert: int = 0,
@@ -104,7 +124,9 @@ class ExpertBlock:
         # passes with every operand quantized by moe_quantize_mxfp4
         self.mx4 = prec == B.PREC_MXFP4
         self.fp8 = prec == B.PREC_FP8
-        self._router_bufs, self._ws_grad, self.grad_norm = {}, {}, None
+        # router_loss()'s buffers and the streams they were used on, by shape
+        self._router_bufs, self._router_captured = {}, set()
+        self._ws_grad, self.grad_norm = {}, None
         self._dprobs_valid = False   # whether dprobs are of the rows last routed
         if self.fp8 and (recompute or unfused):
             raise ValueError("the FP8 layer has no recompute path, and always runs as separate passes")
@@ -652,12 +674,13 @@ class ExpertBlock:
         idx = self.expert_idx if expert_idx is None else expert_idx
         if tuple(idx.shape) != (T, self.k):
             raise ValueError(f"expert_idx must be [{T}][{self.k}], one row for each of the logits'")
-        # buffers of every shape stay as long as the block: a graph captured with
-        # one shape still writes them after a call with another
-        bufs = self._router_bufs.get((T, E_all))
-        if bufs is None:
+        if (T, E_all) not in self._router_bufs:
+            # one shape's buffers are kept, and those that a capture used: a graph
+            # captured with one shape still writes them after a call with another
+            for shape in [s for s in self._router_bufs if s not in self._router_captured]:
+                del self._router_bufs[shape]
             dev = logits.device
-            bufs = self._router_bufs[T, E_all] = dict(
+            bufs = dict(
                 router_counts=torch.empty(E_all, dtype=torch.int32, device=dev),
                 router_tokens=torch.empty(1, dtype=torch.int32, device=dev),
                 router_prob_mean=torch.empty(E_all, dtype=torch.float32, device=dev),
@@ -665,13 +688,26 @@ class ExpertBlock:
                 dlogits=torch.empty(T, E_all, dtype=torch.float32, device=dev),
                 ws_loss=torch.empty(B.moe_router_loss_workspace_size(T, E_all),
                                     dtype=torch.uint8, device=dev))
-        self.__dict__.update(bufs)
+            self._router_bufs[T, E_all] = bufs, {_stream_of(logits)}
+        self.__dict__.update(self._router_bufs[T, E_all][0])
+        self._use_router_bufs(T, E_all)
         self._router_args = dict(T=T, E=E_all, k=self.k, logits=logits, expert_idx=idx,
                                  token_mask=token_mask, balance_coef=balance_coef, z_coef=z_coef,
                                  counts=self.router_counts, n_tokens=self.router_tokens)
         B.moe_router_loss(**self._router_args, prob_mean=self.router_prob_mean,
                           loss=self.router_losses, workspace=self.ws_loss)
         return self.router_losses
+
+    def _use_router_bufs(self, T: int, E_all: int) -> None:
+        """Before a call that uses the shape's buffers: notes a capture, and
+        streams other than the one that the buffers were made under."""
+        bufs, streams = self._router_bufs[T, E_all]
+        if _capturing(bufs["dlogits"]):
+            self._router_captured.add((T, E_all))
+        elif _stream_of(bufs["dlogits"]) not in streams:
+            streams.add(_stream_of(bufs["dlogits"]))
+            for t in bufs.values():
+                _record(t)
 
     def router_backward(self, dloss: Optional[torch.Tensor] = None,
                         dprobs: Optional[torch.Tensor] = None):
@@ -688,6 +724,7 @@ class ExpertBlock:
         dprobs = self.dprobs if dprobs is None else dprobs
         if tuple(dprobs.shape) != (self._router_args["T"], self.k):
             raise ValueError(f"dprobs must be [{self._router_args['T']}][{self.k}]")
+        self._use_router_bufs(self._router_args["T"], self._router_args["E"])
         B.moe_router_bwd(**self._router_args, dloss=dloss,
                          dprobs=dprobs, dlogits=self.dlogits)
         return self.dlogits

@@ -86,3 +86,39 @@ def test_router_gradient_of_two_shares():
                              whole.router_counts.cpu().numpy(), T, None, 0.5, 0.1)
     # 400 half steps of the terms' magnitudes for each of the three
     assert (np.abs(parts[0] + parts[1] - want) <= 3 * 400 * 2.0 ** -24 * scale).all()
+
+
+def test_router_losses_of_many_shapes_and_streams():
+    """Steps of other token counts, now and then on another stream, around a
+    graph captured with one: all give the results of a block of their own, and
+    the memory of earlier shapes is given back."""
+    E, k, T, H, I = 64, 2, 16, 128, 128
+    blk = mg.ExpertBlock(E, H, I, T, k, prec=mg.PREC_FP8)
+    logits = torch.randn(4096, E, device=DEV, generator=torch.Generator(DEV).manual_seed(3))
+    idx = logits.topk(k, dim=1).indices.to(torch.int32)
+    zeros = torch.zeros(4096, k, device=DEV)
+
+    def step(b, n):
+        losses = b.router_loss(logits[:n], expert_idx=idx[:n], balance_coef=0.5, z_coef=0.1)
+        return losses, b.router_backward(dprobs=zeros[:n])
+
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        held = step(blk, 1000)
+    base = torch.cuda.memory_allocated()
+    for i in range(60):
+        n = 4096 - 50 * i
+        with torch.cuda.stream(side if i % 3 == 1 else torch.cuda.current_stream()):
+            got = [t.clone() for t in step(blk, n)]
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for m, have in ((n, got), (1000, held)):
+            want = step(mg.ExpertBlock(E, H, I, T, k, prec=mg.PREC_FP8), m)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(have, want)), (i, m)
+        del got, have, want
+        # one shape's gradient (1 MB at most) and workspace (at most 256 of 12 (E + 1) bytes)
+        assert torch.cuda.memory_allocated() - base < 4 * 4096 * E + 256 * 12 * (E + 1) + (1 << 16), i
