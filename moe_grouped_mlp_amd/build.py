@@ -4,8 +4,9 @@
 
 Every HIP source is compiled for gfx950 only, with packed-fp32 instruction
 selection switched off, then linked into one shared library next to this
-file, and with it _call.so, the compiled part of the Python binding.  Objects
-go to moe_grouped_mlp_amd/_build/.
+file, and with it, where torch is installed, _call.so, the compiled part of the
+Python binding.  Objects go to moe_grouped_mlp_amd/_build/.  The library itself
+needs no torch: `python moe_grouped_mlp_amd/build.py` builds it without.
 """
 
 from __future__ import annotations
@@ -54,10 +55,15 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _compile_call() -> str:
-    """csrc/py_call.cpp, host code on CPython's and torch's headers."""
+def _compile_call() -> str | None:
+    """csrc/py_call.cpp, host code on CPython's and torch's headers; None
+    where torch is not installed."""
     import sysconfig
 
+    try:
+        import torch  # noqa: F401
+    except ModuleNotFoundError:
+        return None
     from torch.utils import cpp_extension
     obj = os.path.join(BUILD, "py_call.o")
     cmd = [HIPCC, "-x", "c++", "-O2", "-fPIC", "-std=c++17", "-Wall", "-fvisibility=hidden",
@@ -97,9 +103,13 @@ def build(verbose: bool = True) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_call(call.result())
+    obj = call.result()
+    if obj is not None:
+        _link_call(obj)
+    elif os.path.exists(CALL):
+        os.remove(CALL)   # of an older library
     if verbose:
-        print(f"built {LIB}\nbuilt {CALL}")
+        print(f"built {LIB}\n" + (f"built {CALL}" if obj else "no _call.so: torch, which the Python binding needs, is not installed"))
     return LIB
 
 
