@@ -5,9 +5,11 @@ import pytest
 import torch
 
 import moe_grouped_mlp_amd as mg
+from oracle import numerics as nu
 from oracle import step as st
 
-from .test_gpu_fp8 import DEV, _margin, _operands, _product, _starts, _wgrad, _wgrad_operands, _wgrad_ref
+from .test_gpu_fp8 import (DEV, _check, _margin, _operands, _product, _reference, _starts, _wgrad, _wgrad_operands,
+                           _wgrad_ref)
 from .test_gpu_fp8_block import _inputs
 
 pytestmark = pytest.mark.gpu
@@ -122,3 +124,82 @@ def test_router_losses_of_many_shapes_and_streams():
         del got, have, want
         # one shape's gradient (1 MB at most) and workspace (at most 256 of 12 (E + 1) bytes)
         assert torch.cuda.memory_allocated() - base < 4 * 4096 * E + 256 * 12 * (E + 1) + (1 << 16), i
+
+
+# ----------------------------------------- K cut with tiles of every width ---
+@pytest.mark.parametrize("leave", [48, 80])
+@pytest.mark.parametrize("c_type,fast", [(mg.TYPE_F32, False), (mg.TYPE_BF16, False), (mg.TYPE_BF16, True)])
+@pytest.mark.parametrize("sizes", [[40, 0, 1], [100, 256, 65], [170, 0, 300], [250, 129, 0]])
+def test_product_cut_along_k_every_tile_width(sizes, c_type, fast, leave):
+    """A row buffer far larger than the routed rows and few CUs: the tiles are
+    wide (two groups of 64 tokens, with fp8_sums and 48 CUs four), few, and K is
+    cut; a group's last tile holds one to four groups.  Exact on integers; on
+    random data the order of the parts shows."""
+    N, K, M_cap = 272, 4112, 4096
+    rng = np.random.default_rng(leave + len(sizes))
+    starts = _starts(sizes)
+    kw = dict(cu_margin=_margin(leave), fp8_sums=fast)
+    assert mg.moe_grouped_gemm_fp8_workspace_size(len(sizes), N, K, M_cap, 0) > 0
+
+    def padded(ops):
+        a_q, a_s = np.full((M_cap, K), 0x7F, np.uint8), np.full((ops[1].shape[0], M_cap), np.nan, np.float32)
+        a_q[:starts[-1]], a_s[:, :starts[-1]] = ops[0], ops[1]
+        return a_q, a_s, *ops[2:]
+
+    ops = _operands(rng, sizes, starts, starts[-1], N, K, exact=True)
+    # one scale for all, and so few bits that every sum is exact
+    ops = (nu.e4m3_encode(np.clip(np.nan_to_num(nu.e4m3_decode(ops[0])), -3, 3)), np.ones_like(ops[1]),
+           nu.e4m3_encode(np.clip(nu.e4m3_decode(ops[2]), -3, 3)), np.ones_like(ops[3]))
+    ref, _ = _reference(*ops, sizes, starts)
+    routed = ~np.isnan(ref)
+    want = ref[routed] if c_type == mg.TYPE_F32 else nu.round_bf16(ref[routed])
+    ops = padded(ops)
+    for workspace in (True, False):
+        c = _product(*ops, sizes, starts, c_type, workspace=workspace, **kw)
+        got = c[:starts[-1]].double().cpu().numpy()
+        np.testing.assert_array_equal(got[routed], want)
+        assert (got[~routed] == -77.0).all() and bool((c[starts[-1]:] == -77.0).all())
+    ops = _operands(rng, sizes, starts, starts[-1], N, K)
+    ref, mag = _reference(*ops, sizes, starts)
+    ops = padded(ops)
+    c = _product(*ops, sizes, starts, c_type, **kw)
+    _check(c[:starts[-1]], ref, mag, K, c_type == mg.TYPE_BF16)
+    assert torch.equal(c, _product(*ops, sizes, starts, c_type, **kw))
+    # the order moves an fp32 sum by some 2^-23, and one bf16 output of 10^4 past the
+    # border of two: of 41 x 272 that may be none, of 394 x 272 and more it is ten
+    if c_type == mg.TYPE_F32 or sum(sizes) > 300:
+        assert not torch.equal(c, _product(*ops, sizes, starts, c_type, workspace=False, **kw))
+
+
+def test_pad_rows_of_the_layer_encode_zeros():
+    """The weight gradient reads the pad rows of a group's last block: the
+    codes that the layer stores there are zeros, also after a step that filled
+    them, and the gradient is that of the routed rows alone."""
+    E, k, T, H, I = 6, 2, 150, 128, 192
+    blk = mg.ExpertBlock(E, H, I, T, k, prec=mg.PREC_FP8, wgrad=True, wgrad_type=mg.TYPE_F32)
+    x, dout, w1, w2, _ = _inputs(E, H, 2 * I, I, T, 3)
+    blk.load_weights(w1, w2)
+    probs = torch.full((T, k), 0.5, device=DEV)
+    for seed in range(3):
+        idx = torch.rand(T, E, device=DEV, generator=torch.Generator(DEV).manual_seed(seed)).topk(k, dim=1).indices.to(torch.int32)
+        if seed == 2:
+            idx[:] = torch.tensor([1, 4], dtype=torch.int32)
+        blk.forward(x, idx, probs)
+        blk.backward(dout)
+        blk.weight_grads()
+        torch.cuda.synchronize()
+        sizes, starts = blk.split_sizes.tolist(), blk.padded_offsets.tolist()
+        pads = np.ones(starts[-1], bool)
+        for n, o in zip(sizes, starts):
+            pads[o:o + n] = False
+        assert pads.any()
+        for left, right, dw in (("dz", "xp", blk.dw1), ("dyp", "a", blk.dw2)):
+            ops = []
+            for n in (left, right):
+                q = getattr(blk, n + "T_q8").cpu().numpy()[:, :starts[-1]]
+                assert (q[:, pads] & 0x7F == 0).all(), n
+                v = st.dequantize_rows(q, getattr(blk, n + "T_s8").cpu().numpy()[:starts[-1] // 128])
+                ops.append(np.where(pads[None, :], 0.0, v))
+            ref, mag = st.grouped_weight_grad(*ops, sizes, starts)
+            tol = 2 * (128 + starts[-1] // 128 + 4) * 2.0 ** -23 * mag
+            assert (np.abs(dw.double().cpu().numpy() - ref) <= tol).all()
