@@ -299,13 +299,16 @@ def gemm_bench(args):
                                  "rate": round(M_cap * K * (3 + 1 / 32) / (qms * 1e-3) / 1e9, 1)}
     ws8 = mg.moe_grouped_gemm_fp8_workspace_size(E, N, K, M_cap)
     ws8 = torch.empty(ws8, **u8) if ws8 else None
-    ms = timed(lambda: mg.moe_grouped_gemm_fp8(E=E, N=N, K=K, M_cap=M_cap, split_sizes=split,
-                                               padded_offsets=padded, a=a_q, a_s=a_s, b=b_q,
-                                               b_s=b_s, c=out, workspace=ws8), args.steps)
-    tf = flops / (ms * 1e-3) / 1e12
-    kernels["gemm_fp8"] = {"ms": round(ms, 4), "unit": "TFLOP/s", "rate": round(tf, 2),
-                           "pct_peak": round(100 * tf / PEAK_TFLOPS["mxfp8"], 2)}
-    log(f"  {ms:.3f} ms, {tf:.1f} TFLOP/s ({100 * tf / PEAK_TFLOPS['mxfp8']:.1f}% of peak)")
+    # summed in fp32 by the bf16 matrix instructions, and by the FP8 ones
+    for name, fp8_sums, prec in (("gemm_fp8", False, "bf16"), ("gemm_fp8_fp8_sums", True, "mxfp8")):
+        ms = timed(lambda: mg.moe_grouped_gemm_fp8(E=E, N=N, K=K, M_cap=M_cap, split_sizes=split,
+                                                   padded_offsets=padded, a=a_q, a_s=a_s, b=b_q,
+                                                   b_s=b_s, c=out, workspace=ws8, fp8_sums=fp8_sums),
+                   args.steps)
+        tf = flops / (ms * 1e-3) / 1e12
+        kernels[name] = {"ms": round(ms, 4), "unit": "TFLOP/s", "rate": round(tf, 2),
+                         "pct_peak": round(100 * tf / PEAK_TFLOPS[prec], 2)}
+        log(f"  {name}: {ms:.3f} ms, {tf:.1f} TFLOP/s ({100 * tf / PEAK_TFLOPS[prec]:.1f}% of peak)")
     del a_q, a_s, b_q, b_s, ws8
     # overlap with another kernel (the pages' reason for dynamic scheduling):
     # a kernel holds 64 of the CUs for the first 1 ms of the bf16 GEMM; with
