@@ -37,10 +37,11 @@ int tile_grid(int cu, int margin, int64_t tiles) {
 }
 
 // 64-token groups of a tile: as many as there may be, but half where that still
-// leaves a CU for every tile, as the wider tile takes twice as long (E=2 T=372
-// N=1824 K=1088: 18.4 us with 256 tokens, 10.4 with 64; where tiles are more than
-// CUs, narrow ones read the weights more often: E=22 N=7632 K=1296, 196 rows,
-// 45.7 us with 128, 55.6 with 64).  `tiles`: how many tiles of 64 g tokens.
+// leaves a CU for every tile, as the wider tile takes longer (2 groups of 372 rows,
+// N=1824 K=1088: 23 us with 128 tokens, 19 with 64, by fp8_sums 20 with 256 and 13
+// with 64; where tiles are more than CUs, narrow ones read the weights more often:
+// 22 groups of 196 rows, N=7632 K=1296, 165 us with 128, 210 with 64, by fp8_sums
+// 90 with 256, 162 with 64).  `tiles`: how many tiles of 64 g tokens.
 template <typename F>
 int tile_groups(bool wide, int cu, F&& tiles) {
   int g = moe::fp8_most_groups(wide);
@@ -55,7 +56,10 @@ int streams(int64_t rows, int64_t row) { return rows * row > moe::kStreamBytes &
 // Whether the product may cut K: rows that take the tiled kernel, 24 scale
 // blocks at least, and a row buffer (less a group's padding each) that cannot
 // fill the device with tiles.  The second launch costs 7 us also where nothing
-// was cut (E=22 N=352 K=2080, 34 tiles of few rows: 14 us without it, 21 with).
+// was cut (E=22 N=352 K=2080, 34 tiles of few rows, by fp8_sums: 14 us without it,
+// 21 with).  Groups packed without padding hold more rows than the estimate, and
+// may pay for that launch in vain: 64 of 128 rows, N=4096 K=4096, by fp8_sums 272
+// us against 268.
 int64_t rows_estimate(int E, int64_t M_cap) {
   return std::max<int64_t>(1, M_cap - static_cast<int64_t>(E) * (MOE_GROUP_ALIGN - 1));
 }

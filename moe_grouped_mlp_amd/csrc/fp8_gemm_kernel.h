@@ -47,17 +47,18 @@
 //
 // Bound by the vector instructions beside the MFMAs: a SIMD issues two beside a
 // 16-cycle MFMA for nothing, each further one costs 4 cycles (measured with two
-// waves).  The product has 3.5 (2.5 to widen, 1 to scale): eight experts, 16384
-// rows x 4096 x 14336, 1617 us, 1.19 PFLOP/s; 89 experts of 736 rows on average x
-// 5760 x 2880, 2241 us, 970 TFLOP/s.  The weight gradient has 4.7 (2 to scale),
-// and its MFMAs are busy for a quarter to a third of the time: 32 experts of 7168
-// x 2048 from 16384 rows (4.5 steps a tile), fp32, 855 us, of which 690 without
-// the stores, 300 the stores (1.88 GB) alone.
-// With fp8_sums the first product takes 780 us on a cool device (2.47 PFLOP/s; a
-// product with one scale for all, from a library: 2.71) and about 920 in a long
-// run, where power bounds it: the clock falls to 1.5 .. 1.7 GHz while the MFMAs
-// run, and a loop of nothing but these MFMAs and their scaled sums makes 3.47
-// PFLOP/s.  The second takes 1200 and 1450.
+// waves).  The product has 3.5 (2.5 to widen, 1 to scale) and its MFMAs are busy
+// for half of the time: eight experts, 16384 rows x 4096 x 14336, 1690 us, 1.14
+// PFLOP/s; 89 experts of 736 rows on average x 5760 x 2880, 2350 us, 920 TFLOP/s.
+// The weight gradient has 4.7 (2 to scale), and its MFMAs are busy for a quarter
+// to a third of the time: 32 experts of 7168 x 2048 from 16384 rows (4.5 steps a
+// tile), fp32, 845 us, of which 690 without the stores, 300 the stores (1.88 GB)
+// alone.
+// With fp8_sums the first product takes 795 us (2.42 PFLOP/s; a product with one
+// scale for all, from a library: 2.71) and the second 1210, bound by power: the
+// clock falls to 1.5 .. 1.7 GHz while the MFMAs run, and a loop of nothing but
+// these MFMAs and their scaled sums makes 3.47 PFLOP/s.  (All of a running
+// program, over 1000 calls; the first ten after an idle while take a fifth longer.)
 #include <type_traits>
 #include <utility>
 
@@ -302,8 +303,10 @@ MOE_DEV int fp8_tile_groups(int rows) {
 // cost 0.09 us of the device's time to write and read again, and the second
 // launch about 9 us.  So the best number is near sqrt(16 steps / tiles) (of
 // four steps each at least, and as many workgroups as there are), and it has
-// to save more steps than it costs.  E=2 N=112 K=4736: 50 us uncut, 28 cut
-// into 9; E=4 N=656 K=1168 (31 tiles, 10 steps): 23 us uncut, 41 cut into 2.
+// to save more steps than it costs.  2 groups of 100 rows, N=112 K=4736: 49 us
+// uncut, 22 cut into 9 (fp8_sums, half the time a step: 24 and 19); 2 of 200, N=512
+// K=8192: 80 and 30 (40 and 24); E=4 N=656 K=1168 (31 tiles, 10 steps): 23 us
+// uncut, 41 cut into 2.
 MOE_DEV int fp8_parts(const Fp8Args& g, int total, int workgroups) {
   if (!g.part || total < 1) return 1;
   const int steps = (g.K + kFp8Blk - 1) / kFp8Blk;
@@ -571,7 +574,7 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
       // one chunk) and reads (one row) fall on different banks.  Large outputs
       // (g.stream) pass the caches by, which then hold more of the operands: fp32
       // weight gradients of 1.88 GB 870 -> 856 us, 89 experts' outputs of 755 MB
-      // 1217 -> 1200.  Rows that are no whole 128-byte lines or outputs that fit in
+      // (fp8_sums) 1217 -> 1200.  Rows that are no whole 128-byte lines or outputs that fit in
       // the last-level cache were slower so (59 MB in rows of 2592 bytes: 28.5 ->
       // 31.3 us).
       constexpr int kOut = F32 ? 4 : 2, kRow = 128 * kOut, kChunks = kRow / 16;

@@ -10,9 +10,9 @@
 // be captured in a graph.  Every tensor is cut into chunks of kChunk elements
 // from its first 16-byte boundary on; a workgroup takes chunks with a fixed
 // stride, and its fp64 sum goes to its own slot, so the order of the sum
-// depends on the list alone.  Two bf16 gradients, 2.8 GB: 466 us for the norm
-// (6.0 TB/s), 1020 for the clipping (5.5 TB/s of reads and writes); sixty small
-// ones: 5.3, 1.5 and 6.2 us in three launches.
+// depends on the list alone.  Two bf16 gradients, 2.8 GB: 456 us for the norm
+// (6.2 TB/s), 1021 for the clipping (5.5 TB/s of reads and writes); sixty small
+// ones: 5.2, 1.6 and 6.2 us in three launches.
 #include "common.h"
 #include "kernels.h"
 

@@ -18,9 +18,10 @@
 // sums over its experts fp32).
 //
 // Bound by latencies: a workgroup makes one or a few passes, so all it reads
-// goes out at once, before the first use.  16384 tokens of 256 experts: 8.2 us
-// for the partials (16.8 MB read), 4.7 for their sums, 11.7 for the gradient
-// (33.6 MB, 2.9 TB/s); 256 tokens of 4: 3.4 and 2.8 in one launch each.
+// goes out at once, before the first use.  16384 tokens of 256 experts: 10.8 us
+// for the partials (16.8 MB read; with fp32 sums and exponentials within two steps
+// 8.8), 4.8 for their sums, 13.3 for the gradient (33.6 MB, 2.5 TB/s); 256 tokens
+// of 4: 3.6 and 2.8 in one launch each.
 #include <type_traits>
 
 #include "common.h"
@@ -108,8 +109,8 @@ MOE_DEV bool token_softmax(float (&p)[P], float& lse) {
 constexpr int kMaxLossBlocks = 256;   // workgroups of the loss kernel at most
 constexpr int kLossThreads = 1024;
 // threads of a single workgroup that covers all tokens in one pass: starting
-// and joining 16 waves costs more than 4 (256 tokens of
-// 4 experts: 4.8 us with 16, 3.4 with 4)
+// and joining 16 waves costs more than 4 (256 tokens of 4 experts, sums in fp32:
+// 4.8 us with 16, 3.4 with 4)
 constexpr int kFewThreads = 256;
 
 // Sum over the workgroup's THREADS, in every thread.

@@ -166,7 +166,7 @@ def test_product_cut_along_k_every_tile_width(sizes, c_type, fast, leave):
     _check(c[:starts[-1]], ref, mag, K, c_type == mg.TYPE_BF16)
     assert torch.equal(c, _product(*ops, sizes, starts, c_type, **kw))
     # the order moves an fp32 sum by some 2^-23, and one bf16 output of 10^4 past the
-    # border of two: of 41 x 272 that may be none, of 394 x 272 and more it is ten
+    # border of two: of 41 x 272 that may be none, of 379 x 272 and more it is ten
     if c_type == mg.TYPE_F32 or sum(sizes) > 300:
         assert not torch.equal(c, _product(*ops, sizes, starts, c_type, workspace=False, **kw))
 
