@@ -152,3 +152,49 @@ def test_layer_passes_fp8_sums_on(wtype):
         assert torch.equal(c, dw1)
         outs.append(blk.out.clone())
     assert not torch.equal(*outs) and rows
+
+
+# --------------------------------------------------- NaN and infinite blocks ---
+VARIANTS = [dict(c_type=mg.TYPE_F32), dict(c_type=mg.TYPE_BF16), dict(c_type=mg.TYPE_BF16, fp8_sums=True)]
+
+
+@pytest.mark.parametrize("kw", VARIANTS)
+@pytest.mark.parametrize("hint", [16, 32, 0])
+@pytest.mark.parametrize("code", [0x7F, 0xFF])
+def test_product_nan_and_infinite_blocks(code, hint, kw):
+    """A NaN code makes its token's row NaN, or its weight row's column of the
+    expert; a block whose scale is infinite (codes zero but for a NaN, as the
+    quantizer writes it) makes the row NaN; all else is as without them."""
+    sizes, N, K = [3, 0, 40, 17], 144, 400
+    starts = _starts(sizes)
+    a_q, a_s, b_q, b_s = _operands(np.random.default_rng(7), sizes, starts, starts[-1], N, K, exact=True)
+    clean = _product(a_q, a_s, b_q, b_s, sizes, starts, max_rows=hint, **kw).double().cpu().numpy()
+    r0, r1 = starts[2] + 5, starts[3] + 16
+    a_q[r0, 399] = code
+    a_q[r1, 128:256] = 0
+    a_q[r1, 200] = code
+    a_s[1, r1] = np.inf
+    b_q[2, 77, 130] = code
+    c = _product(a_q, a_s, b_q, b_s, sizes, starts, max_rows=hint, **kw).double().cpu().numpy()
+    bad = np.zeros(c.shape, bool)
+    bad[[r0, r1]] = True
+    bad[starts[2]:starts[2] + sizes[2], 77] = True
+    np.testing.assert_array_equal(np.isnan(c), bad)
+    np.testing.assert_array_equal(c[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("kw", VARIANTS)
+def test_wgrad_nan_and_infinite_blocks(kw):
+    sizes, P, Q = [130, 0, 3], 80, 272
+    starts = _starts(sizes)
+    a_q, a_s, b_q, b_s = _wgrad_operands(np.random.default_rng(8), sizes, starts, starts[-1], P, Q, exact=True)
+    clean = _wgrad(a_q, a_s, b_q, b_s, sizes, starts, **kw).double().cpu().numpy()
+    a_q[5, 129] = 0x7F                       # expert 0, second block
+    b_q[260, starts[2]:starts[2] + 3] = [0, 0xFF, 0]   # expert 2
+    b_s[starts[2] // 128, 260] = np.inf
+    c = _wgrad(a_q, a_s, b_q, b_s, sizes, starts, **kw).double().cpu().numpy()
+    bad = np.zeros(c.shape, bool)
+    bad[0, 5] = True
+    bad[2, :, 260] = True
+    np.testing.assert_array_equal(np.isnan(c), bad)
+    np.testing.assert_array_equal(c[~bad], clean[~bad])
