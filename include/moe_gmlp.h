@@ -65,9 +65,9 @@ typedef enum moe_status {
                                          running past the next group's start
                                          or past M_cap (its rows there are
                                          not computed)                       */
-#define MOE_DEVERR_NONFINITE 0x10     /* moe_grad_clip: the norm is infinite
-                                         or NaN; the gradients were copied
-                                         unscaled                            */
+#define MOE_DEVERR_NONFINITE 0x10     /* the norm is infinite or NaN:
+                                         moe_grad_clip copied the gradients
+                                         unscaled, moe_adamw made no step    */
 
 /* Group-start alignment of the padded row layout (rows).  Every group of
  * the permuted layout starts at a multiple of it, so MXFP8 blocks of 32
@@ -988,6 +988,237 @@ typedef struct moe_grad_args {
 size_t moe_grad_workspace_size(int n_tensors);
 moe_status moe_grad_sumsq(const moe_grad_args* args, void* stream);
 moe_status moe_grad_clip(const moe_grad_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_router_gate -- the choice of experts by scores: what moe_router_topk
+ *   does for one kind of router, for those whose scores are sigmoids, whose
+ *   choice has a balance bias or is limited to groups of experts, or whose
+ *   weights are renormalised.  For every token t, over its E logits x:
+ *     score[e]  = softmax(x)[e] or 1 / (1 + exp(-x[e]))
+ *     choice[e] = score[e] + bias[e]; without a bias x[e], which has the
+ *                 same order
+ *     n_groups > 1: the experts are n_groups equal runs of ids; a group is
+ *                 judged by its largest choice (group_top 1) or by the sum
+ *                 of its two largest score + bias (group_top 2; of one if it
+ *                 has no second), and the experts of all but the topk_groups
+ *                 best groups are left out
+ *     expert_idx[t][0..k-1] = the experts of the k largest choices left, in
+ *                 descending order
+ *     probs[t][j] = scale * score of pick j, or with renorm scale * score /
+ *                 (sum of the picks' scores)
+ *   Choices and groups are compared as 64-bit arithmetic gives them (without
+ *   a bias the logits as they are); equal ones go to the lower id.
+ *   An expert whose logit is -infinity or NaN is ruled out: it has score 0
+ *   and is never picked.  (A bias of -infinity or NaN rules its expert out of
+ *   the choice alone.)  Where fewer than k experts are left, the other slots
+ *   hold id -1 and weight 0, as do all of a token that token_mask leaves out
+ *   (byte 0): moe_permute takes them as picks of no local expert,
+ *   moe_router_loss does not count them.  Logits of +infinity share the
+ *   softmax among themselves.
+ *   logits fp32 or bf16 (logits_type) [T][ld], ld elements between rows (0:
+ *   E).  counts (optional [E]): every pick adds one to its expert's; the
+ *   caller clears them (several calls may add up to one
+ *   moe_router_bias_update).
+ *   Needs 0 <= T, 1 <= E <= 1024, 1 <= k <= min(8, experts of topk_groups
+ *   groups), T * k < 2^31, n_groups 0 (none) to 64 and a divisor of E, 1 <=
+ *   topk_groups <= n_groups, group_top 1 or 2; scale finite.
+ * ---------------------------------------------------------------------- */
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+typedef struct moe_gate_args {
+  int32_t T, E, k;
+  int32_t score;               /* moe_score */
+  int32_t n_groups, topk_groups, group_top;   /* read if n_groups > 1 */
+  int32_t renorm;
+  float scale;
+  int32_t logits_type;         /* moe_type */
+  int64_t ld;
+  const void* logits;          /* device */
+  const float* bias;           /* optional [E] device */
+  const uint8_t* token_mask;   /* optional [T] device */
+  int32_t* expert_idx;         /* [T][k] device, out */
+  float* probs;                /* [T][k] device, out */
+  int32_t* counts;             /* optional [E] device, added to */
+} moe_gate_args;
+
+moe_status moe_router_gate(const moe_gate_args* args, void* stream);
+
+/* moe_router_gate_bwd -- the gradient of the logits from that of the weights
+ *   (dprobs [T][k], moe_unpermute's), with expert_idx as moe_router_gate left
+ *   it (the choice itself has none).  g[j] = scale * dprobs[t][j], s the
+ *   scores, w[j] = s[j] / (sum of the picks' s):
+ *     softmax           dx[e] = s[e] * (g of pick e, if any - sum_j s[j] g[j])
+ *     softmax, renorm   dx of pick j = w[j] * (g[j] - sum_i w[i] g[i])
+ *     sigmoid           dx of pick j = s[j] * (1 - s[j]) * g[j]
+ *     sigmoid, renorm   dx of pick j = (1 - s[j]) * w[j] * (g[j] - sum_i w[i] g[i])
+ *   and zeros for the other logits.  Slots with an id outside [0, E) or of an
+ *   expert that is ruled out have no part, whatever their dprobs are; an id
+ *   listed twice adds twice.
+ *   dlogits has the logits' type [T][ld_d] (0: E); accumulate != 0: added to
+ *   what it holds (say moe_router_bwd's, of the losses), in fp32, one
+ *   rounding.  logits and dlogits may be the same buffer if ld == ld_d and
+ *   accumulate == 0. */
+typedef struct moe_gate_bwd_args {
+  int32_t T, E, k;
+  int32_t score;
+  int32_t renorm;
+  float scale;
+  int32_t logits_type;
+  int32_t accumulate;
+  int64_t ld, ld_d;
+  const void* logits;          /* device */
+  const int32_t* expert_idx;   /* [T][k] device */
+  const float* dprobs;         /* [T][k] device */
+  void* dlogits;               /* device, out */
+} moe_gate_bwd_args;
+
+moe_status moe_router_gate_bwd(const moe_gate_bwd_args* args, void* stream);
+
+/* moe_router_bias_update -- the balance bias after a step: every expert
+ *   that was picked less often than the mean of counts gets bias + rate, one
+ *   picked more often bias - rate.  reset != 0 clears counts afterwards.
+ *   Several processes: sum counts over them first.  1 <= E <= 1024; rate
+ *   finite. */
+typedef struct moe_bias_update_args {
+  int32_t E;
+  float rate;
+  int32_t reset;
+  int32_t* counts;             /* [E] device */
+  float* bias;                 /* [E] device, in and out */
+} moe_bias_update_args;
+
+moe_status moe_router_bias_update(const moe_bias_update_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * moe_adamw -- one AdamW step over a list of tensors.  For every element,
+ *   in fp32:
+ *     d = grad * f;  m = beta1 m + (1 - beta1) d;  v = beta2 v + (1 - beta2) d^2
+ *     w = w - lr * weight_decay * w
+ *           - lr * (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ *   f = 1, or with sumsq (moe_grad_sumsq's) the clipping factor of
+ *   moe_grad_clip, min(1, max_norm / (sqrt(*sumsq) + 1e-6)): gradients that
+ *   are clipped here need no pass of their own.  If sqrt(*sumsq) is infinite
+ *   or NaN nothing is changed and MOE_DEVERR_NONFINITE is set.
+ *   param bf16 or fp32; a bf16 one may have master, its fp32 copy: the step
+ *   is then made on master, and param is written from it (it is not read).
+ *   Without one a bf16 param is updated in fp32 and rounded.
+ *   States (state_type, of the whole list):
+ *     MOE_STATE_F32: m, v fp32 [numel].
+ *     MOE_STATE_FP8: m and the root of v as E4M3 codes u8 [numel], with one
+ *       fp32 scale for each MOE_FP8_BLOCK consecutive elements (m_scale,
+ *       v_scale: [ceil(numel / 128)]), encoded as moe_quantize_fp8's blocks
+ *       are; a v above zero never gets the code of zero.  With stochastic
+ *       != 0 the root is rounded up with the probability of what rounding
+ *       down would lose, by 16 bits of a hash of seed, step, the tensor's
+ *       place in the list and the element: rounding to nearest would not
+ *       see a v that changes by less than a sixteenth a step.  States of
+ *       zeros (codes and scales) are those to begin with.
+ *   step counts from 1; step_dev (optional device int32 [1]) and lr_dev
+ *   (optional device fp32 [1]) are read instead of step and lr, so that a
+ *   captured graph can go on counting: the caller adds one to *step_dev
+ *   before the call.
+ *   tensors: host array, read before the call returns; numel >= 0; each
+ *   tensor contiguous and aligned to its type (16-byte alignment of all of
+ *   a tensor's buffers makes wide loads possible).  A buffer that overlaps
+ *   another one of the list is refused with MOE_ERR_INVALID_ARG (gradients
+ *   may overlap each other).
+ *   0 <= beta < 1, eps >= 0, finite lr and weight_decay, max_norm >= 0.
+ * ---------------------------------------------------------------------- */
+typedef enum moe_state { MOE_STATE_F32 = 0, MOE_STATE_FP8 = 1 } moe_state;
+
+typedef struct moe_adamw_tensor {
+  void* param;                 /* device */
+  const void* grad;            /* device */
+  float* master;               /* optional, bf16 param only */
+  void* m;
+  void* v;
+  float* m_scale;              /* MOE_STATE_FP8 */
+  float* v_scale;
+  int64_t numel;
+  int32_t param_type, grad_type;   /* moe_type */
+  float weight_decay;
+} moe_adamw_tensor;
+
+typedef struct moe_adamw_args {
+  const moe_adamw_tensor* tensors;   /* host */
+  int32_t n_tensors;
+  int32_t state_type;          /* moe_state */
+  double lr, beta1, beta2, eps;   /* double: 1 - 0.999f is off by 5e-5 */
+  int32_t step;
+  float max_norm;
+  const double* sumsq;         /* optional device */
+  const int32_t* step_dev;     /* optional device */
+  const float* lr_dev;         /* optional device */
+  int32_t* err_flag;           /* optional device int32 */
+  int32_t stochastic;
+  uint32_t seed;
+} moe_adamw_args;
+
+moe_status moe_adamw(const moe_adamw_args* args, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit integers with one fp32 scale a row: a token's activations, an output
+ * channel's weights.  A code stands for code * scale.
+ *
+ * moe_quantize_int8 -- bf16 to int8 rows.
+ *   x bf16 [rows][x_stride] (0: cols; a multiple of 8), q int8 [rows][cols],
+ *   s fp32 [rows].  Of a row v, m = max(max|v|, 2^-100), each operation
+ *   rounded to nearest even in fp32:
+ *     s = m / 127,  code = round(v * (127 / m))
+ *   A row that holds an infinity or NaN has codes 0 and the scale NaN, so
+ *   that whatever is made of it is NaN too.
+ *   row_end (optional, device int32, say padded_offsets + E): rows at or past
+ *   *row_end are not read and not written.
+ *   Needs cols % 16 == 0 (the experts' stacked weights [E][N][K] are E * N
+ *   rows); x and q 16-byte aligned; rows 0 is a call with nothing to do,
+ *   whose pointers may be NULL. */
+typedef struct moe_quant_int8_args {
+  int32_t rows, cols;
+  int64_t x_stride;
+  const void* x;               /* bf16 device */
+  int8_t* q;
+  float* s;
+  const int32_t* row_end;      /* optional device int32 */
+} moe_quant_int8_args;
+
+moe_status moe_quantize_int8(const moe_quant_int8_args* args, void* stream);
+
+/* moe_grouped_gemm_int8 -- the grouped product of such rows:
+ *     C[r][n] = a_s[r] * b_s[e][n] * sum_k a[r][k] * b[e][n][k]
+ *   for every row r in [padded_offsets[e], padded_offsets[e] +
+ *   split_sizes[e]).  The sums are integers and exact; they are rounded to
+ *   fp32, scaled there and rounded once to the output type.
+ *   a [M_cap][K], a_s [M_cap]; per expert b [N][K] and b_s [N] (b_stride
+ *   bytes and b_s_stride floats apart, 0: N * K and N).  c, ldc, c_type,
+ *   max_rows, cu_margin, workspace, group starts and inconsistent offsets
+ *   as in moe_grouped_gemm_fp8; results do not depend on whether K is cut.
+ *   Needs N % 16 == 0, K % 16 == 0, E <= 1024, K <= 131056 (a sum of 131072
+ *   products of -128 * -128 does not fit 32 bits); a, b and c 16-byte
+ *   aligned (b_stride too). */
+typedef struct moe_gemm_int8_args {
+  int32_t E, N, K;
+  int64_t M_cap;
+  const int32_t* split_sizes;     /* [E]   device */
+  const int32_t* padded_offsets;  /* [E+1] device */
+  const int8_t* a;
+  const float* a_s;
+  const int8_t* b;
+  const float* b_s;
+  int64_t b_stride;
+  int64_t b_s_stride;
+  void* c;
+  int64_t ldc;
+  int32_t c_type;                 /* moe_type */
+  int32_t max_rows;
+  int32_t cu_margin;
+  int32_t* err_flag;              /* optional device int32 */
+  void* workspace;
+  size_t workspace_bytes;
+} moe_gemm_int8_args;
+
+size_t moe_grouped_gemm_int8_workspace_size(int E, int N, int K, int64_t M_cap,
+                                            int max_rows);
+moe_status moe_grouped_gemm_int8(const moe_gemm_int8_args* args, void* stream);
 
 /* Workspace bytes for these sizes: the backward needs at least the dprobs
  * partials (fp32 M_cap x ceil(I / 256)); the full size adds the area where

@@ -25,5 +25,8 @@ from .binding import (  # noqa: F401
     moe_quantize_fp8, moe_grouped_gemm_fp8, moe_grouped_gemm_fp8_workspace_size,
     moe_grouped_wgrad_fp8, moe_router_loss, moe_router_loss_workspace_size, moe_router_bwd,
     moe_grad_sumsq, moe_grad_clip, moe_grad_workspace_size,
+    PREC_INT8, SCORE_SOFTMAX, SCORE_SIGMOID, STATE_F32, STATE_FP8, moe_router_gate,
+    moe_router_gate_bwd, moe_router_bias_update, moe_adamw, moe_quantize_int8,
+    moe_grouped_gemm_int8, moe_grouped_gemm_int8_workspace_size,
 )
 from .block import ExpertBlock  # noqa: F401

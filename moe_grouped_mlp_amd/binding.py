@@ -9,7 +9,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-from ctypes import c_float, c_int, c_int32, c_int64, c_size_t, c_void_p
+from ctypes import c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(HERE, "libmoe_gmlp.so")
@@ -20,7 +20,10 @@ PREC_BF16, PREC_MXFP8, PREC_MXFP4 = 0, 1, 2
 PREC_FP8 = 3   # block-scaled FP8: a precision of ExpertBlock, not of moe_grouped_mlp_fwd / _bwd
 PERMUTE_BUILD_MAP, PERMUTE_GATHER, PERMUTE_WRITE_MX = 0x1, 0x2, 0x4
 PERMUTE_WRITE_MX4 = 0x8
+PREC_INT8 = 4  # 8-bit integers with a scale a row: a precision of ExpertBlock, for serving
 QUANT_ROW, QUANT_COL, QUANT_BOTH, QUANT_TILE = 0, 1, 2, 3
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+STATE_F32, STATE_FP8 = 0, 1
 TYPE_BF16, TYPE_F32 = 0, 1
 FP8_BLOCK = 128
 GROUP_ALIGN = 128
@@ -43,6 +46,8 @@ EXPORTED_SYMBOLS = (
     "moe_quantize_fp8", "moe_grouped_gemm_fp8", "moe_grouped_gemm_fp8_workspace_size",
     "moe_grouped_wgrad_fp8", "moe_router_loss", "moe_router_loss_workspace_size",
     "moe_router_bwd", "moe_grad_sumsq", "moe_grad_clip", "moe_grad_workspace_size",
+    "moe_router_gate", "moe_router_gate_bwd", "moe_router_bias_update", "moe_adamw",
+    "moe_quantize_int8", "moe_grouped_gemm_int8", "moe_grouped_gemm_int8_workspace_size",
 )
 
 
@@ -232,6 +237,60 @@ class GradArgs(ctypes.Structure):
                 ("workspace_bytes", c_size_t)]
 
 
+class GateArgs(ctypes.Structure):
+    _fields_ = [("T", c_int32), ("E", c_int32), ("k", c_int32), ("score", c_int32),
+                ("n_groups", c_int32), ("topk_groups", c_int32), ("group_top", c_int32),
+                ("renorm", c_int32), ("scale", c_float), ("logits_type", c_int32),
+                ("ld", c_int64), ("logits", c_void_p), ("bias", c_void_p),
+                ("token_mask", c_void_p), ("expert_idx", c_void_p), ("probs", c_void_p),
+                ("counts", c_void_p)]
+
+
+class GateBwdArgs(ctypes.Structure):
+    _fields_ = [("T", c_int32), ("E", c_int32), ("k", c_int32), ("score", c_int32),
+                ("renorm", c_int32), ("scale", c_float), ("logits_type", c_int32),
+                ("accumulate", c_int32), ("ld", c_int64), ("ld_d", c_int64),
+                ("logits", c_void_p), ("expert_idx", c_void_p), ("dprobs", c_void_p),
+                ("dlogits", c_void_p)]
+
+
+class BiasUpdateArgs(ctypes.Structure):
+    _fields_ = [("E", c_int32), ("rate", c_float), ("reset", c_int32), ("counts", c_void_p),
+                ("bias", c_void_p)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("param", c_void_p), ("grad", c_void_p), ("master", c_void_p), ("m", c_void_p),
+                ("v", c_void_p), ("m_scale", c_void_p), ("v_scale", c_void_p),
+                ("numel", c_int64), ("param_type", c_int32), ("grad_type", c_int32),
+                ("weight_decay", c_float)]
+
+
+class AdamwArgs(ctypes.Structure):
+    _fields_ = [("tensors", ctypes.POINTER(AdamwTensor)), ("n_tensors", c_int32),
+                ("state_type", c_int32), ("lr", c_double), ("beta1", c_double),
+                ("beta2", c_double), ("eps", c_double), ("step", c_int32),
+                ("max_norm", c_float), ("sumsq", c_void_p), ("step_dev", c_void_p),
+                ("lr_dev", c_void_p), ("err_flag", c_void_p), ("stochastic", c_int32),
+                ("seed", c_uint32)]
+
+
+class QuantInt8Args(ctypes.Structure):
+    _fields_ = [("rows", c_int32), ("cols", c_int32), ("x_stride", c_int64), ("x", c_void_p),
+                ("q", c_void_p), ("s", c_void_p), ("row_end", c_void_p)]
+
+
+class GemmInt8Args(ctypes.Structure):
+    _fields_ = [("E", c_int32), ("N", c_int32), ("K", c_int32),
+                ("M_cap", c_int64), ("split_sizes", c_void_p),
+                ("padded_offsets", c_void_p), ("a", c_void_p), ("a_s", c_void_p),
+                ("b", c_void_p), ("b_s", c_void_p), ("b_stride", c_int64),
+                ("b_s_stride", c_int64), ("c", c_void_p), ("ldc", c_int64),
+                ("c_type", c_int32), ("max_rows", c_int32), ("cu_margin", c_int32),
+                ("err_flag", c_void_p), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t)]
+
+
 # ---- library loading ------------------------------------------------------
 _LIB = None
 
@@ -271,6 +330,8 @@ def lib() -> ctypes.CDLL:
             c_int, c_int, c_int, c_int64, c_int, c_int]
         L.moe_grouped_gemm_fp8_workspace_size.restype = c_size_t
         L.moe_grouped_gemm_fp8_workspace_size.argtypes = [c_int, c_int, c_int, c_int64, c_int]
+        L.moe_grouped_gemm_int8_workspace_size.restype = c_size_t
+        L.moe_grouped_gemm_int8_workspace_size.argtypes = [c_int, c_int, c_int, c_int64, c_int]
         L.moe_router_loss_workspace_size.restype = c_size_t
         L.moe_router_loss_workspace_size.argtypes = [c_int, c_int]
         L.moe_grad_workspace_size.restype = c_size_t
@@ -293,7 +354,13 @@ def lib() -> ctypes.CDLL:
                          ("moe_router_loss", RouterLossArgs),
                          ("moe_router_bwd", RouterBwdArgs),
                          ("moe_grad_sumsq", GradArgs),
-                         ("moe_grad_clip", GradArgs)):
+                         ("moe_grad_clip", GradArgs),
+                         ("moe_router_gate", GateArgs),
+                         ("moe_router_gate_bwd", GateBwdArgs),
+                         ("moe_router_bias_update", BiasUpdateArgs),
+                         ("moe_adamw", AdamwArgs),
+                         ("moe_quantize_int8", QuantInt8Args),
+                         ("moe_grouped_gemm_int8", GemmInt8Args)):
             f = getattr(L, name)
             f.restype = c_int
             f.argtypes = [ctypes.POINTER(st), c_void_p]
@@ -540,7 +607,7 @@ def moe_glu_unfused(*, direction, E, I, M_cap, split_sizes, padded_offsets,
     _check("moe_glu_unfused", lib().moe_glu_unfused(ctypes.byref(args), _stream(stream)))
 
 
-# ---- block-scaled FP8, router losses, gradient norm -----------------------
+# ---- block-scaled FP8, 8-bit integers, router choice and losses, gradient norm, AdamW ----
 # A small call is as long as its marshalling, so these go through a compiled
 # module (csrc/py_call.cpp), which also checks what the C ABI cannot see: that
 # a tensor is contiguous device memory of the type and at least the size the
@@ -645,3 +712,63 @@ def moe_grad_clip(*, tensors, sumsq, max_norm, out=None, norm=None, err_flag=Non
     sqrt(sumsq) is at most max_norm."""
     d = _device()
     _call.grad_clip(d, tensors, out, max_norm, sumsq, norm, err_flag, stream)
+
+
+def moe_router_gate(*, T, E, k, logits, expert_idx, probs, score=SCORE_SOFTMAX, bias=None,
+                    n_groups=1, topk_groups=1, group_top=1, renorm=False, scale=1.0, ld=0,
+                    token_mask=None, counts=None, stream=None):
+    """Top-k by softmax or sigmoid scores of fp32 or bf16 logits, with a balance
+    bias, groups of experts and renormalised weights; counts (int32 [E]) are
+    added to."""
+    d = _device()
+    _call.router_gate(d, T, E, k, score, n_groups, topk_groups, group_top, renorm, scale, ld,
+                      logits, bias, token_mask, expert_idx, probs, counts, stream)
+
+
+def moe_router_gate_bwd(*, T, E, k, logits, expert_idx, dprobs, dlogits, score=SCORE_SOFTMAX,
+                        renorm=False, scale=1.0, accumulate=False, ld=0, ld_d=0, stream=None):
+    """Gradient of moe_router_gate's weights with respect to the logits; dlogits
+    has their type."""
+    d = _device()
+    _call.router_gate_bwd(d, T, E, k, score, renorm, scale, accumulate, ld, ld_d, logits,
+                          expert_idx, dprobs, dlogits, stream)
+
+
+def moe_router_bias_update(*, E, counts, bias, rate, reset=False, stream=None):
+    """bias += rate for experts picked less often than the mean, -= rate for those
+    picked more often; reset clears the counts."""
+    d = _device()
+    _call.router_bias_update(d, E, rate, reset, counts, bias, stream)
+
+
+def moe_adamw(*, params, grads, m, v, lr, step=1, beta1=0.9, beta2=0.999, eps=1e-8,
+              weight_decay=0.0, master=None, m_scale=None, v_scale=None, sumsq=None, max_norm=0.0,
+              stochastic=False, seed=0, step_dev=None, lr_dev=None, err_flag=None, stream=None):
+    """One AdamW step over lists of tensors.  m and v float32, or (with m_scale
+    and v_scale) 8-bit codes of m and of v's root; master: None, or a list of fp32
+    copies of bf16 parameters with None where there is none; weight_decay: one
+    number or a list; sumsq (moe_grad_sumsq's) clips the gradients to max_norm."""
+    d = _device()
+    _call.adamw(d, params, grads, m, v, master, m_scale, v_scale, weight_decay, lr, beta1, beta2,
+                eps, step, max_norm, stochastic, seed, sumsq, step_dev, lr_dev, err_flag, stream)
+
+
+def moe_quantize_int8(*, rows, cols, x, q, s, x_stride=0, row_end=None, stream=None):
+    """bf16 rows -> int8 codes with one fp32 scale a row."""
+    d = _device()
+    _call.quantize_int8(d, rows, cols, x_stride, x, q, s, row_end, stream)
+
+
+def moe_grouped_gemm_int8_workspace_size(E, N, K, M_cap, max_rows=0) -> int:
+    return lib().moe_grouped_gemm_int8_workspace_size(E, N, K, M_cap, max_rows)
+
+
+def moe_grouped_gemm_int8(*, E, N, K, M_cap, split_sizes, padded_offsets, a, a_s, b, b_s, c,
+                          b_stride=0, b_s_stride=0, ldc=0, c_type=TYPE_BF16, max_rows=0,
+                          cu_margin=0, err_flag=None, workspace=None, stream=None):
+    """C[r] = A[r] . B_e^T on int8 rows with a scale each, for every group's rows;
+    the sums are exact."""
+    d = _device()
+    _call.grouped_gemm_int8(d, E, N, K, M_cap, b_stride, b_s_stride, ldc, c_type, max_rows,
+                            cu_margin, split_sizes, padded_offsets, a, a_s, b, b_s, c, err_flag,
+                            workspace, stream)

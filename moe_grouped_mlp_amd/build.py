@@ -29,6 +29,7 @@ SOURCES = ["api.cpp", "route.hip", "router.hip", "unfused.hip", "permute.hip", "
            "noalloc.hip",
            "api_step.cpp", "fp8_quant.hip", "fp8_gemm.hip", "fp8_wgrad.hip", "fp8_gemm_rows.hip",
            "router_loss.hip", "grad.hip",
+           "gate.hip", "adamw.hip", "int8_quant.hip", "int8_gemm.hip", "int8_gemm_rows.hip",
            "router_route.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

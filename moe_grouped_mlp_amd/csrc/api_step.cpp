@@ -1,6 +1,7 @@
-// C ABI of the operators around the expert products of a training step:
-// block-scaled FP8 (quantization, grouped product, weight gradient), the
-// router's losses and gradient, and the gradient norm and clipping.  As in
+// C ABI of the operators around the expert products: block-scaled FP8
+// (quantization, grouped product, weight gradient), 8-bit integers (quantization,
+// grouped product), the router's choice by scores, its losses and gradients, the
+// gradient norm and clipping, and AdamW.  As in
 // api.cpp every call checks its arguments, then only enqueues kernels.
 #include <hip/hip_runtime.h>
 
@@ -15,6 +16,8 @@ namespace {
 
 using moe::kMaxExperts;
 using moe::kMaxTopK;
+constexpr int kMaxGroups = 64;
+constexpr int kMaxInt8K = 131056;   // K 2^14 < 2^31
 
 constexpr int kBlk = MOE_FP8_BLOCK;
 constexpr int kTileN = 256;              // weight rows of a product's tile
@@ -84,6 +87,29 @@ bool overlap(Range* r, int64_t n) {
   }
   return false;
 }
+
+// Room for n ranges: `few` if they fit, else memory of its own (null: none).
+class Ranges {
+ public:
+  explicit Ranges(size_t n) : r_(n <= kFew ? few_ : new (std::nothrow) Range[n]) {}
+  ~Ranges() {
+    if (r_ != few_) delete[] r_;
+  }
+  Ranges(const Ranges&) = delete;
+  Ranges& operator=(const Ranges&) = delete;
+  bool ok() const { return r_ != nullptr; }
+  void add(const void* p, int64_t bytes, bool write) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    if (p && bytes > 0) r_[n_++] = Range{lo, lo + static_cast<uintptr_t>(bytes), write};
+  }
+  bool bad() { return overlap(r_, n_); }
+
+ private:
+  static constexpr size_t kFew = 2 * moe::kGradList;
+  Range few_[kFew];
+  Range* r_;
+  int64_t n_ = 0;
+};
 
 // Checks of the tensor list that both calls share.
 moe_status list_check(const moe_grad_args* a) {
@@ -251,6 +277,112 @@ moe_status moe_grouped_wgrad_fp8(const moe_wgrad_fp8_args* a, void* stream) {
   return launched(moe::launch_fp8_wgrad(g, f32, wide, groups, static_cast<hipStream_t>(stream)));
 }
 
+// -------------------------------------------------------- 8-bit integers ----
+moe_status moe_quantize_int8(const moe_quant_int8_args* a, void* stream) {
+  if (!a || a->rows < 0 || a->cols < 16 || a->cols % 16 != 0 || !aligned16(a->x) || !aligned16(a->q) ||
+      (a->x_stride != 0 && (a->x_stride < a->cols || a->x_stride % 8 != 0)) ||
+      (a->rows > 0 && (!a->x || !a->q || !a->s)))
+    return MOE_ERR_INVALID_ARG;
+  if (a->rows >= kMaxGridX) return MOE_ERR_UNSUPPORTED;
+  int cu = 0;
+  if (moe_status st = moe::current_device(&cu)) return st;
+  if (a->rows == 0) return MOE_OK;
+  return launched(moe::launch_quantize_int8(*a, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_grouped_gemm_int8_workspace_size(int E, int N, int K, int64_t M_cap, int max_rows) {
+  return moe_grouped_gemm_fp8_workspace_size(E, N, K, M_cap, max_rows);
+}
+
+moe_status moe_grouped_gemm_int8(const moe_gemm_int8_args* a, void* stream) {
+  if (!a || a->E < 1 || a->E > kMaxExperts || a->N < 16 || a->N % 16 != 0 || a->K < 16 ||
+      a->K % 16 != 0 || a->K > kMaxInt8K || a->M_cap < 1 || a->M_cap > INT32_MAX || !a->split_sizes ||
+      !a->padded_offsets || !a->a || !a->a_s || !a->b || !a->b_s || !a->c || !type_ok(a->c_type) ||
+      !aligned16(a->workspace) || a->max_rows < 0 || a->cu_margin < 0 || !aligned16(a->a) || !aligned16(a->b) ||
+      !aligned16(a->c))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t nk = static_cast<int64_t>(a->N) * a->K;
+  if ((a->b_stride != 0 && (a->b_stride < nk || a->b_stride % 16 != 0)) ||
+      (a->b_s_stride != 0 && a->b_s_stride < a->N) || (a->ldc != 0 && (a->ldc < a->N || a->ldc % 8 != 0)))
+    return MOE_ERR_INVALID_ARG;
+  const int64_t most = a->max_rows ? std::min<int64_t>(a->max_rows, a->M_cap) : a->M_cap;
+  const bool f32 = a->c_type == MOE_TYPE_F32;
+  const int64_t rows = rows_estimate(a->E, a->M_cap), tiles_n = ceil_div(a->N, kTileN);
+  auto at_most = [&](int g) { return (ceil_div(a->M_cap, 64 * g) + a->E) * tiles_n; };
+  if (at_most(moe::fp8_most_groups(false)) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  int cu = 0;
+  if (moe_status st = moe::current_device(&cu)) return st;
+  if (a->cu_margin >= cu) return MOE_ERR_INVALID_ARG;
+  // half a tile of every group is filled on average
+  const int groups = tile_groups(false, cu - a->cu_margin, [&](int g) { return (ceil_div(rows, 64 * g) + a->E / 2) * tiles_n; });
+  moe::Int8Args g{};
+  g.E = a->E;
+  g.N = a->N;
+  g.K = a->K;
+  g.M_cap = a->M_cap;
+  g.split = a->split_sizes;
+  g.padded = a->padded_offsets;
+  g.a = reinterpret_cast<const uint8_t*>(a->a);
+  g.a_s = a->a_s;
+  g.b = reinterpret_cast<const uint8_t*>(a->b);
+  g.b_s = a->b_s;
+  g.b_stride = a->b_stride ? a->b_stride : nk;
+  g.b_s_stride = a->b_s_stride ? a->b_s_stride : a->N;
+  g.c = a->c;
+  g.ldc = a->ldc ? a->ldc : a->N;
+  g.stream = a->M_cap <= (int64_t(1) << 62) / 4 / g.ldc && streams(a->M_cap, g.ldc * type_bytes(a->c_type));
+  g.group_m = 4;
+  g.err = a->err_flag;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  // as in the FP8 product: the kernel for few rows spreads over all CUs, and K
+  // may be cut where there is room for its parts
+  if (most <= 32 && a->cu_margin == 0 && a->N / 32 < kMaxGridX - 1)
+    return launched(moe::launch_int8_rows(g, most <= 16 ? 16 : 32, f32, s));
+  const int full = tile_grid(cu, a->cu_margin, INT32_MAX);
+  const bool cut = cuts_k(a->E, a->N, a->K, a->M_cap, most, cu) && a->workspace &&
+                   a->workspace_bytes >= static_cast<size_t>(full) * moe::kFp8PartFloats * sizeof(int32_t);
+  if (cut) g.part = static_cast<moe::fp8_f32x4*>(a->workspace);
+  g.grid = cut ? full : tile_grid(cu, a->cu_margin, at_most(groups));
+  return launched(moe::launch_int8_gemm(g, f32, groups, s));
+}
+
+// ---------------------------------------------------- router: choice --------
+moe_status moe_router_gate(const moe_gate_args* a, void* stream) {
+  if (!a || a->T < 0 || a->E < 1 || a->E > kMaxExperts || a->k < 1 || a->k > std::min(a->E, kMaxTopK) ||
+      static_cast<int64_t>(a->T) * a->k > INT32_MAX || (a->score != MOE_SCORE_SOFTMAX && a->score != MOE_SCORE_SIGMOID) ||
+      !type_ok(a->logits_type) || !std::isfinite(a->scale) || (a->ld != 0 && a->ld < a->E) ||
+      reinterpret_cast<uintptr_t>(a->logits) % type_bytes(a->logits_type) != 0 ||
+      (a->T > 0 && (!a->logits || !a->expert_idx || !a->probs)) || a->n_groups < 0 || a->n_groups > kMaxGroups)
+    return MOE_ERR_INVALID_ARG;
+  if (a->n_groups > 1 && (a->E % a->n_groups != 0 || a->topk_groups < 1 || a->topk_groups > a->n_groups ||
+                          (a->group_top != 1 && a->group_top != 2) || a->k > a->E / a->n_groups * a->topk_groups))
+    return MOE_ERR_INVALID_ARG;
+  int cu = 0;
+  if (moe_status st = moe::current_device(&cu)) return st;
+  if (a->T == 0) return MOE_OK;
+  return launched(moe::launch_router_gate(*a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_router_gate_bwd(const moe_gate_bwd_args* a, void* stream) {
+  if (!a || a->T < 0 || a->E < 1 || a->E > kMaxExperts || a->k < 1 || a->k > std::min(a->E, kMaxTopK) ||
+      static_cast<int64_t>(a->T) * a->k > INT32_MAX || (a->score != MOE_SCORE_SOFTMAX && a->score != MOE_SCORE_SIGMOID) ||
+      !type_ok(a->logits_type) || !std::isfinite(a->scale) || (a->ld != 0 && a->ld < a->E) || (a->ld_d != 0 && a->ld_d < a->E) ||
+      (reinterpret_cast<uintptr_t>(a->logits) | reinterpret_cast<uintptr_t>(a->dlogits)) % type_bytes(a->logits_type) != 0 ||
+      (a->T > 0 && (!a->logits || !a->expert_idx || !a->dprobs || !a->dlogits)))
+    return MOE_ERR_INVALID_ARG;
+  int cu = 0;
+  if (moe_status st = moe::current_device(&cu)) return st;
+  if (a->T == 0) return MOE_OK;
+  return launched(moe::launch_router_gate_bwd(*a, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_router_bias_update(const moe_bias_update_args* a, void* stream) {
+  if (!a || a->E < 1 || a->E > kMaxExperts || !std::isfinite(a->rate) || !a->counts || !a->bias) return MOE_ERR_INVALID_ARG;
+  int cu = 0;
+  if (moe_status st = moe::current_device(&cu)) return st;
+  return launched(moe::launch_bias_update(*a, static_cast<hipStream_t>(stream)));
+}
+
 // ------------------------------------------------------- router losses ------
 size_t moe_router_loss_workspace_size(int T, int E) {
   if (T < 0 || E < 1 || E > kMaxExperts) return 0;
@@ -317,24 +449,15 @@ moe_status moe_grad_clip(const moe_grad_args* a, void* stream) {
   // no tensor that is written may overlap another range of the list; a
   // tensor scaled in place is one range
   {
-    Range few[2 * moe::kGradList];
-    Range* r = few;
-    if (a->n_tensors > moe::kGradList) {
-      r = new (std::nothrow) Range[2 * static_cast<size_t>(a->n_tensors)];
-      if (!r) return MOE_ERR_UNSUPPORTED;
-    }
-    int64_t n = 0;
+    Ranges r(2 * static_cast<size_t>(a->n_tensors));
+    if (!r.ok()) return MOE_ERR_UNSUPPORTED;
     for (int i = 0; i < a->n_tensors; ++i) {
       const moe_tensor& t = a->tensors[i];
-      if (t.numel == 0) continue;
-      const uintptr_t bytes = static_cast<uintptr_t>(t.numel) * type_bytes(t.type);
-      const uintptr_t in = reinterpret_cast<uintptr_t>(t.data);
-      const uintptr_t out = t.out ? reinterpret_cast<uintptr_t>(t.out) : in;
-      if (out != in) r[n++] = Range{in, in + bytes, false};
-      r[n++] = Range{out, out + bytes, true};
+      const int64_t bytes = t.numel * type_bytes(t.type);
+      if (t.out && t.out != t.data) r.add(t.data, bytes, false);
+      r.add(t.out ? t.out : t.data, bytes, true);
     }
-    const bool bad = overlap(r, n);
-    if (r != few) delete[] r;
+    const bool bad = r.bad();
     if (bad) return MOE_ERR_INVALID_ARG;
   }
   int cu = 0;
@@ -343,6 +466,83 @@ moe_status moe_grad_clip(const moe_grad_args* a, void* stream) {
   return for_lists(a, [&](const moe::GradList& l) {
     return launched(moe::launch_grad_scale(l, a->sumsq, a->max_norm, a->norm, a->err_flag, s));
   });
+}
+
+// ---------------------------------------------------------------- AdamW -----
+moe_status moe_adamw(const moe_adamw_args* a, void* stream) {
+  if (!a || a->n_tensors < 0 || (a->n_tensors > 0 && !a->tensors) ||
+      (a->state_type != MOE_STATE_F32 && a->state_type != MOE_STATE_FP8) || !std::isfinite(a->lr) ||
+      !(a->beta1 >= 0.0 && a->beta1 < 1.0) || !(a->beta2 >= 0.0 && a->beta2 < 1.0) || !(a->eps >= 0.0) ||
+      !std::isfinite(a->eps) || (!a->step_dev && a->step < 1) || (a->sumsq && !(a->max_norm >= 0.0f)) ||
+      (reinterpret_cast<uintptr_t>(a->sumsq) & 7) || ((reinterpret_cast<uintptr_t>(a->step_dev) | reinterpret_cast<uintptr_t>(a->lr_dev)) & 3))
+    return MOE_ERR_INVALID_ARG;
+  const bool fp8 = a->state_type == MOE_STATE_FP8;
+  Ranges r(7 * static_cast<size_t>(a->n_tensors));
+  if (!r.ok()) return MOE_ERR_UNSUPPORTED;
+  for (int i = 0; i < a->n_tensors; ++i) {
+    const moe_adamw_tensor& t = a->tensors[i];
+    if (!type_ok(t.param_type) || !type_ok(t.grad_type) || t.numel < 0 || t.numel > (int64_t(1) << 46) ||
+        !std::isfinite(t.weight_decay) || (t.master && t.param_type != MOE_TYPE_BF16))
+      return MOE_ERR_INVALID_ARG;
+    if (t.numel == 0) continue;
+    if (!t.param || !t.grad || !t.m || !t.v || (fp8 && (!t.m_scale || !t.v_scale))) return MOE_ERR_INVALID_ARG;
+    auto off = [](const void* p, int64_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; };
+    if (off(t.param, type_bytes(t.param_type)) || off(t.grad, type_bytes(t.grad_type)) || off(t.master, 4) ||
+        (fp8 ? off(t.m_scale, 4) || off(t.v_scale, 4) : off(t.m, 4) || off(t.v, 4)))
+      return MOE_ERR_INVALID_ARG;
+    const int64_t state = t.numel * (fp8 ? 1 : 4), scales = ceil_div(t.numel, kBlk) * 4;
+    r.add(t.param, t.numel * type_bytes(t.param_type), true);
+    r.add(t.grad, t.numel * type_bytes(t.grad_type), false);
+    r.add(t.master, t.numel * 4, true);
+    r.add(t.m, state, true);
+    r.add(t.v, state, true);
+    if (fp8) {
+      r.add(t.m_scale, scales, true);
+      r.add(t.v_scale, scales, true);
+    }
+  }
+  if (r.bad()) return MOE_ERR_INVALID_ARG;
+  int cu = 0;
+  if (moe_status st = moe::current_device(&cu)) return st;
+  moe::AdamList l{};
+  l.b1_64 = a->beta1;
+  l.b2_64 = a->beta2;
+  l.b1 = static_cast<float>(a->beta1);
+  l.b2 = static_cast<float>(a->beta2);
+  l.a1 = static_cast<float>(1.0 - a->beta1);
+  l.a2 = static_cast<float>(1.0 - a->beta2);
+  l.eps = static_cast<float>(a->eps);
+  l.lr = static_cast<float>(a->lr);
+  l.step = a->step;
+  l.c1 = a->step_dev ? 1.0 : 1.0 - std::pow(a->beta1, a->step);
+  l.lr_c1 = static_cast<float>(a->lr / l.c1);
+  l.rs_c2 = a->step_dev ? 1.0f : static_cast<float>(1.0 / std::sqrt(1.0 - std::pow(a->beta2, a->step)));
+  l.max_norm = a->max_norm;
+  l.sumsq = a->sumsq;
+  l.step_dev = a->step_dev;
+  l.lr_dev = a->lr_dev;
+  l.err = a->err_flag;
+  l.stochastic = fp8 && a->stochastic;
+  l.seed = a->seed;
+  int i = 0;
+  do {
+    l.n = 0;
+    l.chunks = 0;
+    for (; i < a->n_tensors && l.n < moe::kAdamList; ++i) {
+      const moe_adamw_tensor& t = a->tensors[i];
+      if (t.numel == 0) continue;
+      const bool vec = aligned16(t.param) && aligned16(t.grad) && aligned16(t.master) && aligned16(t.m) && aligned16(t.v);
+      moe::AdamEntry& e = l.t[l.n++];
+      e = moe::AdamEntry{t.param, t.grad, t.master, t.m, t.v, t.m_scale, t.v_scale, t.numel, l.chunks, t.weight_decay,
+                         (t.param_type == MOE_TYPE_BF16 ? moe::kAdamParam16 : 0) | (t.grad_type == MOE_TYPE_BF16 ? moe::kAdamGrad16 : 0) |
+                             (vec ? moe::kAdamVec : 0),
+                         static_cast<uint32_t>(i)};
+      l.chunks += ceil_div(t.numel, moe::kAdamChunk);
+    }
+    if (l.chunks == 0) continue;
+    if (moe_status st = launched(moe::launch_adamw(l, fp8, static_cast<hipStream_t>(stream)))) return st;
+  } while (i < a->n_tensors);
+  return MOE_OK;
 }
 
 }  // extern "C"

@@ -172,6 +172,20 @@ hipError_t launch_fp8_gemm(const Fp8Args& g, bool f32, bool wide, int groups, hi
 hipError_t launch_fp8_rows(const Fp8Args& g, int tile_rows, bool f32, bool wide, hipStream_t s);
 hipError_t launch_fp8_wgrad(const Fp8Args& g, bool f32, bool wide, int groups, hipStream_t s);
 
+// ---- 8-bit integers ---------------------------------------------------------
+hipError_t launch_quantize_int8(const moe_quant_int8_args& a, hipStream_t s);
+
+// the FP8 product's arguments: codes are int8, a_s [M_cap], b_s [N] per expert,
+// part holds 32-bit integers
+using Int8Args = Fp8Args;
+hipError_t launch_int8_gemm(const Int8Args& g, bool f32, int groups, hipStream_t s);
+hipError_t launch_int8_rows(const Int8Args& g, int tile_rows, bool f32, hipStream_t s);
+
+// ---- router: choice by scores -------------------------------------------------
+hipError_t launch_router_gate(const moe_gate_args& a, hipStream_t s);
+hipError_t launch_router_gate_bwd(const moe_gate_bwd_args& a, hipStream_t s);
+hipError_t launch_bias_update(const moe_bias_update_args& a, hipStream_t s);
+
 // ---- router losses ----------------------------------------------------------
 size_t router_loss_workspace_bytes(int T, int E);
 hipError_t launch_router_loss(const moe_router_loss_args& a, hipStream_t s);
@@ -202,6 +216,43 @@ hipError_t launch_grad_sumsq(const GradList& l, double* partial, hipStream_t s);
 hipError_t launch_grad_sum(const double* partial, int n, double* sumsq, hipStream_t s);
 hipError_t launch_grad_scale(const GradList& l, const double* sumsq, float max_norm, float* norm,
                              int32_t* err, hipStream_t s);
+
+// ---- AdamW ----------------------------------------------------------------------
+constexpr int kAdamList = 40;          // tensors of one launch (3.6 KB of arguments)
+constexpr int kAdamBlocks = 2048;      // workgroups of one launch at most
+constexpr int64_t kAdamChunk = 16384;  // elements a workgroup takes at a time
+enum AdamFlags : int32_t { kAdamParam16 = 1, kAdamGrad16 = 2, kAdamVec = 4 };
+struct AdamEntry {
+  void* param;
+  const void* grad;
+  float* master;           // nullable
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t numel;
+  int64_t first;           // chunks of the entries before it
+  float weight_decay;
+  int32_t flags;           // AdamFlags
+  uint32_t index;          // place in the caller's list
+};
+struct AdamList {
+  AdamEntry t[kAdamList];
+  int n;
+  int64_t chunks;
+  float lr, lr_c1, rs_c2;  // lr, lr / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
+  float b1, a1, b2, a2;    // beta and 1 - beta
+  float eps, max_norm;
+  double c1, b1_64, b2_64; // 1 - beta1^step; for steps counted on the device
+  const double* sumsq;
+  const int32_t* step_dev;
+  const float* lr_dev;
+  int32_t* err;
+  int32_t step, stochastic;
+  uint32_t seed;
+};
+static_assert(sizeof(AdamList) <= 4000, "a launch takes 4 KB of arguments");
+hipError_t launch_adamw(const AdamList& l, bool fp8, hipStream_t s);
 
 // ---- entry-point bodies shared between C-ABI variants (api.cpp) ---------
 // moe_grouped_mlp_bwd with the workspace given apart from the arguments

@@ -27,7 +27,7 @@ PyObject* g_raw_stream = nullptr;   // device -> the current stream's handle
 
 struct Raised {};   // a Python exception is set
 
-enum : unsigned { kF32 = 1, kBF16 = 2, kF64 = 4, kI32 = 8, kU8 = 16, kE4M3 = 32, kBool = 64,
+enum : unsigned { kF32 = 1, kBF16 = 2, kF64 = 4, kI32 = 8, kU8 = 16, kE4M3 = 32, kBool = 64, kI8 = 128,
                   kCodes = kU8 | kE4M3, kMask = kU8 | kBool };
 
 struct TypeName {
@@ -39,7 +39,7 @@ constexpr TypeName kTypes[] = {
     {kF32, at::kFloat, "torch.float32"},   {kBF16, at::kBFloat16, "torch.bfloat16"},
     {kF64, at::kDouble, "torch.float64"},  {kI32, at::kInt, "torch.int32"},
     {kU8, at::kByte, "torch.uint8"},       {kE4M3, at::kFloat8_e4m3fn, "torch.float8_e4m3fn"},
-    {kBool, at::kBool, "torch.bool"}};
+    {kBool, at::kBool, "torch.bool"},      {kI8, at::kChar, "torch.int8"}};
 
 unsigned type_bit(at::ScalarType t) {
   for (const TypeName& n : kTypes)
@@ -63,6 +63,7 @@ class Args {
   [[noreturn]] void refuse(const std::string& text) const { fail(PyExc_ValueError, fn_ + (": " + text)); }
 
   PyObject* next() { return a_[at_++]; }
+  PyObject* peek() const { return a_[at_]; }
   int64_t i64() {
     const long long v = PyLong_AsLongLong(next());
     if (v == -1 && PyErr_Occurred()) throw Raised{};
@@ -74,10 +75,13 @@ class Args {
       fail(PyExc_OverflowError, fn_ + (": " + std::to_string(v) + " does not fit in 32 bits"));
     return static_cast<int32_t>(v);
   }
-  float f32() {
-    const double v = PyFloat_AsDouble(next());
-    if (v == -1.0 && PyErr_Occurred()) throw Raised{};
-    return static_cast<float>(v);
+  double f64() { return number(next()); }
+  float f32() { return static_cast<float>(f64()); }
+  uint32_t u32() {
+    const int64_t v = i64();
+    if (v < 0 || v > std::numeric_limits<uint32_t>::max())
+      fail(PyExc_OverflowError, fn_ + (": " + std::to_string(v) + " does not fit in 32 bits without a sign"));
+    return static_cast<uint32_t>(v);
   }
   bool truth() {
     const int v = PyObject_IsTrue(next());
@@ -127,6 +131,89 @@ class Args {
     if (n != v.size()) refuse(other);
     return v;
   }
+  // A list that goes with params (n tensors): f(i, tensor), for None entries too
+  // (null) where they may be.
+  template <typename F>
+  void along(PyObject* seq, const char* name, size_t n, bool none, F&& f) {
+    size_t got = 0;
+    each(
+        seq,
+        [&](size_t i, const at::Tensor* t) {
+          if (i >= n) refuse(std::string(name) + " must have an entry for each of params");
+          if (t) at_home(*t);
+          f(i, t);
+          ++got;
+        },
+        none);
+    if (got != n) refuse(std::string(name) + " must have an entry for each of params");
+  }
+  // moe_adamw's lists.
+  std::vector<moe_adamw_tensor> adamw_list(int32_t* state_type) {
+    std::vector<moe_adamw_tensor> v;
+    PyObject *params = next(), *grads = next(), *m = next(), *vv = next(), *master = next(), *m_scale = next(), *v_scale = next(),
+             *decay = next();
+    each(params, [&](size_t i, const at::Tensor& t) {
+      const unsigned type = type_bit(t.scalar_type());
+      if (!(type & (kF32 | kBF16))) refuse("params[" + std::to_string(i) + "] must be bfloat16 or float32");
+      at_home(t);
+      moe_adamw_tensor a{};
+      a.param = t.data_ptr();
+      a.numel = t.numel();
+      a.param_type = type == kF32 ? MOE_TYPE_F32 : MOE_TYPE_BF16;
+      v.push_back(a);
+    });
+    const size_t n = v.size();
+    auto of = [&](const char* name, size_t i, const at::Tensor& t, unsigned types, int64_t numel) {
+      if (!(type_bit(t.scalar_type()) & types) || t.numel() != numel)
+        refuse(std::string(name) + "[" + std::to_string(i) + "] is of another type or size than params[" + std::to_string(i) + "] takes");
+    };
+    along(grads, "grads", n, false, [&](size_t i, const at::Tensor* t) {
+      of("grads", i, *t, kF32 | kBF16, v[i].numel);
+      v[i].grad = t->data_ptr();
+      v[i].grad_type = type_bit(t->scalar_type()) == kF32 ? MOE_TYPE_F32 : MOE_TYPE_BF16;
+    });
+    // the states' type is that of the scales being there
+    const bool fp8 = m_scale != Py_None;
+    if (fp8 != (v_scale != Py_None)) refuse("m_scale and v_scale go together");
+    *state_type = fp8 ? MOE_STATE_FP8 : MOE_STATE_F32;
+    const unsigned state = fp8 ? kCodes : kF32;
+    along(m, "m", n, false, [&](size_t i, const at::Tensor* t) {
+      of("m", i, *t, state, v[i].numel);
+      v[i].m = t->data_ptr();
+    });
+    along(vv, "v", n, false, [&](size_t i, const at::Tensor* t) {
+      of("v", i, *t, state, v[i].numel);
+      v[i].v = t->data_ptr();
+    });
+    if (master != Py_None)
+      along(master, "master", n, true, [&](size_t i, const at::Tensor* t) {
+        if (!t) return;
+        of("master", i, *t, kF32, v[i].numel);
+        if (v[i].param_type != MOE_TYPE_BF16) refuse("master[" + std::to_string(i) + "] is of a parameter that is float32 itself");
+        v[i].master = static_cast<float*>(t->data_ptr());
+      });
+    if (fp8) {
+      along(m_scale, "m_scale", n, false, [&](size_t i, const at::Tensor* t) {
+        of("m_scale", i, *t, kF32, static_cast<int64_t>(blocks(v[i].numel)));
+        v[i].m_scale = static_cast<float*>(t->data_ptr());
+      });
+      along(v_scale, "v_scale", n, false, [&](size_t i, const at::Tensor* t) {
+        of("v_scale", i, *t, kF32, static_cast<int64_t>(blocks(v[i].numel)));
+        v[i].v_scale = static_cast<float*>(t->data_ptr());
+      });
+    }
+    if (PyNumber_Check(decay) && !PySequence_Check(decay)) {
+      const float d = static_cast<float>(number(decay));
+      for (moe_adamw_tensor& t : v) t.weight_decay = d;
+    } else {
+      PyObject* fast = PySequence_Fast(decay, "weight_decay must be a number or a list of them");
+      if (!fast) throw Raised{};
+      const Drop drop{fast};
+      if (PySequence_Fast_GET_SIZE(fast) != static_cast<Py_ssize_t>(n)) refuse("weight_decay must have an entry for each of params");
+      for (size_t i = 0; i < n; ++i) v[i].weight_decay = static_cast<float>(number(PySequence_Fast_GET_ITEM(fast, static_cast<Py_ssize_t>(i))));
+    }
+    return v;
+  }
   void* stream() {
     PyObject* s = next();
     if (PyLong_Check(s)) return pointer(s);
@@ -153,22 +240,34 @@ class Args {
     if (!here(t))
       refuse("the tensors must be contiguous and on the current device (cuda:" + std::to_string(dev_) + ")");
   }
+  struct Drop {
+    PyObject* o;
+    ~Drop() { Py_DECREF(o); }
+  };
+  static double number(PyObject* o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+    return v;
+  }
+  // f(i, tensor) for a list of tensors; none: f(i, pointer), null for None.
   template <typename F>
   void each(PyObject* seq, F&& f) {
+    each(seq, [&](size_t i, const at::Tensor* t) { f(i, *t); }, false);
+  }
+  template <typename F>
+  void each(PyObject* seq, F&& f, bool none) {
     PyObject* fast = PySequence_Fast(seq, "");
     if (!fast) {
       PyErr_Clear();
       refuse("a list of tensors is needed");
     }
-    struct Drop {
-      PyObject* o;
-      ~Drop() { Py_DECREF(o); }
-    } drop{fast};
+    const Drop drop{fast};
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
     for (Py_ssize_t i = 0; i < n; ++i) {
       PyObject* o = PySequence_Fast_GET_ITEM(fast, i);
-      if (!THPVariable_Check(o)) refuse("a list of tensors is needed");
-      f(static_cast<size_t>(i), THPVariable_Unpack(o));
+      const bool is = THPVariable_Check(o);
+      if (!is && !(none && o == Py_None)) refuse("a list of tensors is needed");
+      f(static_cast<size_t>(i), is ? &THPVariable_Unpack(o) : nullptr);
     }
   }
   static void* pointer(PyObject* o) {
@@ -371,6 +470,146 @@ PyObject* grad_clip(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
   });
 }
 
+// The type of a tensor that may have two.
+int32_t type_of(PyObject* o) {
+  return THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kBFloat16 ? MOE_TYPE_BF16 : MOE_TYPE_F32;
+}
+
+PyObject* router_gate(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
+  constexpr const char* fn = "moe_router_gate";
+  return guarded(fn, [&] {
+    Args p(fn, args, n_args, 18);
+    moe_gate_args a{};
+    a.T = p.i32();
+    a.E = p.i32();
+    a.k = p.i32();
+    a.score = p.i32();
+    a.n_groups = p.i32();
+    a.topk_groups = p.i32();
+    a.group_top = p.i32();
+    a.renorm = p.truth();
+    a.scale = p.f32();
+    a.ld = p.i64();
+    const Size T = a.T;
+    a.logits_type = type_of(p.peek());
+    a.logits = p.buf("logits", kF32 | kBF16, T > 0 ? (T - 1) * (a.ld ? a.ld : a.E) + a.E : 0);
+    a.bias = p.buf<float>("bias", kF32, a.E);
+    a.token_mask = p.buf<uint8_t>("token_mask", kMask, T);
+    a.expert_idx = p.buf<int32_t>("expert_idx", kI32, T * a.k);
+    a.probs = p.buf<float>("probs", kF32, T * a.k);
+    a.counts = p.buf<int32_t>("counts", kI32, a.E);
+    return call(p, moe_router_gate, a);
+  });
+}
+
+PyObject* router_gate_bwd(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
+  constexpr const char* fn = "moe_router_gate_bwd";
+  return guarded(fn, [&] {
+    Args p(fn, args, n_args, 15);
+    moe_gate_bwd_args a{};
+    a.T = p.i32();
+    a.E = p.i32();
+    a.k = p.i32();
+    a.score = p.i32();
+    a.renorm = p.truth();
+    a.scale = p.f32();
+    a.accumulate = p.truth();
+    a.ld = p.i64();
+    a.ld_d = p.i64();
+    const Size T = a.T;
+    a.logits_type = type_of(p.peek());
+    a.logits = p.buf("logits", kF32 | kBF16, T > 0 ? (T - 1) * (a.ld ? a.ld : a.E) + a.E : 0);
+    a.expert_idx = p.buf<int32_t>("expert_idx", kI32, T * a.k);
+    a.dprobs = p.buf<float>("dprobs", kF32, T * a.k);
+    a.dlogits = p.buf("dlogits", a.logits_type == MOE_TYPE_F32 ? kF32 : kBF16, T > 0 ? (T - 1) * (a.ld_d ? a.ld_d : a.E) + a.E : 0);
+    return call(p, moe_router_gate_bwd, a);
+  });
+}
+
+PyObject* router_bias_update(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
+  constexpr const char* fn = "moe_router_bias_update";
+  return guarded(fn, [&] {
+    Args p(fn, args, n_args, 7);
+    moe_bias_update_args a{};
+    a.E = p.i32();
+    a.rate = p.f32();
+    a.reset = p.truth();
+    a.counts = p.buf<int32_t>("counts", kI32, a.E);
+    a.bias = p.buf<float>("bias", kF32, a.E);
+    return call(p, moe_router_bias_update, a);
+  });
+}
+
+PyObject* adamw(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
+  constexpr const char* fn = "moe_adamw";
+  return guarded(fn, [&] {
+    Args p(fn, args, n_args, 22);
+    moe_adamw_args a{};
+    const std::vector<moe_adamw_tensor> v = p.adamw_list(&a.state_type);
+    a.tensors = v.data();
+    a.n_tensors = static_cast<int32_t>(v.size());
+    a.lr = p.f64();
+    a.beta1 = p.f64();
+    a.beta2 = p.f64();
+    a.eps = p.f64();
+    a.step = p.i32();
+    a.max_norm = p.f32();
+    a.stochastic = p.truth();
+    a.seed = p.u32();
+    a.sumsq = p.buf<double>("sumsq", kF64, 1);
+    a.step_dev = p.buf<int32_t>("step_dev", kI32, 1);
+    a.lr_dev = p.buf<float>("lr_dev", kF32, 1);
+    a.err_flag = p.buf<int32_t>("err_flag", kI32, 1);
+    return call(p, moe_adamw, a);
+  });
+}
+
+PyObject* quantize_int8(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
+  constexpr const char* fn = "moe_quantize_int8";
+  return guarded(fn, [&] {
+    Args p(fn, args, n_args, 9);
+    moe_quant_int8_args a{};
+    a.rows = p.i32();
+    a.cols = p.i32();
+    a.x_stride = p.i64();
+    const Size R = a.rows, C = a.cols;
+    a.x = p.buf("x", kBF16, R > 0 ? (R - 1) * (a.x_stride ? a.x_stride : C) + C : 0);
+    a.q = p.buf<int8_t>("q", kI8, R * C);
+    a.s = p.buf<float>("s", kF32, R);
+    a.row_end = p.buf<int32_t>("row_end", kI32, 1);
+    return call(p, moe_quantize_int8, a);
+  });
+}
+
+PyObject* grouped_gemm_int8(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
+  constexpr const char* fn = "moe_grouped_gemm_int8";
+  return guarded(fn, [&] {
+    Args p(fn, args, n_args, 21);
+    moe_gemm_int8_args a{};
+    a.E = p.i32();
+    a.N = p.i32();
+    a.K = p.i32();
+    a.M_cap = p.i64();
+    a.b_stride = p.i64();
+    a.b_s_stride = p.i64();
+    a.ldc = p.i64();
+    a.c_type = p.i32();
+    a.max_rows = p.i32();
+    a.cu_margin = p.i32();
+    const Size E = a.E, N = a.N, K = a.K, M = a.M_cap, nk = N * K;
+    a.split_sizes = p.buf<int32_t>("split_sizes", kI32, E);
+    a.padded_offsets = p.buf<int32_t>("padded_offsets", kI32, E + 1);
+    a.a = p.buf<int8_t>("a", kI8, M * K);
+    a.a_s = p.buf<float>("a_s", kF32, M);
+    a.b = p.buf<int8_t>("b", kI8, (E - 1) * (a.b_stride ? a.b_stride : nk) + nk);
+    a.b_s = p.buf<float>("b_s", kF32, (E - 1) * (a.b_s_stride ? a.b_s_stride : N) + N);
+    a.c = p.buf("c", a.c_type == MOE_TYPE_F32 ? kF32 : kBF16, (M - 1) * (a.ldc ? a.ldc : N) + N);
+    a.err_flag = p.buf<int32_t>("err_flag", kI32, 1);
+    a.workspace = p.buf("workspace", kU8, 0, &a.workspace_bytes);
+    return call(p, moe_grouped_gemm_int8, a);
+  });
+}
+
 PyObject* setup(PyObject*, PyObject* args) {
   PyObject *check, *raw_stream;
   if (!PyArg_ParseTuple(args, "OO", &check, &raw_stream)) return nullptr;
@@ -386,6 +625,8 @@ PyObject* setup(PyObject*, PyObject* args) {
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {FAST(quantize_fp8), FAST(grouped_gemm_fp8), FAST(grouped_wgrad_fp8), FAST(router_loss),
                           FAST(router_bwd),   FAST(grad_sumsq),       FAST(grad_clip),
+                          FAST(router_gate),  FAST(router_gate_bwd),  FAST(router_bias_update), FAST(adamw),
+                          FAST(quantize_int8), FAST(grouped_gemm_int8),
                           {"setup", setup, METH_VARARGS, nullptr},
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_call", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
