@@ -360,7 +360,7 @@ moe_status moe_router_gate(const moe_gate_args* a, void* stream) {
   int cu = 0;
   if (moe_status st = moe::current_device(&cu)) return st;
   if (a->T == 0) return MOE_OK;
-  return launched(moe::launch_router_gate(*a, static_cast<hipStream_t>(stream)));
+  return launched(moe::launch_router_gate(*a, cu, static_cast<hipStream_t>(stream)));
 }
 
 moe_status moe_router_gate_bwd(const moe_gate_bwd_args* a, void* stream) {

@@ -182,7 +182,7 @@ hipError_t launch_int8_gemm(const Int8Args& g, bool f32, int groups, hipStream_t
 hipError_t launch_int8_rows(const Int8Args& g, int tile_rows, bool f32, hipStream_t s);
 
 // ---- router: choice by scores -------------------------------------------------
-hipError_t launch_router_gate(const moe_gate_args& a, hipStream_t s);
+hipError_t launch_router_gate(const moe_gate_args& a, int cu, hipStream_t s);
 hipError_t launch_router_gate_bwd(const moe_gate_bwd_args& a, hipStream_t s);
 hipError_t launch_bias_update(const moe_bias_update_args& a, hipStream_t s);
 
