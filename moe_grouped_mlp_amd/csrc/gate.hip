@@ -36,6 +36,7 @@ MOE_DEV float logit_of(T v) {
 struct Layout {
   int E, Eg, n_groups, P, lgP, W;
   int lgPw, Ww;        // P and W if a whole wave takes the token
+  int full;            // every lane has V experts
   int vec, vec_bias;   // rows, the bias can be read vec_of(V) values at a time
 };
 struct Place {
@@ -73,10 +74,14 @@ MOE_DEV void load_row(const T* row, bool vec, const Place& p, float (&x)[V]) {
 }
 // The lane's logits; slots without an expert and ruled-out ones are -infinity.
 template <int V, typename T>
-MOE_DEV void load_logits(const T* row, const Layout& l, const Place& p, bool live, float (&x)[V]) {
+MOE_DEV void load_logits(const T* row, const Layout& l, const Place& p, float (&x)[V]) {
   load_row<V>(row, l.vec, p, x);
+  if (!l.full) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) x[i] = live && i < p.n && x[i] > neg_inf() ? x[i] : neg_inf();
+    for (int i = 0; i < V; ++i) x[i] = i < p.n ? x[i] : neg_inf();
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = fmaxf(x[i], neg_inf());   // NaN too
 }
 
 template <int CTRL>
@@ -207,8 +212,18 @@ MOE_DEV void choices32(const GateP& g, const Place& p, int lane, const float (&x
   const float err = score_error(g.sigmoid);
   auto score = [&](float v, float ev) { return g.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-v)) : ev * rz; };
   if (g.bias) {
+    if (g.sigmoid) {   // (a choice inside the loop would part the exponentials)
 #pragma unroll
-    for (int i = 0; i < V; ++i) c[i] = x[i] > neg_inf() ? fmaxf(score(x[i], e[i]) + bias[i], neg_inf()) : neg_inf();
+      for (int i = 0; i < V; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[i]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = e[i] * rz;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      c[i] = fmaxf(c[i] + bias[i], neg_inf());
+      c[i] = x[i] > neg_inf() ? c[i] : neg_inf();
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) c[i] = x[i];
@@ -351,44 +366,44 @@ MOE_DEV void picks_of_wave(const GateP& g, const Place& p, int lane, const float
 
 // The picks of a token by 64-bit choices, by a whole wave, V of them a lane:
 // ids to own[0 .. k - 1].  Few tokens come here, and wait for this code to be
-// loaded, so it is short: loops over a lane's logits, read again, and its
-// choices in LDS (room).
+// loaded, so it is short: the long steps are loops over choices in LDS.
 struct Room64 {
   uint64_t key[16];
   int id[16];
 };
 template <int V, typename T>
-MOE_DEV void picks64(const GateP& g, const T* row, bool kept, double* choice, Room64* room, int* own) {
+MOE_DEV void picks64(const GateP& g, const T* row, double* choice, Room64* room, int* own) {
   const int lane = threadIdx.x & (kWave - 1);
   const Place p = place_of(g.l, lane, g.l.lgPw, g.l.Ww);
   choice += lane;   // choice i at 64 i
-  auto logit = [&](int i) {
-    const float x = logit_of(row[i < p.n ? p.id0 + i : 0]);
-    return kept && i < p.n && x > neg_inf() ? x : neg_inf();
-  };
+  float x[V], bias[V] = {};
+  if (g.bias) load_row<V>(g.bias, false, p, bias);
+  load_row<V>(row, false, p, x);
   float m = neg_inf();
-  double z = 1.0;
-  if (!g.sigmoid) {
-#pragma unroll 1
-    for (int i = 0; i < V; ++i) m = fmaxf(m, logit(i));
-    m = max_lanes<kWave>(m);
-    z = 0.0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    x[i] = fmaxf(i < p.n ? x[i] : neg_inf(), neg_inf());
+    m = fmaxf(m, x[i]);
+    choice[kWave * i] = x[i];
   }
+  if (!g.sigmoid) m = max_lanes<kWave>(m);
+  double z = g.sigmoid ? 1.0 : 0.0;
 #pragma unroll 1
   for (int i = 0; i < V; ++i) {
-    const float x = logit(i);
-    const double e = exp(g.sigmoid ? -static_cast<double>(x) : x == m ? 0.0 : static_cast<double>(x) - static_cast<double>(m));
-    const double s = g.sigmoid ? 1.0 / (1.0 + e) : x > neg_inf() ? e : 0.0;
+    const double v = choice[kWave * i];
+    double s = exp(g.sigmoid ? -v : v == m ? 0.0 : v - m);
+    if (g.sigmoid) s = 1.0 / (1.0 + s);
+    else z += s = v > neg_inf64() ? s : 0.0;
     choice[kWave * i] = s;
-    if (!g.sigmoid) z += s;
   }
   if (!g.sigmoid) z = sum_lanes<kWave>(z);
   double a = neg_inf64(), b = neg_inf64();   // the lane's two largest
 #pragma unroll 1
+  for (int i = 0; i < V; ++i) choice[kWave * i] /= z;
+#pragma unroll
   for (int i = 0; i < V; ++i) {
-    double c = choice[kWave * i] / z;
-    if (g.bias) c += static_cast<double>(g.bias[i < p.n ? p.id0 + i : 0]);
-    c = logit(i) > neg_inf() && c > neg_inf64() ? c : neg_inf64();
+    double c = choice[kWave * i] + static_cast<double>(bias[i]);
+    c = x[i] > neg_inf() && c > neg_inf64() ? c : neg_inf64();
     b = fmax(b, fmin(a, c));
     a = fmax(a, c);
     choice[kWave * i] = c;
@@ -417,7 +432,7 @@ MOE_DEV void picks64(const GateP& g, const T* row, bool kept, double* choice, Ro
   for (int i = 0; i < V; ++i) {
     double c = choice[kWave * i];
     const bool in = stays && c > neg_inf64();
-    if (!g.bias && in) c = static_cast<double>(logit(i));
+    if (!g.bias && in) c = x[i];
     const uint64_t u = __builtin_bit_cast(uint64_t, c);
     const uint64_t key = in ? u ^ (static_cast<uint64_t>(static_cast<int64_t>(u) >> 63) | 1ull << 63) : 0;
     choice[kWave * i] = __builtin_bit_cast(double, key);
@@ -494,29 +509,30 @@ MOE_DEV void sort_keys(uint32_t (&k)[V]) {   // descending: Batcher's odd-even m
 template <int kList, int V, int... I>
 MOE_DEV void pop(uint32_t (&k)[V], bool win, std::integer_sequence<int, I...>) {
   ((k[I] = win ? k[I + 1] : k[I]), ...);
-  if (kList == V) k[kList - 1] = win ? 0 : k[kList - 1];
+  if (kList == V) k[kList - 1] = win ? 0 : k[kList - 1];   // (no key is 0)
 }
-// room: the token's 16 words.
+// room: 16 pairs of words for the token.
 template <int LPT, int V>
-MOE_DEV void picks_of_lanes(const GateP& g, const Place& p, int lane, const float (&c)[V], int* room, int* own, bool& open) {
-  constexpr uint32_t kLow = V - 1;
+MOE_DEV void picks_of_lanes(const GateP& g, const Place& p, int lane, const float (&c)[V], uint2* room, int* own, bool& open) {
+  constexpr uint32_t kLow = V - 1, kNone = 0x00800000u;   // (keys of -infinity are below kNone)
   constexpr int kList = V < kMaxTopK + 1 ? V : kMaxTopK + 1;
   uint32_t k[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) k[i] = c[i] > neg_inf() ? (key_of(c[i]) & ~kLow) | (kLow - i) : 0;
+  for (int i = 0; i < V; ++i) k[i] = (key_of(c[i]) & ~kLow) | (kLow - i);
   sort_keys<V>(k);
   const int at = threadIdx.x & (kWave - 1) & ~(LPT - 1);   // the token's first lane
   // (rolled: a launch waits for its code)
 #pragma unroll 1
   for (int j = 0; j <= g.k; ++j) {
-    const uint32_t top = max_lanes<LPT>(k[0] & ~kLow);
-    const uint64_t with = __ballot((k[0] & ~kLow) == top);
-    const uint32_t half = at & 32 ? static_cast<uint32_t>(with >> 32) : static_cast<uint32_t>(with);
-    const bool win = lane == __builtin_ctz(half >> (at & 31));   // (a lane of the token has it)
-    if (win) {
-      room[j] = static_cast<int>(k[0]);
-      if (j < g.k) own[j] = top != 0 ? p.id0 + static_cast<int>(kLow - (k[0] & kLow)) : -1;
+    const uint32_t head = k[0] & ~kLow, top = max_lanes<LPT>(head);
+    bool win = head == top;
+    const uint64_t with = __ballot(win);
+    if (__popcll(with) != kWave / LPT) {   // equal ones: the token's lowest lane
+      asm volatile("");   // (a branch: the selects of both ways cost more)
+      const uint32_t half = at & 32 ? static_cast<uint32_t>(with >> 32) : static_cast<uint32_t>(with);
+      win = lane == __builtin_ctz(half >> (at & 31));
     }
+    if (win) room[j] = uint2{k[0], static_cast<uint32_t>(p.id0 + static_cast<int>(kLow - (k[0] & kLow)))};
     pop<kList, V>(k, win, std::make_integer_sequence<int, kList - 1>{});
   }
   asm volatile("" ::: "memory");
@@ -524,15 +540,16 @@ MOE_DEV void picks_of_lanes(const GateP& g, const Place& p, int lane, const floa
   // neighbours in the order
   bool near = false;
   for (int j = lane; j < g.k; j += LPT) {
-    const uint32_t a = static_cast<uint32_t>(room[j]), b = static_cast<uint32_t>(room[j + 1]);
-    if (b == 0) continue;
+    const uint2 a = room[j], b = room[j + 1];
+    own[j] = a.x >= kNone ? static_cast<int>(a.y) : -1;
+    if (b.x < kNone) continue;
     if (g.bias) {
-      const float hi = value_of(a | kLow), lo = value_of(b | kLow);
+      const float hi = value_of(a.x | kLow), lo = value_of(b.x | kLow);
       const float big = fmaxf(fabsf(hi), fabsf(lo));
       // either key's low bits, of a 23-bit mantissa, and either's error
       near |= hi - lo <= static_cast<float>(V) * 0x1p-22f * big + 2.0f * score_error(g.sigmoid) * (1.0f + big);
     } else {
-      near |= (a ^ b) <= kLow;
+      near |= (a.x ^ b.x) <= kLow;
     }
   }
   if (!g.bias && __ballot(near)) {   // (equal leading bits decide if the others are zeros)
@@ -545,7 +562,7 @@ MOE_DEV void picks_of_lanes(const GateP& g, const Place& p, int lane, const floa
 }
 
 template <int LPT, int V, typename T>
-MOE_DEV void gate_token(const GateP& g, const T* row, const Place& p, int lane, int64_t t, const float (&x)[V], const float (&bias)[V],
+MOE_DEV void gate_token(const GateP& g, const T* row, const Place& p, int lane, int64_t t, bool kept, const float (&x)[V], const float (&bias)[V],
                         int* own, int* room, double* choice, Room64* room64, int* s_count) {
   // softmax: the largest logit, the exponentials and their sum
   float e[V] = {}, m = 0.0f, z = 1.0f;
@@ -566,18 +583,18 @@ MOE_DEV void gate_token(const GateP& g, const T* row, const Place& p, int lane, 
   bool open = false;
   choices32<LPT, V>(g, p, lane, x, bias, e, m, z > 0.0f ? 1.0f / z : 0.0f, c, open);
   if constexpr (LPT == kWave) picks_of_wave<V>(g, p, lane, c, room, own, open);
-  else picks_of_lanes<LPT, V>(g, p, lane, c, room, own, open);
+  else picks_of_lanes<LPT, V>(g, p, lane, c, reinterpret_cast<uint2*>(room), own, open);
   asm volatile("" ::: "memory");
   __builtin_amdgcn_wave_barrier();
   // the tokens left open, one after the other
-  for (uint64_t left = __ballot(open); left;) {
+  for (uint64_t left = __ballot(open && kept); left;) {
     const int first = __builtin_ctzll(left) & ~(LPT - 1);   // the token's first lane
     left &= ~((LPT == kWave ? ~uint64_t{0} : (uint64_t{1} << (LPT & 63)) - 1) << first);
     const int64_t token = __builtin_amdgcn_readlane(static_cast<int>(t), first);
-    picks64<(LPT * V + kWave - 1) / kWave, T>(g, static_cast<const T*>(g.logits) + token * g.ld, !g.mask || g.mask[token] != 0, choice, room64,
+    picks64<(LPT * V + kWave - 1) / kWave, T>(g, static_cast<const T*>(g.logits) + token * g.ld, choice, room64,
                                               own - (threadIdx.x & (kWave - 1)) / LPT * kMaxTopK + first / LPT * kMaxTopK);
   }
-  const int id = lane < g.k ? own[lane] : -1;
+  const int id = kept && lane < g.k ? own[lane] : -1;
   const bool live = id >= 0;
   const float xi = live ? logit_of(row[id]) : neg_inf();
   float w;
@@ -592,12 +609,13 @@ MOE_DEV void gate_token(const GateP& g, const T* row, const Place& p, int lane, 
 
 // Workgroups of kThreads, or larger ones where these leave no CU free: what a
 // workgroup counts goes to counts in one pass.
-constexpr int gate_threads(int V) { return V > 8 ? 2 * kThreads : 4 * kThreads; }
+constexpr int gate_threads(int V) { return V > 16 ? 2 * kThreads : 4 * kThreads; }
 
 template <int LPT, int V, typename T>
 __global__ __launch_bounds__(gate_threads(V)) void gate_kernel(const GateP g) {
   constexpr int kTokens = gate_threads(V) / LPT, kWaves = gate_threads(V) / kWave, kWide = (LPT * V + kWave - 1) / kWave;
-  __shared__ int s_id[kTokens][kMaxTopK], s_room[kTokens][LPT == kWave ? 32 : 16];
+  __shared__ int s_id[kTokens][kMaxTopK];
+  __shared__ __attribute__((aligned(8))) int s_room[kTokens][32];
   __shared__ int s_count[kMaxExperts];
   __shared__ double s_choice[kWaves][kWave * kWide];
   __shared__ Room64 s_room64[kWaves];
@@ -611,19 +629,24 @@ __global__ __launch_bounds__(gate_threads(V)) void gate_kernel(const GateP g) {
   const bool kept = t < g.T && (!g.mask || g.mask[tl] != 0);
   float x[V], bias[V] = {};
   if (g.bias) load_row<V>(g.bias, g.l.vec_bias, p, bias);
-  load_logits<V>(row, g.l, p, kept, x);
+  load_logits<V>(row, g.l, p, x);
   if (g.counts) {
     for (int e = threadIdx.x; e < g.l.E; e += threads) s_count[e] = 0;
     __syncthreads();
   }
   // (all lanes of a wave stay: a token's exact choice is made by all of them)
   if (__ballot(t < g.T))
-    gate_token<LPT, V, T>(g, row, p, lane, t, x, bias, s_id[in_wg], s_room[in_wg], s_choice[threadIdx.x / kWave],
+    gate_token<LPT, V, T>(g, row, p, lane, t, kept, x, bias, s_id[in_wg], s_room[in_wg], s_choice[threadIdx.x / kWave],
                           s_room64 + threadIdx.x / kWave, s_count);
   if (g.counts) {
     __syncthreads();
-    for (int e = threadIdx.x; e < g.l.E; e += threads)
+    // (each from a place of its own: 512 workgroups that all begin with the same
+    // line take 5 us)
+    int e = (threadIdx.x + blockIdx.x * kWave) % g.l.E;
+    for (int i = threadIdx.x; i < g.l.E; i += threads) {
       if (s_count[e]) atomicAdd(g.counts + e, s_count[e]);
+      e = (e + threads) % g.l.E;
+    }
   }
 }
 
@@ -659,7 +682,7 @@ __global__ __launch_bounds__(kThreads) void gate_bwd_kernel(const GateBwdP g) {
   float x[V];
   float term, dot = 0.0f;
   if (full) {
-    load_logits<V>(row, g.l, p, true, x);
+    load_logits<V>(row, g.l, p, x);
     float m = neg_inf();
 #pragma unroll
     for (int i = 0; i < V; ++i) m = fmaxf(m, x[i]);
@@ -749,6 +772,7 @@ int shape_for(int E, int n_groups, bool wave, Layout* l) {
     l->lgPw = 0;
     while (1 << l->lgPw < kWave / g2) ++l->lgPw;
     l->Ww = (l->Eg + kWave / g2 - 1) / (kWave / g2);
+    l->full = l->Eg == l->P * kShapes[i].values && n_groups == g2;
     if (l->W <= kShapes[i].values) return i;
   }
   return -1;
