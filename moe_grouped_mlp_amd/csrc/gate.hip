@@ -72,6 +72,30 @@ MOE_DEV void load_row(const T* row, bool vec, const Place& p, float (&x)[V]) {
     for (int i = 0; i < V; ++i) x[i] = logit_of(row[static_cast<uint32_t>(i < p.n ? p.id0 + i : 0)]);
   }
 }
+// The lane's own values of a row.  (vec: n is a multiple of N; the LDS rows are
+// made of whole vectors.)
+template <int V, typename T>
+MOE_DEV void store_row(T* row, bool vec, const Place& p, const float (&x)[V]) {
+  constexpr int N = vec_of(V);
+  auto put = [](float f) {
+    if constexpr (std::is_same_v<T, float>) return f;
+    else return static_cast<T>(pack_bf16x2(f, 0.0f));
+  };
+  if (vec) {
+    typedef T Vec __attribute__((ext_vector_type(N)));
+#pragma unroll
+    for (int i = 0; i < V; i += N) {
+      Vec f;
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[j] = put(x[i + j]);
+      if (i < p.n) *reinterpret_cast<Vec*>(row + p.id0 + i) = f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < p.n) row[p.id0 + i] = put(x[i]);
+  }
+}
 // The lane's logits; slots without an expert and ruled-out ones are -infinity.
 template <int V, typename T>
 MOE_DEV void load_logits(const T* row, const Layout& l, const Place& p, float (&x)[V]) {
@@ -662,6 +686,7 @@ struct GateBwdP {
   uint8_t sigmoid, renorm, accumulate, vec_d;
 };
 
+// A wave for a token from 65 experts on (16384 x 256: 8.5 us, with 16 lanes 10.9).
 // Rows go out through LDS of their own, where the picks' terms are added to
 // them.
 template <int LPT, int V, typename T>
@@ -674,12 +699,12 @@ __global__ __launch_bounds__(kThreads) void gate_bwd_kernel(const GateBwdP g) {
   const T* row = static_cast<const T*>(g.logits) + t * g.ld;
   const Place p = place_of(g.l, lane);
   const bool full = !g.sigmoid && !g.renorm;   // every logit has a gradient
-  int id = lane < g.k ? g.idx[t * g.k + lane] : -1;
+  // (loads not behind conditions: a lane without a pick has the first one's)
+  const int64_t slot = t * g.k + (lane < g.k ? lane : 0);
+  const int id = lane < g.k ? g.idx[slot] : -1;
+  const float dp = g.dprobs[slot];
   bool live = id >= 0 && id < g.E;
-  float xi = live ? logit_of(row[id]) : neg_inf();
-  live = live && xi > neg_inf();
-  const float d = live ? g.scale * g.dprobs[t * g.k + lane] : 0.0f;
-  float x[V];
+  float x[V] = {};
   float term, dot = 0.0f;
   if (full) {
     load_logits<V>(row, g.l, p, x);
@@ -695,34 +720,47 @@ __global__ __launch_bounds__(kThreads) void gate_bwd_kernel(const GateBwdP g) {
     }
     z = sum_lanes<LPT>(z);
     const float r = z > 0.0f ? 1.0f / z : 0.0f;
-    term = live ? expf(below(xi, m)) * r * d : 0.0f;
+    store_row<V>(own, true, p, x);   // the picks' scores come from there
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();   // LDS operations of one wave complete in order
+    // (a ruled-out pick's is 0, and its gradient too, whatever its dprobs is)
+    const float e = live ? own[id] : 0.0f;
+    live = e > 0.0f;
+    term = live ? e * r * (g.scale * dp) : 0.0f;
     dot = sum_lanes<LPT>(term) * r;
-  } else if (g.renorm) {
-    const float w = renormed(g.sigmoid, live, xi);
-    const float mean = sum_lanes<LPT>(w * d);
-    term = live ? w * (d - mean) : 0.0f;
-    if (g.sigmoid) term *= sigmoid_of(-xi);
-  } else {
-    const float e = expf(-fabsf(xi));   // s (1 - s), either sign
-    term = live ? d * (e / ((1.0f + e) * (1.0f + e))) : 0.0f;
-  }
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (i < p.n) own[p.id0 + i] = full ? -x[i] * dot : 0.0f;
+    for (int i = 0; i < V; ++i) x[i] *= -dot;
+  } else {
+    const float xi = live ? logit_of(row[id]) : neg_inf();
+    live = live && xi > neg_inf();
+    const float d = live ? g.scale * dp : 0.0f;
+    if (g.renorm) {
+      const float w = renormed(g.sigmoid, live, xi);
+      const float mean = sum_lanes<LPT>(w * d);
+      term = live ? w * (d - mean) : 0.0f;
+      if (g.sigmoid) term *= sigmoid_of(-xi);
+    } else {
+      const float e = expf(-fabsf(xi));   // s (1 - s), either sign
+      term = live ? d * (e / ((1.0f + e) * (1.0f + e))) : 0.0f;
+    }
+  }
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_wave_barrier();   // LDS operations of one wave complete in order
+  __builtin_amdgcn_wave_barrier();
+  store_row<V>(own, true, p, x);
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
   if (live) atomicAdd(own + id, term);
   asm volatile("" ::: "memory");
   __builtin_amdgcn_wave_barrier();
   T* out = static_cast<T*>(g.dlogits) + t * g.ld_d;
+  load_row<V>(own, true, p, x);
+  if (g.accumulate) {
+    float before[V];
+    load_row<V>(out, g.vec_d, p, before);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (i >= p.n) continue;
-    float v = own[p.id0 + i];
-    if (g.accumulate) v += logit_of(out[p.id0 + i]);
-    if constexpr (std::is_same_v<T, float>) out[p.id0 + i] = v;
-    else out[p.id0 + i] = static_cast<bf16_t>(pack_bf16x2(v, 0.0f));
+    for (int i = 0; i < V; ++i) x[i] += before[i];
   }
+  store_row<V>(out, g.vec_d, p, x);
 }
 
 constexpr int kBiasThreads = 1024;
