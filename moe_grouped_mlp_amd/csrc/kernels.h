@@ -219,8 +219,8 @@ hipError_t launch_grad_scale(const GradList& l, const double* sumsq, float max_n
 
 // ---- AdamW ----------------------------------------------------------------------
 constexpr int kAdamList = 40;          // tensors of one launch (3.6 KB of arguments)
-constexpr int kAdamBlocks = 2048;      // workgroups of one launch at most
-constexpr int64_t kAdamChunk = 16384;  // elements a workgroup takes at a time
+constexpr int kAdamBlocks = 1 << 20;   // workgroups of one launch at most
+constexpr int64_t kAdamChunk = 4096;   // elements a workgroup takes at a time
 enum AdamFlags : int32_t { kAdamParam16 = 1, kAdamGrad16 = 2, kAdamVec = 4 };
 struct AdamEntry {
   void* param;
