@@ -48,6 +48,18 @@ weight_grads(accumulate=True) adds.  The products sum in fp32; fp8_sums=True
 lets the FP8 matrix instructions sum inside a block for the bf16 outputs, which
 keeps fewer bits at up to twice the rate.  No bias and no recompute path.
 
+With prec=PREC_INT8 the block serves: W8A8 on 8-bit integers with one scale for
+each token and each weight row.  forward() quantizes the routed rows and the
+activations (moe_quantize_int8) and multiplies with moe_grouped_gemm_int8;
+there is no backward.
+
+gate() is route_logits() for routers by scores (sigmoid or softmax, a balance
+bias, groups of experts, renormalised weights; moe_router_gate),
+gate_backward() the gradient of its logits from the dprobs of backward(), and
+update_bias() the balance bias's update from the picks that gate() counted.
+adamw_step() updates the weights from dw1 and dw2 (moe_adamw), clipped to a
+largest norm on the way, with states in fp32 or 8 bits.
+
 Around the experts, router_loss() gives the router's balance and z losses and
 per-expert counts, router_backward() the gradient of its logits from these
 and from the dprobs of backward(), and clip_grads() scales the weight
@@ -124,12 +136,18 @@ class ExpertBlock:
         # passes with every operand quantized by moe_quantize_mxfp4
         self.mx4 = prec == B.PREC_MXFP4
         self.fp8 = prec == B.PREC_FP8
+        # 8-bit integers: forward only
+        self.int8 = prec == B.PREC_INT8
+        # gate()'s buffers by number of experts and type (kept for captured graphs)
+        self._gate_bufs, self._gate_args, self._adamw = {}, None, None
         # router_loss()'s buffers and the streams they were used on, by shape
         self._router_bufs, self._router_captured = {}, set()
         self._ws_grad, self.grad_norm = {}, None
         self._dprobs_valid = False   # whether dprobs are of the rows last routed
         if self.fp8 and (recompute or unfused):
             raise ValueError("the FP8 layer has no recompute path, and always runs as separate passes")
+        if self.int8 and (recompute or unfused or wgrad):
+            raise ValueError("the 8-bit integer layer serves: it has no backward, and always runs as separate passes")
         if wgrad_type != B.TYPE_BF16 and not self.fp8:
             raise ValueError("fp32 weight gradients are of the FP8 layer (prec=PREC_FP8)")
         if fp8_sums and not self.fp8:
@@ -182,14 +200,19 @@ class ExpertBlock:
         self.yp = torch.empty(M, H, **bf)
         self.out = torch.empty(T, H, **bf)
         self.amax = torch.zeros(1, **f32)
-        self.dz = torch.empty(M, N1, **bf) if keep else None
-        self.dprobs_p = torch.zeros(M, **f32)
-        self.dxp = torch.empty(M, H, **bf)
-        self.dx = torch.empty(T, H, **bf)
-        self.dprobs = torch.zeros(T, k, **f32)
+        if self.int8:
+            self.dz = self.dprobs_p = self.dxp = self.dx = self.dprobs = None
+        else:
+            self.dz = torch.empty(M, N1, **bf) if keep else None
+            self.dprobs_p = torch.zeros(M, **f32)
+            self.dxp = torch.empty(M, H, **bf)
+            self.dx = torch.empty(T, H, **bf)
+            self.dprobs = torch.zeros(T, k, **f32)
         self.ws = torch.empty(
             max(1, max(B.moe_grouped_gemm_fp8_workspace_size(E, n, k, M, T)
                        for n, k in ((N1, H), (H, I), (I, H), (H, N1))) if self.fp8 else
+                max(B.moe_grouped_gemm_int8_workspace_size(E, n, k, M, T)
+                    for n, k in ((N1, H), (H, I))) if self.int8 else
                 B.moe_grouped_mlp_workspace_size(E, H, I, M, prec, self.act.act)),
             dtype=torch.uint8, device=dev)
         self.w1i = torch.empty(E, N1, H, **bf)
@@ -220,7 +243,12 @@ class ExpertBlock:
                 self.aT_q = self.aT_s = self.dzT_q = self.dzT_s = None
         elif not self.mx4 or keep:
             self.xp = torch.empty(M, H, **bf)
-            self.dyp = torch.empty(M, H, **bf)
+            self.dyp = None if self.int8 else torch.empty(M, H, **bf)
+        if self.int8:
+            i8 = dict(dtype=torch.int8, device=dev)
+            for name, shape in (("xp", (M, H)), ("a", (M, I)), ("w1", (E, N1, H)), ("w2", (E, H, I))):
+                setattr(self, name + "_qi", torch.empty(*shape, **i8))
+                setattr(self, name + "_si", torch.empty(*shape[:-1], **f32))
         if self.mx4:
             def fp4_pair(*shape):
                 n = 1
@@ -301,7 +329,11 @@ class ExpertBlock:
         else:
             self.w1i.copy_(w1)
         self.w2.copy_(w2)
-        if self.mx or self.mx4 or self.fp8:
+        self._adamw = None   # states and copies were of other weights
+        self._requantize()
+
+    def _requantize(self) -> None:
+        if self.mx or self.mx4 or self.fp8 or self.int8:
             self.quantize_weights()
 
     def quantize_weights(self, live_only: bool = False) -> None:
@@ -314,6 +346,11 @@ class ExpertBlock:
         step's GEMMs read none of their weights; their copies are left as
         they were)."""
         E, H, I, N1 = self.E, self.H, self.I, self.N1
+        if self.int8:   # every expert's rows, each with its own scale
+            for x, rows, cols, copy in ((self.w1i, E * N1, H, "w1"), (self.w2, E * H, I, "w2")):
+                B.moe_quantize_int8(rows=rows, cols=cols, x=x, q=getattr(self, copy + "_qi"),
+                                    s=getattr(self, copy + "_si"))
+            return
         if self.fp8:
             for x, rows, cols, copy, copy_t in ((self.w1i, N1, H, "w1", "w1t"),
                                                 (self.w2, H, I, "w2", "w2t")):
@@ -477,6 +514,8 @@ class ExpertBlock:
         self.route(expert_idx, probs, x)
         if self.fp8:
             self.experts_forward_fp8()
+        elif self.int8:
+            self.experts_forward_int8()
         elif self.unfused:
             self.experts_forward_unfused()
         else:
@@ -513,6 +552,8 @@ class ExpertBlock:
             self.release_z()
 
     def backward(self, dout, timing_events=None):
+        if self.int8:
+            raise RuntimeError("the 8-bit integer layer (prec=PREC_INT8) has no backward")
         self.gather(dout, self.dyp, *self._mx_dst("dyp"))
         if self.fp8:
             self.experts_backward_fp8()
@@ -660,6 +701,158 @@ class ExpertBlock:
                           dprobs_p=self.dprobs_p, act=self.act)
         self._quantize8("dz", self.dz, self.N1)
         self._gemm8(self.H, self.N1, "dz", "w1t", self.dxp)
+
+    # ------------------------------------------ 8-bit integer layer ----------
+    def _int8_product(self, name, weight, x, N, K, c):
+        q, sc = getattr(self, name + "_qi"), getattr(self, name + "_si")
+        B.moe_quantize_int8(rows=self.M_cap, cols=K, x=x, q=q, s=sc,
+                            row_end=self.padded_offsets[self.E:])
+        B.moe_grouped_gemm_int8(E=self.E, N=N, K=K, M_cap=self.M_cap, split_sizes=self.split_sizes,
+                                padded_offsets=self.padded_offsets, a=q, a_s=sc,
+                                b=getattr(self, weight + "_qi"), b_s=getattr(self, weight + "_si"),
+                                c=c, max_rows=self.T, cu_margin=self.cu_margin,
+                                err_flag=self.err_flag, workspace=self.ws)
+
+    def experts_forward_int8(self) -> None:
+        if self.bias1 is not None:
+            raise RuntimeError("the FC1 bias is applied by the fused path only")
+        self._int8_product("xp", "w1", self.xp, self.N1, self.H, self.z)
+        B.moe_glu_unfused(direction=0, E=self.E, I=self.I, M_cap=self.M_cap,
+                          split_sizes=self.split_sizes,
+                          padded_offsets=self.padded_offsets, probs_p=self.probs_p,
+                          z=self.z, a=self.a, amax=self.amax, act=self.act)
+        self._int8_product("a", "w2", self.a, self.H, self.I, self.yp)
+
+    # -------------------------------------------------- router by scores --
+    def gate(self, logits: torch.Tensor, x: Optional[torch.Tensor] = None, *,
+             score: int = B.SCORE_SOFTMAX, bias: Optional[torch.Tensor] = None,
+             n_groups: int = 1, topk_groups: int = 1, group_top: int = 1,
+             renorm: bool = False, scale: float = 1.0,
+             token_mask: Optional[torch.Tensor] = None, count: bool = False) -> None:
+        """The router's choice by scores (moe_router_gate) from logits
+        [T][E_total], fp32 or bf16, into self.expert_idx / self.probs, and the
+        routing metadata of the local experts (with x, its gather), as
+        route_logits() does for the softmax router.  count: the picks are added
+        to gate_counts (int32 [E_total], of this number of experts), which
+        update_bias() reads and clears.  Keeps references to its arguments for
+        gate_backward()."""
+        T, E_all = logits.shape
+        if T != self.T:
+            raise ValueError(f"logits must have {self.T} rows, one for each of the block's tokens")
+        dev = logits.device
+        if not hasattr(self, "expert_idx"):
+            self.expert_idx = torch.empty(T, self.k, dtype=torch.int32, device=dev)
+            self.probs = torch.empty(T, self.k, dtype=torch.float32, device=dev)
+        if E_all not in self._gate_bufs:
+            self._gate_bufs[E_all] = torch.zeros(E_all, dtype=torch.int32, device=dev)
+        self.gate_counts = self._gate_bufs[E_all]
+        self._gate_args = dict(T=T, E=E_all, k=self.k, logits=logits, expert_idx=self.expert_idx,
+                               score=score, renorm=renorm, scale=scale)
+        B.moe_router_gate(**self._gate_args, probs=self.probs, bias=bias, n_groups=n_groups,
+                          topk_groups=topk_groups, group_top=group_top, token_mask=token_mask,
+                          counts=self.gate_counts if count else None)
+        self.route(self.expert_idx, self.probs, x)
+
+    def gate_backward(self, dprobs: Optional[torch.Tensor] = None,
+                      dlogits: Optional[torch.Tensor] = None, accumulate: bool = False):
+        """Gradient of the logits given to gate() from that of the kept weights
+        (by default the dprobs of the backward() since the last route()).
+        dlogits: where to (of the logits' type and shape; its own buffer by
+        default); accumulate: added to what it holds, say the losses'."""
+        if self._gate_args is None:
+            raise RuntimeError("gate_backward() needs gate() first")
+        if dprobs is None and not self._dprobs_valid:
+            raise RuntimeError("gate_backward() needs the backward() of the rows last routed, or dprobs")
+        dprobs = self.dprobs if dprobs is None else dprobs
+        logits = self._gate_args["logits"]
+        if tuple(dprobs.shape) != (self.T, self.k):
+            raise ValueError(f"dprobs must be [{self.T}][{self.k}]")
+        if accumulate and dlogits is None:
+            raise ValueError("accumulate needs the dlogits to add to")
+        if dlogits is None:
+            key = (logits.shape[1], logits.dtype)
+            if key not in self._gate_bufs:
+                self._gate_bufs[key] = torch.empty_like(logits)
+            dlogits = self._gate_bufs[key]
+        elif dlogits.shape != logits.shape or dlogits.dtype != logits.dtype:
+            raise ValueError("dlogits must have the logits' shape and type")
+        B.moe_router_gate_bwd(**self._gate_args, dprobs=dprobs, dlogits=dlogits, accumulate=accumulate)
+        return dlogits
+
+    def update_bias(self, bias: torch.Tensor, rate: float) -> None:
+        """The balance bias [E_total] after a step, from the picks that
+        gate(count=True) counted since the last update (several processes: sum
+        gate_counts over them before); the counts are cleared."""
+        if self._gate_args is None:
+            raise RuntimeError("update_bias() needs gate(count=True) first")
+        B.moe_router_bias_update(E=self.gate_counts.numel(), counts=self.gate_counts, bias=bias,
+                                 rate=rate, reset=True)
+
+    # ------------------------------------------------------------ update --
+    def adamw_step(self, lr, *, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                   weight_decay: float = 0.0, max_norm: Optional[float] = None,
+                   state: int = B.STATE_F32, master: bool = True, stochastic: bool = False,
+                   seed: int = 0, capturable: bool = False, requantize: bool = True) -> None:
+        """One AdamW step of w1i and w2 from dw1 and dw2 (moe_adamw).  The first
+        call makes the states (state: fp32, or 8 bits with their roots rounded
+        stochastically if asked) and, with master, fp32 copies of the weights
+        that the steps are made on; load_weights() drops them.  max_norm: the
+        gradients count as if clip_grads(max_norm) had scaled them, without its
+        pass; a norm that is not finite makes no step (but counts as one) and
+        sets MOE_DEVERR_NONFINITE in err_flag.  capturable: the step number is
+        counted on the device and lr may be a tensor (fp32 [1]), so that a
+        captured graph goes on from replay to replay.  requantize: the copies
+        of the weights that the products read are made anew."""
+        if not self.wgrad:
+            raise RuntimeError("ExpertBlock was built without wgrad=True")
+        capturing = _capturing(self.w2)
+        if not capturable and (capturing or isinstance(lr, torch.Tensor)):
+            raise RuntimeError("a captured step, or a rate in a tensor, needs capturable=True")
+        params, grads = [self.w1i, self.w2], [self.dw1, self.dw2]
+        if self._adamw is None:
+            if capturing:
+                raise RuntimeError("the first adamw_step() makes the states: it cannot be captured")
+            self._adamw = self._adamw_states(params, state, master, capturable)
+            self.adamw_steps = 0   # (of steps that are not capturable)
+        st = self._adamw
+        if st["kind"] != (state, master, capturable):
+            raise ValueError("the states were made by steps of another kind (load_weights() drops them)")
+        kw = {}
+        if max_norm is not None:
+            if self.grad_norm is None:
+                self.grad_sumsq = torch.empty(1, dtype=torch.float64, device=self.dw1.device)
+                self.grad_norm = torch.empty(1, dtype=torch.float32, device=self.dw1.device)
+            need = B.moe_grad_workspace_size(len(grads))
+            if need not in self._ws_grad:
+                self._ws_grad[need] = torch.empty(need, dtype=torch.uint8, device=self.dw1.device)
+            B.moe_grad_sumsq(tensors=grads, sumsq=self.grad_sumsq, workspace=self._ws_grad[need])
+            kw = dict(sumsq=self.grad_sumsq, max_norm=max_norm, err_flag=self.err_flag)
+        if capturable:
+            st["step"].add_(1)
+            kw["step_dev"] = st["step"]
+            if isinstance(lr, torch.Tensor):
+                kw["lr_dev"], lr = lr, 0.0
+        else:
+            self.adamw_steps += 1
+        B.moe_adamw(params=params, grads=grads, m=st["m"], v=st["v"], master=st["master"],
+                    m_scale=st["m_scale"], v_scale=st["v_scale"], lr=lr, step=max(1, self.adamw_steps),
+                    beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
+                    stochastic=stochastic, seed=seed, **kw)
+        if requantize:
+            self._requantize()
+
+    def _adamw_states(self, params, state, master, capturable):
+        dev = self.w2.device
+        if state == B.STATE_FP8:
+            made = lambda p: torch.zeros(p.numel(), dtype=torch.uint8, device=dev)
+            scales = lambda: [torch.zeros(-(-p.numel() // B.FP8_BLOCK), dtype=torch.float32, device=dev) for p in params]
+        else:
+            made = lambda p: torch.zeros(p.numel(), dtype=torch.float32, device=dev)
+            scales = lambda: None
+        return dict(kind=(state, master, capturable), m=[made(p) for p in params], v=[made(p) for p in params],
+                    m_scale=scales(), v_scale=scales(),
+                    master=[p.float().view(-1) for p in params] if master else None,
+                    step=torch.zeros(1, dtype=torch.int32, device=dev))
 
     # ------------------------------------------------- around the experts --
     def router_loss(self, logits: torch.Tensor, *, balance_coef: float = 0.0,
