@@ -1190,8 +1190,9 @@ moe_status moe_quantize_int8(const moe_quant_int8_args* args, void* stream);
  *   fp32, scaled there and rounded once to the output type.
  *   a [M_cap][K], a_s [M_cap]; per expert b [N][K] and b_s [N] (b_stride
  *   bytes and b_s_stride floats apart, 0: N * K and N).  c, ldc, c_type,
- *   max_rows, cu_margin, workspace, group starts and inconsistent offsets
- *   as in moe_grouped_gemm_fp8; results do not depend on whether K is cut.
+ *   max_rows, cu_margin, workspace (with it the last round of tiles may be
+ *   cut along K), group starts and inconsistent offsets as in
+ *   moe_grouped_gemm_fp8; results do not depend on whether K is cut.
  *   Needs N % 16 == 0, K % 16 == 0, E <= 1024, K <= 131056 (a sum of 131072
  *   products of -128 * -128 does not fit 32 bits); a, b and c 16-byte
  *   aligned (b_stride too). */

@@ -3,18 +3,43 @@
 //
 //   C[t][n] = a_s[t] b_s[n] sum_k a[t][k] w[n][k]
 //
+// Bound by power: the MFMAs are busy for 58% of the cycles at 1.9 .. 2.0 GHz.
+// With v_mfma_i32_32x32x32_i8, which reads its operands half as often, the same
+// took 6% fewer cycles at a clock 12% lower.
+//
 // The sums of v_mfma_i32_16x16x64_i8 are exact in 32 bits, so the accumulators
 // run through all of K and the scales come in once, as the tile is stored: the
 // K loop is loads and MFMAs alone.
 //
 // Tiles, stages and their order are the FP8 product's (fp8_gemm_kernel.h): 8
 // waves, up to 256 tokens x 256 weight rows, 128 bytes of K a stage, two stages
-// in LDS, fewer tokens where tiles are few, K cut where that still leaves CUs
-// idle (the parts are integers: their order does not matter).
+// in LDS, fewer tokens where tiles are few, K cut where tiles leave CUs idle (the
+// parts are integers: their order does not matter).
 #include "int8_gemm.h"
 
 namespace moe {
 namespace {
+
+// The last round of tiles, which leaves workgroups idle, is cut along K: its
+// tiles from `whole` on have `parts` parts, one for a workgroup.  Each costs its
+// sums' way out and back (256 KB, 0.09 us of the device's time), all of them the
+// second launch, so the best number is near sqrt(16 steps / tiles) (of four
+// steps each at least), and it has to save more steps than it costs.  16384 rows
+// over 8 experts x 4096 x 14336, 1104 tiles on 256 CUs: 800 us uncut, 767 with the
+// last 80 in 3 parts (2.51 PFLOP/s; a library's product of 16384 x 4096 x 14336 and
+// one scale for all: 2.52).
+struct Int8Cut {
+  int whole, parts;
+};
+MOE_DEV Int8Cut int8_cut(const Int8Args& g, int total) {
+  const int tail = total % g.grid;
+  if (!g.part || tail == 0) return {total, 1};
+  const int steps = (g.K + kInt8Blk - 1) / kInt8Blk, room = g.grid / tail;
+  int n = steps / 4 < room ? steps / 4 : room;
+  while (n > 1 && static_cast<int64_t>(n) * n * tail > 16 * static_cast<int64_t>(steps)) --n;
+  if (n > 1 && steps - steps / n >= 6 + tail * n / 16) return {total - tail, n};
+  return {total, 1};
+}
 
 template <int JMAX, bool F32>
 __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 2))) void int8_gemm_kernel(const Int8Args g) {
@@ -29,14 +54,16 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
   const int wave_s = __builtin_amdgcn_readfirstlane(wave);
   const int wn = wave & 1, wt = wave >> 1;
   const int total = fp8_tile_prefix<BT, false>(g, s_tab);
-  const int parts = fp8_parts(g, total, g.grid);
+  const Int8Cut cut = int8_cut(g, total);
+  const int items = cut.whole + (total - cut.whole) * cut.parts;
 
-  for (int item = fp8_workgroup(g); item < total * parts; item += g.grid) {
-    const Fp8Tile tile = fp8_tile_at<BT, false>(g, s_tab, item / parts);
+  for (int item = fp8_workgroup(g); item < items; item += g.grid) {
+    const int q = item - cut.whole, parts = q < 0 ? 1 : cut.parts;
+    const Fp8Tile tile = fp8_tile_at<BT, false>(g, s_tab, q < 0 ? item : cut.whole + q / parts);
     const int e = tile.e, start = tile.start, rows_t = tile.rows_t, t0 = tile.t0, n0 = tile.n0;
     // the steps [k0, k1) of this part
     const int all_steps = (g.K + kInt8Blk - 1) / kInt8Blk;
-    const int part = item % parts;
+    const int part = q < 0 ? 0 : q % parts;
     const int k0 = parts > 1 ? static_cast<int>(static_cast<int64_t>(all_steps) * part / parts) : 0;
     const int k1 = parts > 1 ? static_cast<int>(static_cast<int64_t>(all_steps) * (part + 1) / parts) : all_steps;
 
@@ -158,7 +185,7 @@ __global__ __launch_bounds__(kFp8Threads) __attribute__((amdgpu_waves_per_eu(2, 
       }
 
       if (parts > 1) {   // the accumulators as they are, for int8_join_kernel
-        i32x4* out = reinterpret_cast<i32x4*>(g.part) + static_cast<int64_t>(item) * kFp8PartFloats / 4 + tid;
+        i32x4* out = reinterpret_cast<i32x4*>(g.part) + static_cast<int64_t>(q) * kFp8PartFloats / 4 + tid;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -271,10 +298,10 @@ __global__ __launch_bounds__(kFp8Threads) void int8_join_kernel(const Int8Args g
   constexpr int BT = 64 * JMAX, kStep = F32 ? 1 : 2;
   __shared__ Fp8Tables s_tab;
   const int total = fp8_tile_prefix<BT, false>(g, s_tab);
-  const int parts = fp8_parts(g, total, g.grid);
-  const int item = blockIdx.x;
-  if (parts == 1 || item >= total * parts) return;
-  const Fp8Tile tile = fp8_tile_at<BT, false>(g, s_tab, item / parts);
+  const Int8Cut cut = int8_cut(g, total);
+  const int parts = cut.parts, item = blockIdx.x;
+  if (parts == 1 || item >= (total - cut.whole) * parts) return;
+  const Fp8Tile tile = fp8_tile_at<BT, false>(g, s_tab, cut.whole + item / parts);
   const int J = fp8_tile_groups<JMAX>(tile.rows_t - tile.t0);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wn = wave & 1, wt = wave >> 1, l16 = lane & 15, g4 = lane >> 4;
