@@ -194,6 +194,30 @@ def test_many_tiles():
             _check_product(ops, sizes, starts, out)
 
 
+@pytest.mark.parametrize("rows,N,K,out", [(4352, 4096, 4112, torch.bfloat16), (4400, 4096, 4112, torch.float32), (8000, 2304, 4128, torch.bfloat16)])
+def test_last_round_cut_along_k(rows, N, K, out):
+    """More tiles than CUs, and a last round of a few, which are cut."""
+    g = torch.Generator(DEV).manual_seed(rows)
+    sizes = [rows - 300, 0, 300]
+    starts = _starts(sizes)
+    a = torch.randint(-127, 128, (starts[-1], K), generator=g, device=DEV, dtype=torch.int8)
+    b = torch.randint(-127, 128, (3, N, K), generator=g, device=DEV, dtype=torch.int8)
+    a_s, b_s = torch.rand(starts[-1], generator=g, device=DEV), torch.rand(3, N, generator=g, device=DEV)
+    got = {}
+    need = mg.moe_grouped_gemm_int8_workspace_size(3, N, K, starts[-1])
+    assert need > 0
+    for ws in (None, torch.empty(need, dtype=torch.uint8, device=DEV)):
+        c = torch.full((starts[-1], N), -3.0, dtype=out, device=DEV)
+        mg.moe_grouped_gemm_int8(E=3, N=N, K=K, M_cap=starts[-1], split_sizes=_dev(np.array(sizes, np.int32)), padded_offsets=_dev(np.array(starts, np.int32)),
+                                 a=a, a_s=a_s, b=b, b_s=b_s, c=c, c_type=mg.TYPE_F32 if out == torch.float32 else mg.TYPE_BF16, workspace=ws)
+        for e, (n, o) in enumerate(zip(sizes, starts)):
+            s = (a[o:o + n].double() @ b[e].double().t().contiguous()).float()   # (sums below 2^53 are exact)
+            assert torch.equal(c[o:o + n], (s * a_s[o:o + n, None] * b_s[e][None, :]).to(out))
+            assert (c[o + n:starts[e + 1]] == -3.0).all()
+        got[ws is None] = c
+    assert torch.equal(got[True], got[False])
+
+
 def test_extremes_do_not_overflow():
     """The longest K with the largest codes, either sign."""
     K = 131056
