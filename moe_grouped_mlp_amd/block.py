@@ -139,7 +139,7 @@ class ExpertBlock:
         # 8-bit integers: forward only
         self.int8 = prec == B.PREC_INT8
         # gate()'s buffers by number of experts and type (kept for captured graphs)
-        self._gate_bufs, self._gate_args, self._adamw = {}, None, None
+        self._gate_bufs, self._gate_args, self._gate_routed, self._adamw = {}, None, False, None
         # router_loss()'s buffers and the streams they were used on, by shape
         self._router_bufs, self._router_captured = {}, set()
         self._ws_grad, self.grad_norm = {}, None
@@ -376,6 +376,7 @@ class ExpertBlock:
     def route(self, expert_idx: torch.Tensor, probs: torch.Tensor,
               x: Optional[torch.Tensor] = None) -> None:
         self._dprobs_valid = False
+        self._gate_routed = expert_idx is getattr(self, "expert_idx", None)
         flags = B.PERMUTE_BUILD_MAP
         xq, xs = self._mx_dst("xp")
         if x is not None:
@@ -411,6 +412,7 @@ class ExpertBlock:
         moe_router_topk followed by route() (four launches before the
         gather).  Both give the same bits."""
         T, E_all = logits.shape
+        self._gate_args = None   # (its picks go)
         if not hasattr(self, "expert_idx"):
             dev = logits.device
             self.expert_idx = torch.empty(T, self.k, dtype=torch.int32, device=dev)
@@ -740,6 +742,8 @@ class ExpertBlock:
         if T != self.T:
             raise ValueError(f"logits must have {self.T} rows, one for each of the block's tokens")
         dev = logits.device
+        if E_all not in self._gate_bufs and _capturing(logits):
+            raise RuntimeError("the first gate() of a number of experts makes its counters: it cannot be captured")
         if not hasattr(self, "expert_idx"):
             self.expert_idx = torch.empty(T, self.k, dtype=torch.int32, device=dev)
             self.probs = torch.empty(T, self.k, dtype=torch.float32, device=dev)
@@ -760,9 +764,9 @@ class ExpertBlock:
         dlogits: where to (of the logits' type and shape; its own buffer by
         default); accumulate: added to what it holds, say the losses'."""
         if self._gate_args is None:
-            raise RuntimeError("gate_backward() needs gate() first")
-        if dprobs is None and not self._dprobs_valid:
-            raise RuntimeError("gate_backward() needs the backward() of the rows last routed, or dprobs")
+            raise RuntimeError("gate_backward() needs gate() first, and no route_logits() since")
+        if dprobs is None and not (self._dprobs_valid and self._gate_routed):
+            raise RuntimeError("gate_backward() needs the backward() of gate()'s picks, the rows last routed, or dprobs")
         dprobs = self.dprobs if dprobs is None else dprobs
         logits = self._gate_args["logits"]
         if tuple(dprobs.shape) != (self.T, self.k):
@@ -783,7 +787,7 @@ class ExpertBlock:
         """The balance bias [E_total] after a step, from the picks that
         gate(count=True) counted since the last update (several processes: sum
         gate_counts over them before); the counts are cleared."""
-        if self._gate_args is None:
+        if not hasattr(self, "gate_counts"):
             raise RuntimeError("update_bias() needs gate(count=True) first")
         B.moe_router_bias_update(E=self.gate_counts.numel(), counts=self.gate_counts, bias=bias,
                                  rate=rate, reset=True)
