@@ -1021,7 +1021,8 @@ moe_status moe_grad_clip(const moe_grad_args* args, void* stream);
  *   moe_router_bias_update).
  *   Needs 0 <= T, 1 <= E <= 1024, 1 <= k <= min(8, experts of topk_groups
  *   groups), T * k < 2^31, n_groups 0 (none) to 64 and a divisor of E, 1 <=
- *   topk_groups <= n_groups, group_top 1 or 2; scale finite.
+ *   topk_groups <= n_groups, group_top 1 or 2; scale finite.  2^26 tokens and
+ *   more are MOE_ERR_UNSUPPORTED (in moe_router_gate_bwd too).
  * ---------------------------------------------------------------------- */
 typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 
@@ -1116,7 +1117,7 @@ moe_status moe_router_bias_update(const moe_bias_update_args* args, void* stream
  *   step counts from 1; step_dev (optional device int32 [1]) and lr_dev
  *   (optional device fp32 [1]) are read instead of step and lr, so that a
  *   captured graph can go on counting: the caller adds one to *step_dev
- *   before the call.
+ *   before the call (a number below 1 there counts as 1).
  *   tensors: host array, read before the call returns; numel >= 0; each
  *   tensor contiguous and aligned to its type (16-byte alignment of all of
  *   a tensor's buffers makes wide loads possible).  A buffer that overlaps

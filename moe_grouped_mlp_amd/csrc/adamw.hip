@@ -8,6 +8,12 @@
 // consecutive elements at a time, so 16 lanes hold a block of an 8-bit state
 // and its new scale is a maximum over them.  The clipping factor is applied to
 // the gradients as they are read.
+//
+// Bound by HBM: an element of a bf16 weight with an fp32 master, gradient and
+// states moves 30 bytes, one with 8-bit states and a bf16 gradient 10.1.  705 M
+// elements take 3.72 ms (5.7 TB/s) and 1.22 ms (5.8); a copy of as much reaches 5.5
+// .. 5.8, one that reads 4 arrays and writes 3 5.5.  12 small tensors take 8 us, 6 of
+// them the kernel's.
 #include <type_traits>
 
 #include "common.h"
@@ -398,9 +404,10 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamList l) {
     if (l.lr_dev) c.lr = *l.lr_dev;
     double c1 = l.c1;
     if (l.step_dev) {
-      step = static_cast<uint32_t>(*l.step_dev);
-      c1 = 1.0 - pow(l.b1_64, static_cast<double>(*l.step_dev));
-      c.rs_c2 = static_cast<float>(1.0 / sqrt(1.0 - pow(l.b2_64, static_cast<double>(*l.step_dev))));
+      const int n = *l.step_dev > 1 ? *l.step_dev : 1;
+      step = static_cast<uint32_t>(n);
+      c1 = 1.0 - pow(l.b1_64, static_cast<double>(n));
+      c.rs_c2 = static_cast<float>(1.0 / sqrt(1.0 - pow(l.b2_64, static_cast<double>(n))));
     }
     c.lr_c1 = static_cast<float>(static_cast<double>(c.lr) / c1);
   }

@@ -319,3 +319,14 @@ def test_refusals():
             mg.moe_adamw(**{**f, "lr": 0.1, **bad})
     with pytest.raises(OverflowError):
         mg.moe_adamw(**f, lr=0.1, seed=-1)
+
+
+@pytest.mark.parametrize("n", [0, -3])
+def test_a_step_below_one_counts_as_one(n):
+    s = _state([3000], False, master=True)
+    two = _copy(s)
+    for t, at in ((s, n), (two, 1)):
+        mg.moe_adamw(**t, lr=0.01, step_dev=torch.full((1,), at, dtype=torch.int32, device=DEV))
+    for k in s:
+        for a, b in zip(s[k] or [], two[k] or []):
+            assert torch.equal(a, b) and torch.isfinite(a.float()).all()

@@ -167,3 +167,8 @@ def test_workspace_sizes():
     assert m.moe_grouped_gemm_int8_workspace_size(2, 256, 8192, 512) > 0
     assert m.moe_grouped_gemm_int8_workspace_size(2, 256, 8192, 512, max_rows=16) == 0
     assert m.moe_grouped_gemm_int8_workspace_size(0, 256, 8192, 512) == 0
+
+
+def test_more_tokens_than_a_launch_has_threads_for():
+    for name, make in (("moe_router_gate", gate), ("moe_router_gate_bwd", bwd)):
+        _refuses(name, make, [dict(T=1 << 26), dict(T=(1 << 27) - 1)], UNSUPPORTED)
