@@ -11,9 +11,10 @@
 //
 // Bound by HBM: an element of a bf16 weight with an fp32 master, gradient and
 // states moves 30 bytes, one with 8-bit states and a bf16 gradient 10.1.  705 M
-// elements take 3.72 ms (5.7 TB/s) and 1.22 ms (5.8); a copy of as much reaches 5.5
-// .. 5.8, one that reads 4 arrays and writes 3 5.5.  12 small tensors take 8 us, 6 of
-// them the kernel's.
+// elements take 3.72 ms (5.7 TB/s) and 1.22 ms (5.8; roots, codes and random bits
+// keep the vector units busy for all of that time too); a copy of as much reaches
+// 5.5 .. 5.8, one that reads 4 arrays and writes 3 5.5.  12 small tensors take 8 us,
+// 6 of them the kernel's.
 #include <type_traits>
 
 #include "common.h"

@@ -10,12 +10,13 @@
 // ids, all in registers (V is what they hold), so a token's logits are read once
 // and an equal choice of a lower id is one of a lower lane or slot.
 //
-// Few tokens wait for a launch and its code; many are bound by the instructions
-// of the choice, not by their bytes.  16 tokens of 256 experts in 8 groups take
-// 5.2 us, 16384 of them 16.2 (17.8 MB: 3.2 at the rate of a copy) and 16384 of 128
-// experts without groups 9.3.  Without the counts and the tokens that fp32 leaves
-// open the second would take 9.9.  All choices in 64 bits took 127, 32 bits and a
-// search for the largest in a whole wave 27 .. 36.
+// Few tokens wait for a launch and its code, many for the steps of the choice,
+// each of which needs the one before; their bytes take less.  16 tokens of 256
+// experts in 8 groups take 5.3 us, 16384 of them 16.5 (17.8 MB: 3.2 at the rate of
+// a copy) and 16384 of 128 experts without groups 9.3.  The second would take 9.9
+// without the counts and without the tokens that fp32 leaves open, some 30, for
+// which a wave each goes on alone.  All choices in 64 bits took 127, 32 bits and a
+// search for the largest by a whole wave 27 .. 36.
 #include <type_traits>
 #include <utility>
 

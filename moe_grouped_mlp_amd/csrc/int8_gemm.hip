@@ -3,7 +3,7 @@
 //
 //   C[t][n] = a_s[t] b_s[n] sum_k a[t][k] w[n][k]
 //
-// Bound by power: the MFMAs are busy for 58% of the cycles at 1.9 .. 2.0 GHz.
+// Bound by power: the MFMAs are busy for 67% of the cycles at 1.8 GHz.
 // With v_mfma_i32_32x32x32_i8, which reads its operands half as often, the same
 // took 6% fewer cycles at a clock 12% lower.
 //
@@ -26,8 +26,8 @@ namespace {
 // second launch, so the best number is near sqrt(16 steps / tiles) (of four
 // steps each at least), and it has to save more steps than it costs.  16384 rows
 // over 8 experts x 4096 x 14336, 1104 tiles on 256 CUs: 800 us uncut, 767 with the
-// last 80 in 3 parts (2.51 PFLOP/s; a library's product of 16384 x 4096 x 14336 and
-// one scale for all: 2.52).
+// last 80 in 3 parts (755 .. 790 over runs, 2.44 .. 2.55 PFLOP/s; a library's product
+// of 16384 x 4096 x 14336 and one scale for all: 2.52).
 struct Int8Cut {
   int whole, parts;
 };

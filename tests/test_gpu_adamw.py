@@ -8,6 +8,8 @@ own; the decayed weight 2, a bf16 weight one more (2^-8).  8-bit states: their
 values are within half a step (to nearest) or one step (stochastic) of the
 exact state on the grid of the block's scale."""
 
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -16,6 +18,15 @@ import moe_grouped_mlp_amd as mg
 from oracle import layer as ol
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _give_back():
+    """Tests after these measure what torch's allocator holds."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
+
 
 DEV = "cuda"
 F8, BF, F32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32

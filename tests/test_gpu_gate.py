@@ -10,6 +10,8 @@ the value, and 2^-140 where it leaves the normal range.  Gradients are sums of
 such products: the same of the sum of their magnitudes; bf16 ones are rounded
 once more (2^-8)."""
 
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -18,6 +20,15 @@ import moe_grouped_mlp_amd as mg
 from oracle import layer as ol
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _give_back():
+    """Tests after these measure what torch's allocator holds."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
+
 
 DEV = "cuda"
 INF = float("inf")

@@ -3,6 +3,8 @@
 right value each, and a product's result is two fp32 multiplications of it and
 one rounding: everything is compared bit for bit."""
 
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -11,6 +13,15 @@ import moe_grouped_mlp_amd as mg
 from oracle import layer as ol
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _give_back():
+    """Tests after these measure what torch's allocator holds."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
+
 
 DEV = "cuda"
 

@@ -6,6 +6,8 @@ Tolerances: integer products bit for bit; the activation against float64 with
 its own two roundings (fp32 evaluation, 2^-16 of it for the fast exponential and
 reciprocal, then bf16, 2^-8); weights after a step as in test_gpu_adamw."""
 
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -17,6 +19,15 @@ from .test_gpu_adamw import U
 from .test_gpu_fp8_block import _host, _inputs
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _give_back():
+    """Tests after these measure what torch's allocator holds."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
+
 
 DEV = "cuda"
 GATE = dict(score=mg.SCORE_SIGMOID, n_groups=4, topk_groups=2, group_top=2, renorm=True, scale=2.5)
