@@ -747,7 +747,8 @@ def moe_adamw(*, params, grads, m, v, lr, step=1, beta1=0.9, beta2=0.999, eps=1e
     """One AdamW step over lists of tensors.  m and v float32, or (with m_scale
     and v_scale) 8-bit codes of m and of v's root; master: None, or a list of fp32
     copies of bf16 parameters with None where there is none; weight_decay: one
-    number or a list; sumsq (moe_grad_sumsq's) clips the gradients to max_norm."""
+    number or a list; sumsq (moe_grad_sumsq's) clips the gradients to max_norm,
+    which has no meaning without it."""
     d = _device()
     _call.adamw(d, params, grads, m, v, master, m_scale, v_scale, weight_decay, lr, beta1, beta2,
                 eps, step, max_norm, stochastic, seed, sumsq, step_dev, lr_dev, err_flag, stream)
