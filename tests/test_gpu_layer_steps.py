@@ -227,3 +227,75 @@ def test_refusals():
         blk.adamw_step(0.1, state=mg.STATE_FP8)
     with pytest.raises(RuntimeError):
         mg.ExpertBlock(8, 128, 64, 16, 2).adamw_step(0.1)
+
+
+def test_shards_of_the_experts_add_up():
+    """Two blocks with half of the experts each, fed the same logits; every output
+    is off by one rounding, and the sums by fp32's."""
+    E, k, T, H, I = 16, 4, 50, 256, 128
+    x, _, w1, w2, logits = _inputs(E, H, 2 * I, I, T, 8)
+    outs, mags = [], []
+    for first, n in ((0, E), (0, E // 2), (E // 2, E // 2)):
+        blk = mg.ExpertBlock(n, H, I, T, k, prec=mg.PREC_INT8, first_expert=first)
+        blk.load_weights(w1[first:first + n].contiguous(), w2[first:first + n].contiguous())
+        blk.gate(logits, count=True, **GATE)
+        outs.append(_host(blk.forward(x, blk.expert_idx, blk.probs)))
+        yp, rid = _host(blk.yp), blk.row_id_map.cpu().numpy()
+        mags.append(np.stack([sum((np.abs(yp[r]) for r in rid[t] if r >= 0), np.zeros(H)) for t in range(T)]))
+        assert int(blk.gate_counts.sum()) == T * k and blk.err_flag.item() == 0   # (of all experts)
+    tol = 2.0 ** -8 * sum(np.abs(o) + 16 * U * m for o, m in zip(outs, mags)) + 16 * U * sum(mags)
+    assert np.abs(outs[0]).max() > 0 and (np.abs(outs[0] - outs[1] - outs[2]) <= tol).all()
+
+
+def test_captured_serving_step():
+    """Router and layer in a graph, replayed with other tokens: as eager calls."""
+    E, k, T, H, I = 8, 2, 6, 256, 128
+    x, _, w1, w2, logits = _inputs(E, H, 2 * I, I, T, 9)
+    blocks = [mg.ExpertBlock(E, H, I, T, k, prec=mg.PREC_INT8) for _ in range(2)]
+    mask = torch.ones(T, dtype=torch.uint8, device=DEV)
+
+    def step(blk):
+        blk.gate(logits, token_mask=mask, count=True, **GATE)
+        return blk.forward(x, blk.expert_idx, blk.probs)
+
+    for blk in blocks:
+        blk.load_weights(w1, w2)
+        step(blk)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(blocks[0])
+    for i in range(4):
+        x.copy_(torch.randn(T, H, device=DEV))
+        logits.copy_(torch.randn(T, E, device=DEV))
+        mask.fill_(1)
+        mask[i:i + 2] = 0
+        graph.replay()
+        want = step(blocks[1])
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and not out[i:i + 2].any() and out[(i + 3) % T].any()
+        assert torch.equal(blocks[0].gate_counts, blocks[1].gate_counts)
+
+
+def test_two_layers_on_two_streams_at_once():
+    """Nothing is shared between calls: layers that run side by side give what
+    each gives alone."""
+    E, k, T, H, I = 8, 2, 700, 512, 512
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sets, alone = [], []
+    for seed in (10, 11):
+        x, _, w1, w2, logits = _inputs(E, H, 2 * I, I, T, seed)
+        blk = mg.ExpertBlock(E, H, I, T, k, prec=mg.PREC_INT8)
+        blk.load_weights(w1, w2)
+        sets.append((blk, x, logits))
+        blk.gate(logits, **GATE)
+        alone.append(blk.forward(x, blk.expert_idx, blk.probs).clone())
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(10):
+        for i, (blk, x, logits) in enumerate(sets):
+            with torch.cuda.stream(streams[i]):
+                blk.gate(logits, **GATE)
+                got[i] = blk.forward(x, blk.expert_idx, blk.probs)
+    torch.cuda.synchronize()
+    for a, b in zip(got, alone):
+        assert torch.equal(a, b)
