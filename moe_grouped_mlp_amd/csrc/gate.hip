@@ -13,9 +13,11 @@
 // Few tokens wait for a launch and its code, many for the steps of the choice,
 // each of which needs the one before; their bytes take less.  16 tokens of 256
 // experts in 8 groups take 5.3 us, 16384 of them 16.5 (17.8 MB: 3.2 at the rate of
-// a copy) and 16384 of 128 experts without groups 9.3.  The second would take 9.9
-// without the counts and without the tokens that fp32 leaves open, some 30, for
-// which a wave each goes on alone.  All choices in 64 bits took 127, 32 bits and a
+// a copy) and 16384 of 128 experts without groups 9.3.  The second would take 9.7
+// without the counts (every workgroup's atomics on the same lines, one after the
+// other) and without the tokens that fp32 leaves open, some 20, for which a wave
+// each goes on alone; with either it takes 15.5 .. 16.5, since the two overlap.  All
+// choices in 64 bits took 127, 32 bits and a
 // search for the largest by a whole wave 27 .. 36.
 #include <type_traits>
 #include <utility>
