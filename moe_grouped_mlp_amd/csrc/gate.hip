@@ -17,8 +17,8 @@
 // without the counts (every workgroup's atomics on the same lines, one after the
 // other) and without the tokens that fp32 leaves open, some 20, for which a wave
 // each goes on alone; with either it takes 15.5 .. 16.5, since the two overlap.  All
-// choices in 64 bits took 127, 32 bits and a
-// search for the largest by a whole wave 27 .. 36.
+// choices in 64 bits took 127, 32 bits and a search for the largest by a whole wave
+// 27 .. 36.
 #include <type_traits>
 #include <utility>
 
