@@ -1097,8 +1097,9 @@ moe_status moe_router_bias_update(const moe_bias_update_args* args, void* stream
  *     w = w - lr * weight_decay * w
  *           - lr * (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
  *   f = 1, or with sumsq (moe_grad_sumsq's) the clipping factor of
- *   moe_grad_clip, min(1, max_norm / (sqrt(*sumsq) + 1e-6)): gradients that
- *   are clipped here need no pass of their own.  If sqrt(*sumsq) is infinite
+ *   moe_grad_clip, min(1, max_norm / (sqrt(*sumsq) + 1e-6)), in fp64 and
+ *   rounded to fp32 once: gradients that are clipped here need no pass of
+ *   their own.  If sqrt(*sumsq) is infinite
  *   or NaN nothing is changed and MOE_DEVERR_NONFINITE is set.
  *   param bf16 or fp32; a bf16 one may have master, its fp32 copy: the step
  *   is then made on master, and param is written from it (it is not read).
@@ -1146,7 +1147,7 @@ typedef struct moe_adamw_args {
   int32_t state_type;          /* moe_state */
   double lr, beta1, beta2, eps;   /* double: 1 - 0.999f is off by 5e-5 */
   int32_t step;
-  float max_norm;
+  double max_norm;             /* double: f is rounded once */
   const double* sumsq;         /* optional device */
   const int32_t* step_dev;     /* optional device */
   const float* lr_dev;         /* optional device */

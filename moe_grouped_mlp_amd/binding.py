@@ -270,7 +270,7 @@ class AdamwArgs(ctypes.Structure):
     _fields_ = [("tensors", ctypes.POINTER(AdamwTensor)), ("n_tensors", c_int32),
                 ("state_type", c_int32), ("lr", c_double), ("beta1", c_double),
                 ("beta2", c_double), ("eps", c_double), ("step", c_int32),
-                ("max_norm", c_float), ("sumsq", c_void_p), ("step_dev", c_void_p),
+                ("max_norm", c_double), ("sumsq", c_void_p), ("step_dev", c_void_p),
                 ("lr_dev", c_void_p), ("err_flag", c_void_p), ("stochastic", c_int32),
                 ("seed", c_uint32)]
 

@@ -418,7 +418,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamList l) {
       if (blockIdx.x == 0 && threadIdx.x == 0) set_err(l.err, MOE_DEVERR_NONFINITE);
       return;
     }
-    const double f = static_cast<double>(l.max_norm) / (norm + 1e-6);
+    const double f = l.max_norm / (norm + 1e-6);
     c.f = f < 1.0 ? static_cast<float>(f) : 1.0f;
   }
   const uint32_t key0 = STOCHASTIC ? mix32(l.seed + step * 0x9e3779b9u) : 0;

@@ -242,7 +242,8 @@ struct AdamList {
   int64_t chunks;
   float lr, lr_c1, rs_c2;  // lr, lr / (1 - beta1^step), 1 / sqrt(1 - beta2^step)
   float b1, a1, b2, a2;    // beta and 1 - beta
-  float eps, max_norm;
+  float eps;
+  double max_norm;         // (in fp32 its rounding moves one clipping factor in seven by a step, and 8-bit codes with it)
   double c1, b1_64, b2_64; // 1 - beta1^step; for steps counted on the device
   const double* sumsq;
   const int32_t* step_dev;

@@ -553,7 +553,7 @@ PyObject* adamw(PyObject*, PyObject* const* args, Py_ssize_t n_args) {
     a.beta2 = p.f64();
     a.eps = p.f64();
     a.step = p.i32();
-    a.max_norm = p.f32();
+    a.max_norm = p.f64();
     a.stochastic = p.truth();
     a.seed = p.u32();
     a.sumsq = p.buf<double>("sumsq", kF64, 1);
