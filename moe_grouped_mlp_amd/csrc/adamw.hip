@@ -184,7 +184,9 @@ MOE_DEV u32x2 encode_m(const Coding& k, const float (&m)[kPer]) {
 // Roots: to nearest, or up with the probability of what rounding down would
 // lose.  Times 2^-120 a value's upper bits are its code (E4M3's exponents,
 // subnormal ones too, are fp32's then) and the 20 below it the part to decide by,
-// so 16 random bits are added there.  i: of the first value (even).
+// so 16 random bits are added there.  (That power comes after the scale factor:
+// both in one would leave fp32's normal range for roots from 2.9e4 on.)  i: of the
+// first value (even).
 template <bool STOCHASTIC>
 MOE_DEV u32x2 encode_r(const Coding& k, uint32_t key, int64_t i, const float (&r)[kPer]) {
   // (a block with an infinity has the factor 0, and codes of zero: NaN all of it)
@@ -198,7 +200,6 @@ MOE_DEV u32x2 encode_r(const Coding& k, uint32_t key, int64_t i, const float (&r
     }
     return encode8(y);
   } else {
-    const float f = k.r * 0x1p-120f;
     u32x2 w = {0, 0};
     bool nan = false;
 #pragma unroll
@@ -206,9 +207,9 @@ MOE_DEV u32x2 encode_r(const Coding& k, uint32_t key, int64_t i, const float (&r
       const uint32_t h = mix32(key + static_cast<uint32_t>(i >> 1) + j / 2);
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        const float y = r[j + n] * f;
+        const float y = r[j + n] * k.r;
         nan |= y != y;
-        uint32_t u = __float_as_uint(y) + ((n ? h >> 16 : h & 0xffffu) << 4);
+        uint32_t u = __float_as_uint(y * 0x1p-120f) + ((n ? h >> 16 : h & 0xffffu) << 4);
         u = u < 0x07efffffu ? u : 0x07efffffu;                 // 448
         const uint32_t some = __float_as_uint(r[j + n]) < least ? __float_as_uint(r[j + n]) : least;
         u = u > some ? u : some;                               // not zero
@@ -219,7 +220,7 @@ MOE_DEV u32x2 encode_r(const Coding& k, uint32_t key, int64_t i, const float (&r
       asm volatile("");
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const float y = r[j] * f;
+        const float y = r[j] * k.r;
         if (y != y) w[j / 4] |= 0x7fu << (8 * (j % 4));
       }
     }

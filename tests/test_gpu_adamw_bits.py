@@ -96,3 +96,26 @@ def test_clipped_steps(stochastic, ptype, off):
         mg.moe_adamw(**s, **HYPER, **kw, sumsq=torch.full((1,), norm * norm, dtype=torch.float64, device=DEV), max_norm=max_norm)
         same(s, before, f=f, **kw)
     assert moved > 0   # (some limits are not those of their fp32 values)
+
+
+@pytest.mark.parametrize("stochastic", [False, True])
+@pytest.mark.parametrize("size", [1e-30, 1e-20, 1e-10, 1.0, 2e4, 4e4, 1e5, 1e9, 1e11, 1e12, 1e15, 1e18])
+def test_roots_of_every_size(stochastic, size):
+    """beta2 = 0: the root of v is the gradient's magnitude.  (That of the smallest
+    is zero: its square leaves fp32.)"""
+    n = 128 * 6 + 50
+    s = _state([n, n], True, F32, seed=13, first=True)
+    g = torch.Generator(DEV).manual_seed(3)
+    for i, wide in enumerate((0.5, 3.0)):   # the second's codes reach the subnormal ones and the least one
+        s["grads"][i].copy_(size * torch.exp(wide * torch.randn(n, generator=g, device=DEV)).clamp(max=10))
+        s["grads"][i][::7] *= -1
+        s["grads"][i][128:256:3] = 0
+    before = _copy(s)
+    kw = dict(step=3, stochastic=stochastic, seed=2, beta2=0.0)
+    mg.moe_adamw(**s, **{**HYPER, **kw})
+    same(s, before, **kw)
+    root = _f32(s["v"][0]) * _spread(_f32(s["v_scale"][0]), n)
+    want = np.abs(_f32(before["grads"][0])) if size > 1e-30 else np.zeros(n)
+    ok = want > size * 0.05   # (whose codes are normal ones: within a step, an eighth)
+    assert ok.sum() > n // 2 or size == 1e-30
+    assert (np.abs(root - want)[ok] <= 0.126 * want[ok]).all()
