@@ -19,6 +19,7 @@
 
 #include "common.h"
 #include "kernels.h"
+#include "root.h"
 
 namespace moe {
 namespace {
@@ -143,9 +144,8 @@ MOE_DEV float stepped(const Consts& c, float wd_lr, float m, float r, float w) {
   return __builtin_fmaf(-c.lr_c1, step, __builtin_fmaf(-wd_lr, w, w));
 }
 
-// Correctly rounded roots of values in [2^-96, inf): one Newton step from the
-// hardware's reciprocal root, with the residual in a fused multiply-add.  Others
-// (zeros, mostly) take the library's.
+// Correctly rounded roots: of values in [2^-96, inf) from the hardware's reciprocal
+// root, which is off by an ulp at most.  Others (zeros, mostly) take the library's.
 MOE_DEV void roots(const float (&v)[kPer], float (&r)[kPer]) {
   constexpr uint32_t kLo = 0x0f800000u, kSpan = 0x7f800000u - kLo;
   uint32_t out = 0;
@@ -153,8 +153,7 @@ MOE_DEV void roots(const float (&v)[kPer], float (&r)[kPer]) {
   for (int j = 0; j < kPer; ++j) {
     const uint32_t t = __float_as_uint(v[j]) - kLo;
     out = t > out ? t : out;
-    const float y = __builtin_amdgcn_rsqf(v[j]), s = v[j] * y;
-    r[j] = __builtin_fmaf(__builtin_fmaf(-s, s, v[j]), 0.5f * y, s);
+    r[j] = root_from(v[j], __builtin_amdgcn_rsqf(v[j]));
   }
   if (out >= kSpan) {
     asm volatile("");   // (a branch)

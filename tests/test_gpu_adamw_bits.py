@@ -119,3 +119,48 @@ def test_roots_of_every_size(stochastic, size):
     ok = want > size * 0.05   # (whose codes are normal ones: within a step, an eighth)
     assert ok.sum() > n // 2 or size == 1e-30
     assert (np.abs(root - want)[ok] <= 0.126 * want[ok]).all()
+
+
+@pytest.mark.parametrize("base,beta2", [(1.0, 0.5), (2.0, 0.25)])
+def test_roots_of_every_significand(base, beta2):
+    """One element of each block has a v in [1/2, 1) or [1, 2), so that the block's
+    scale shows its root (a quotient of which is rounded once more)."""
+    n, seen = 1 << 20, torch.zeros(1 << 23, dtype=torch.bool, device=DEV)
+    first = torch.arange(n, device=DEV) * 128
+    low = beta2 * base * base
+    grads, codes, zeros = (torch.zeros(128 * n, dtype=t, device=DEV) for t in (F32, torch.uint8, torch.uint8))
+    codes[first] = 0x38   # 1
+    for part in range(8):
+        k = torch.arange(part * n, (part + 1) * n, device=DEV, dtype=torch.float64)
+        d = (k * 2.0 ** -23 * low / (1 - beta2)).sqrt().float()
+        grads[first] = d
+        m, v, ms, vs = zeros.clone(), codes.clone(), torch.ones(n, device=DEV), torch.full((n,), base, device=DEV)
+        mg.moe_adamw(params=[torch.zeros(128 * n, dtype=BF, device=DEV)], grads=[grads], m=[m], v=[v], m_scale=[ms], v_scale=[vs], lr=0.0, beta1=0.0,
+                     beta2=beta2)
+        x = low + (1 - beta2) * d * d   # (fp32, each operation rounded)
+        assert torch.equal(vs, (x.double().sqrt().float().double() / 448).float())
+        seen[(x.view(torch.int32) & 0x7fffff).long()[x < 2 * low]] = True
+    assert seen.float().mean() > 0.6
+
+
+def test_root_of_the_significand_that_depends_on_the_hardware():
+    """v = 0x406e9372 times 4^k (a half of a scale's square): the one root that an
+    approximation within an ulp could spoil, by an ulp down.  The block's largest
+    root makes it 11.5 before its code, a tie that goes to 12; an ulp less would
+    go to 11."""
+    k = torch.arange(-48, 58, device=DEV, dtype=torch.float64)
+    n = len(k)
+    scale, d = (torch.tensor(x, dtype=F32, device=DEV).double().mul(torch.exp2(k)).float() for x in (2.730476, 106.36985))
+    grads, v = torch.zeros(128 * n, device=DEV), torch.zeros(128 * n, dtype=torch.uint8, device=DEV)
+    v[::128] = 0x38   # 1
+    grads[1::128] = d
+    m, ms, vs = torch.zeros_like(v), torch.ones(n, device=DEV), scale.clone()
+    mg.moe_adamw(params=[torch.zeros(128 * n, dtype=BF, device=DEV)], grads=[grads], m=[m], v=[v], m_scale=[ms], v_scale=[vs], lr=0.0, beta2=0.5)
+    x = 0.5 * (scale * scale)
+    assert ((x.view(torch.int32) & 0x7fffff) == 0x6e9372).all()
+    largest = (0.5 * d * d).double().sqrt().float()
+    r = x.double().sqrt().float()
+    y = r * (448.0 / largest.double()).float()
+    assert (y == 11.5).all() and (torch.nextafter(r, torch.zeros_like(r)) * (448.0 / largest.double()).float() < 11.5).all()
+    assert torch.equal(vs, (largest.double() / 448).float())
+    assert (v[::128].view(torch.float8_e4m3fn).float() == 12).all()
