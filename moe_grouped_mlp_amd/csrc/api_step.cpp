@@ -537,6 +537,8 @@ moe_status moe_adamw(const moe_adamw_args* a, void* stream) {
   l.lr_dev = a->lr_dev;
   l.err = a->err_flag;
   l.stochastic = fp8 && a->stochastic;
+  // (the largest such root, over sqrt(1 - beta2^step), is 2^-24 of eps)
+  l.small_roots = a->eps * std::sqrt(1.0 - a->beta2) < 0x1p-39;
   l.seed = a->seed;
   int i = 0;
   do {

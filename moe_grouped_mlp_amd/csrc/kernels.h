@@ -250,6 +250,7 @@ struct AdamList {
   const float* lr_dev;
   int32_t* err;
   int32_t step, stochastic;
+  int32_t small_roots;     // eps is so small that roots of v below 2^-126 count
   uint32_t seed;
 };
 static_assert(sizeof(AdamList) <= 4000, "a launch takes 4 KB of arguments");
