@@ -1124,7 +1124,8 @@ moe_status moe_router_bias_update(const moe_bias_update_args* args, void* stream
  *   a tensor's buffers makes wide loads possible).  A buffer that overlaps
  *   another one of the list is refused with MOE_ERR_INVALID_ARG (gradients
  *   may overlap each other).
- *   0 <= beta < 1, eps >= 0, finite lr and weight_decay, max_norm >= 0.
+ *   0 <= beta < 1, eps 0 or at least 2^-126 (the kernels' reciprocal takes
+ *   subnormal numbers for zero), finite lr and weight_decay, max_norm >= 0.
  * ---------------------------------------------------------------------- */
 typedef enum moe_state { MOE_STATE_F32 = 0, MOE_STATE_FP8 = 1 } moe_state;
 

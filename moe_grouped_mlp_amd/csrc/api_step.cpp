@@ -486,7 +486,7 @@ moe_status moe_grad_clip(const moe_grad_args* a, void* stream) {
 moe_status moe_adamw(const moe_adamw_args* a, void* stream) {
   if (!a || a->n_tensors < 0 || (a->n_tensors > 0 && !a->tensors) ||
       (a->state_type != MOE_STATE_F32 && a->state_type != MOE_STATE_FP8) || !std::isfinite(a->lr) ||
-      !(a->beta1 >= 0.0 && a->beta1 < 1.0) || !(a->beta2 >= 0.0 && a->beta2 < 1.0) || !(a->eps >= 0.0) ||
+      !(a->beta1 >= 0.0 && a->beta1 < 1.0) || !(a->beta2 >= 0.0 && a->beta2 < 1.0) || !(a->eps == 0.0 || a->eps >= 0x1p-126) ||
       !std::isfinite(a->eps) || (!a->step_dev && a->step < 1) || (a->sumsq && !(a->max_norm >= 0.0)) ||
       (reinterpret_cast<uintptr_t>(a->sumsq) & 7) || ((reinterpret_cast<uintptr_t>(a->step_dev) | reinterpret_cast<uintptr_t>(a->lr_dev)) & 3))
     return MOE_ERR_INVALID_ARG;

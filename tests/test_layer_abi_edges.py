@@ -2,8 +2,23 @@
 
 from moe_grouped_mlp_amd import binding as B
 
+from .test_abi import DEVICE, INVALID, _call, no_device
+from .test_layer_abi import _adamw, _tensor
+
 
 def test_the_largest_norm_keeps_64_bits():
     a = B.AdamwArgs()
     a.max_norm = 0.1
     assert a.max_norm == 0.1 and B.AdamwArgs.max_norm.size == 8
+
+
+def test_adamw_refuses_a_subnormal_eps():
+    """0 / eps would not be 0: the reciprocal of a subnormal number is infinite there."""
+    for eps in (1e-40, 2.0 ** -127, 1e-300):
+        assert _call("moe_adamw", _adamw([_tensor()], eps=eps)) == INVALID, eps
+
+
+@no_device
+def test_adamw_accepts_small_eps():
+    for eps in (0.0, 2.0 ** -126, 1e-30):
+        assert _call("moe_adamw", _adamw([_tensor()], eps=eps)) == DEVICE, eps
