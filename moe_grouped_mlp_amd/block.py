@@ -139,7 +139,10 @@ class ExpertBlock:
         # 8-bit integers: forward only
         self.int8 = prec == B.PREC_INT8
         # gate()'s buffers by number of experts and type (kept for captured graphs)
-        self._gate_bufs, self._gate_args, self._gate_routed, self._adamw = {}, None, False, None
+        self._gate_bufs, self._gate_args, self._gate_routed = {}, None, False
+        # adamw_step()'s states, whether a step was made since they were, and those
+        # that a capture used (its graph writes them whatever was loaded since)
+        self._adamw, self._adamw_used, self._adamw_captured = None, False, []
         # router_loss()'s buffers and the streams they were used on, by shape
         self._router_bufs, self._router_captured = {}, set()
         self._ws_grad, self.grad_norm = {}, None
@@ -329,7 +332,7 @@ class ExpertBlock:
         else:
             self.w1i.copy_(w1)
         self.w2.copy_(w2)
-        self._adamw = None   # states and copies were of other weights
+        self._reset_adamw()   # states and copies were of other weights
         self._requantize()
 
     def _requantize(self) -> None:
@@ -800,7 +803,8 @@ class ExpertBlock:
         """One AdamW step of w1i and w2 from dw1 and dw2 (moe_adamw).  The first
         call makes the states (state: fp32, or 8 bits with their roots rounded
         stochastically if asked) and, with master, fp32 copies of the weights
-        that the steps are made on; load_weights() drops them.  max_norm: the
+        that the steps are made on; load_weights() begins them anew where they
+        are, for captured graphs too.  max_norm: the
         gradients count as if clip_grads(max_norm) had scaled them, without its
         pass; a norm that is not finite makes no step (but counts as one) and
         sets MOE_DEVERR_NONFINITE in err_flag.  capturable: the step number is
@@ -813,14 +817,21 @@ class ExpertBlock:
         if not capturable and (capturing or isinstance(lr, torch.Tensor)):
             raise RuntimeError("a captured step, or a rate in a tensor, needs capturable=True")
         params, grads = [self.w1i, self.w2], [self.dw1, self.dw2]
+        kind = (state, master, capturable)
+        if self._adamw is not None and self._adamw["kind"] != kind:
+            if self._adamw_used:
+                raise ValueError("the states were made by steps of another kind (load_weights() begins them anew)")
+            self._adamw = None
+        if self._adamw is None:
+            self._adamw = next((st for st in self._adamw_captured if st["kind"] == kind), None)
         if self._adamw is None:
             if capturing:
                 raise RuntimeError("the first adamw_step() makes the states: it cannot be captured")
             self._adamw = self._adamw_states(params, state, master, capturable)
             self.adamw_steps = 0   # (of steps that are not capturable)
-        st = self._adamw
-        if st["kind"] != (state, master, capturable):
-            raise ValueError("the states were made by steps of another kind (load_weights() drops them)")
+        st, self._adamw_used = self._adamw, True
+        if capturing and not any(st is c for c in self._adamw_captured):
+            self._adamw_captured.append(st)
         kw = {}
         if max_norm is not None:
             if self.grad_norm is None:
@@ -844,6 +855,17 @@ class ExpertBlock:
                     stochastic=stochastic, seed=seed, **kw)
         if requantize:
             self._requantize()
+
+    def _reset_adamw(self) -> None:
+        """States of zeros and copies of the weights as they are, in place: a graph
+        captured with them goes on from these."""
+        self.adamw_steps, self._adamw_used = 0, False
+        made = [] if self._adamw is None else [self._adamw]
+        for st in made + [c for c in self._adamw_captured if c is not self._adamw]:
+            for t in (*st["m"], *st["v"], *(st["m_scale"] or ()), *(st["v_scale"] or ()), st["step"]):
+                t.zero_()
+            for copy, w in zip(st["master"] or (), (self.w1i, self.w2)):
+                copy.copy_(w.view(-1))
 
     def _adamw_states(self, params, state, master, capturable):
         dev = self.w2.device

@@ -1,0 +1,77 @@
+"""ExpertBlock's AdamW steps between loads, graphs and checkpoints."""
+
+import gc
+
+import pytest
+import torch
+
+import moe_grouped_mlp_amd as mg
+
+from .test_gpu_fp8_block import _inputs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+E, H, I, T, K = 4, 128, 128, 32, 2
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _give_back():
+    """Tests after these measure what torch's allocator holds."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
+
+
+def setup_module(module):
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    mg.lib()
+
+
+def _block(seed):
+    _, _, w1, w2, _ = _inputs(E, H, 2 * I, I, T, seed)
+    blk = mg.ExpertBlock(E, H, I, T, K, wgrad=True)
+    blk.load_weights(w1, w2)
+    return blk, w1, w2
+
+
+def _grads(blk, seed):
+    g = torch.Generator(DEV).manual_seed(seed)
+    for dw in (blk.dw1, blk.dw2):
+        dw.copy_(torch.randn(dw.shape, generator=g, device=DEV))
+
+
+def _states(blk):
+    st = blk._adamw
+    return [blk.w1i, blk.w2, *st["m"], *st["v"], *(st["m_scale"] or ()), *(st["v_scale"] or ()), *(st["master"] or ())]
+
+
+def _equal(a, b):
+    return all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(_states(a), _states(b)))
+
+
+@pytest.mark.parametrize("state,master", [(mg.STATE_F32, True), (mg.STATE_FP8, False)])
+def test_a_captured_step_goes_on_after_load_weights(state, master):
+    """Replays after other weights were loaded are the first steps from those, as
+    an eager block makes them."""
+    kw = dict(weight_decay=0.1, max_norm=3.0, state=state, master=master, stochastic=state == mg.STATE_FP8, seed=1, capturable=True)
+    blk, *_ = _block(1)
+    _grads(blk, 0)
+    blk.adamw_step(1e-2, **kw)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        blk.adamw_step(1e-2, **kw)
+    graph.replay()
+    other, w1, w2 = _block(2)
+    blk.load_weights(w1, w2)
+    spare = [torch.full_like(t, 3) for t in _states(blk)]   # (memory given back would be these now)
+    for step in range(3):
+        _grads(blk, step)
+        _grads(other, step)
+        graph.replay()
+        other.adamw_step(1e-2, **kw)
+        torch.cuda.synchronize()
+        assert _equal(blk, other) and blk._adamw["step"].item() == step + 1
+    assert all((t == 3).all() for t in spare)
+    blk.adamw_step(1e-2, **kw)   # and an eager one after them
+    other.adamw_step(1e-2, **kw)
+    assert _equal(blk, other)
