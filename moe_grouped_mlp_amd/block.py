@@ -829,7 +829,7 @@ class ExpertBlock:
                 raise RuntimeError("the first adamw_step() makes the states: it cannot be captured")
             self._adamw = self._adamw_states(params, state, master, capturable)
             self.adamw_steps = 0   # (of steps that are not capturable)
-        st, self._adamw_used = self._adamw, True
+        st = self._adamw
         if capturing and not any(st is c for c in self._adamw_captured):
             self._adamw_captured.append(st)
         kw = {}
@@ -847,12 +847,17 @@ class ExpertBlock:
             kw["step_dev"] = st["step"]
             if isinstance(lr, torch.Tensor):
                 kw["lr_dev"], lr = lr, 0.0
-        else:
-            self.adamw_steps += 1
-        B.moe_adamw(params=params, grads=grads, m=st["m"], v=st["v"], master=st["master"],
-                    m_scale=st["m_scale"], v_scale=st["v_scale"], lr=lr, step=max(1, self.adamw_steps),
-                    beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
-                    stochastic=stochastic, seed=seed, **kw)
+        try:
+            B.moe_adamw(params=params, grads=grads, m=st["m"], v=st["v"], master=st["master"],
+                        m_scale=st["m_scale"], v_scale=st["v_scale"], lr=lr, step=self.adamw_steps + 1,
+                        beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay,
+                        stochastic=stochastic, seed=seed, **kw)
+        except BaseException:   # a refused step is none
+            if capturable:
+                st["step"].sub_(1)
+            raise
+        self.adamw_steps += not capturable
+        self._adamw_used = True
         if requantize:
             self._requantize()
 

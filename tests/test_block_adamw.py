@@ -87,3 +87,27 @@ def test_states_of_no_graph_are_given_back(block):
     _load(block, 1.0)
     block.adamw_step(0.1, state=mg.STATE_FP8)
     assert not block._adamw_captured and block._adamw is not first
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_a_refused_step_is_none(block, capturable):
+    """Neither counted nor held to its kind of states."""
+    def refuse(**kw):
+        raise mg.MoeError("moe_adamw", 1, "no")
+
+    def steps():
+        return block._adamw["step"].item() if capturable else block.adamw_steps
+
+    with mock.patch.object(B, "moe_adamw", refuse):
+        with pytest.raises(mg.MoeError):
+            block.adamw_step(0.1, state=mg.STATE_FP8)
+        with pytest.raises(mg.MoeError):
+            block.adamw_step(0.1, capturable=capturable)
+        assert steps() == 0
+    seen = []
+    with mock.patch.object(B, "moe_adamw", lambda **kw: seen.append(kw["step_dev"].item() if capturable else kw["step"])):
+        block.adamw_step(0.1, capturable=capturable)
+        with mock.patch.object(B, "moe_adamw", refuse), pytest.raises(mg.MoeError):
+            block.adamw_step(float("nan"), capturable=capturable)
+        block.adamw_step(0.1, capturable=capturable)
+    assert seen == [1, 2] and steps() == 2
