@@ -145,7 +145,7 @@ class ExpertBlock:
         self._adamw, self._adamw_used, self._adamw_captured = None, False, []
         # router_loss()'s buffers and the streams they were used on, by shape
         self._router_bufs, self._router_captured = {}, set()
-        self._ws_grad, self.grad_norm = {}, None
+        self._ws_grad, self.grad_sumsq, self.grad_norm = {}, None, None
         self._dprobs_valid = False   # whether dprobs are of the rows last routed
         if self.fp8 and (recompute or unfused):
             raise ValueError("the FP8 layer has no recompute path, and always runs as separate passes")
@@ -834,14 +834,7 @@ class ExpertBlock:
             self._adamw_captured.append(st)
         kw = {}
         if max_norm is not None:
-            if self.grad_norm is None:
-                self.grad_sumsq = torch.empty(1, dtype=torch.float64, device=self.dw1.device)
-                self.grad_norm = torch.empty(1, dtype=torch.float32, device=self.dw1.device)
-            need = B.moe_grad_workspace_size(len(grads))
-            if need not in self._ws_grad:
-                self._ws_grad[need] = torch.empty(need, dtype=torch.uint8, device=self.dw1.device)
-            B.moe_grad_sumsq(tensors=grads, sumsq=self.grad_sumsq, workspace=self._ws_grad[need])
-            kw = dict(sumsq=self.grad_sumsq, max_norm=max_norm, err_flag=self.err_flag)
+            kw = dict(sumsq=self._sum_squares(grads), max_norm=max_norm, err_flag=self.err_flag)
         if capturable:
             st["step"].add_(1)
             kw["step_dev"] = st["step"]
@@ -960,17 +953,22 @@ class ExpertBlock:
         if not self.wgrad:
             raise RuntimeError("ExpertBlock was built without wgrad=True")
         grads = [self.dw1, self.dw2, *extra]
+        if self.grad_norm is None:
+            self.grad_norm = torch.empty(1, dtype=torch.float32, device=self.dw1.device)
+        B.moe_grad_clip(tensors=grads, sumsq=self._sum_squares(grads), max_norm=max_norm,
+                        norm=self.grad_norm, err_flag=self.err_flag)
+        return self.grad_norm
+
+    def _sum_squares(self, grads):
+        """Their sum of squares, in grad_sumsq."""
         need = B.moe_grad_workspace_size(len(grads))
         dev = self.dw1.device
-        if self.grad_norm is None:
+        if self.grad_sumsq is None:
             self.grad_sumsq = torch.empty(1, dtype=torch.float64, device=dev)
-            self.grad_norm = torch.empty(1, dtype=torch.float32, device=dev)
         if need not in self._ws_grad:   # (kept for captured graphs, as above)
             self._ws_grad[need] = torch.empty(need, dtype=torch.uint8, device=dev)
         B.moe_grad_sumsq(tensors=grads, sumsq=self.grad_sumsq, workspace=self._ws_grad[need])
-        B.moe_grad_clip(tensors=grads, sumsq=self.grad_sumsq, max_norm=max_norm,
-                        norm=self.grad_norm, err_flag=self.err_flag)
-        return self.grad_norm
+        return self.grad_sumsq
 
     def weight_grads(self, timing_events=None, accumulate: bool = False):
         """dW1 (rows in w1i's interleaved order) and dW2 of the last

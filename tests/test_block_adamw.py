@@ -111,3 +111,13 @@ def test_a_refused_step_is_none(block, capturable):
             block.adamw_step(float("nan"), capturable=capturable)
         block.adamw_step(0.1, capturable=capturable)
     assert seen == [1, 2] and steps() == 2
+
+
+def test_the_norm_is_clip_grads_own(block):
+    """adamw_step() leaves it (it held nothing before), and both sum into one buffer."""
+    block.adamw_step(0.1, max_norm=1.0)
+    assert block.grad_norm is None
+    total = block.grad_sumsq
+    with mock.patch.object(B, "moe_grad_clip"):
+        norm = block.clip_grads(1.0)
+    assert norm is block.grad_norm and block.grad_sumsq is total
