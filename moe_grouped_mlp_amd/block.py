@@ -797,17 +797,22 @@ class ExpertBlock:
 
     # ------------------------------------------------------------ update --
     def adamw_step(self, lr, *, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
-                   weight_decay: float = 0.0, max_norm: Optional[float] = None,
-                   state: int = B.STATE_F32, master: bool = True, stochastic: bool = False,
+                   weight_decay: float = 0.0, max_norm: Optional[float] = None, extra=(),
+                   sumsq: Optional[torch.Tensor] = None, state: int = B.STATE_F32, master: bool = True, stochastic: bool = False,
                    seed: int = 0, capturable: bool = False, requantize: bool = True) -> None:
         """One AdamW step of w1i and w2 from dw1 and dw2 (moe_adamw).  The first
         call makes the states (state: fp32, or 8 bits with their roots rounded
         stochastically if asked) and, with master, fp32 copies of the weights
         that the steps are made on; load_weights() begins them anew where they
         are, for captured graphs too.  max_norm: the
-        gradients count as if clip_grads(max_norm) had scaled them, without its
-        pass; a norm that is not finite makes no step (but counts as one) and
-        sets MOE_DEVERR_NONFINITE in err_flag.  capturable: the step number is
+        gradients count as if clip_grads(max_norm, extra) had scaled them,
+        without its pass: extra are the other parameters' gradients, which
+        take part in the norm and are left as they are (moe_adamw makes their
+        parameters' step, with grad_sumsq, this sum, and the same max_norm).
+        sumsq: the sum of squares itself (fp64 [1]), say summed over several
+        processes, in place of that of dw1, dw2 and extra.  A norm that is not
+        finite makes no step (but counts as one) and sets
+        MOE_DEVERR_NONFINITE in err_flag.  capturable: the step number is
         counted on the device and lr may be a tensor (fp32 [1]), so that a
         captured graph goes on from replay to replay.  requantize: the copies
         of the weights that the products read are made anew."""
@@ -816,6 +821,10 @@ class ExpertBlock:
         capturing = _capturing(self.w2)
         if not capturable and (capturing or isinstance(lr, torch.Tensor)):
             raise RuntimeError("a captured step, or a rate in a tensor, needs capturable=True")
+        if max_norm is None and (extra or sumsq is not None):
+            raise ValueError("extra and sumsq are of the norm that max_norm clips to")
+        if extra and sumsq is not None:
+            raise ValueError("the sum of squares is either given (sumsq) or made, with extra")
         params, grads = [self.w1i, self.w2], [self.dw1, self.dw2]
         kind = (state, master, capturable)
         if self._adamw is not None and self._adamw["kind"] != kind:
@@ -834,7 +843,9 @@ class ExpertBlock:
             self._adamw_captured.append(st)
         kw = {}
         if max_norm is not None:
-            kw = dict(sumsq=self._sum_squares(grads), max_norm=max_norm, err_flag=self.err_flag)
+            if sumsq is None:
+                sumsq = self._sum_squares([*grads, *extra])
+            kw = dict(sumsq=sumsq, max_norm=max_norm, err_flag=self.err_flag)
         if capturable:
             st["step"].add_(1)
             kw["step_dev"] = st["step"]

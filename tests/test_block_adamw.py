@@ -113,6 +113,23 @@ def test_a_refused_step_is_none(block, capturable):
     assert seen == [1, 2] and steps() == 2
 
 
+def test_norm_over_other_gradients(block):
+    """extra takes part in the norm and nothing else; a sum that is given is taken."""
+    more = [torch.zeros(5), torch.zeros(3)]
+    with mock.patch.object(B, "moe_grad_sumsq") as total, mock.patch.object(B, "moe_adamw") as step:
+        block.adamw_step(0.1, max_norm=2.0, extra=more)
+        assert [t is u for t, u in zip(total.call_args.kwargs["tensors"], (block.dw1, block.dw2, *more))] == [True] * 4
+        assert len(step.call_args.kwargs["params"]) == 2 and step.call_args.kwargs["sumsq"] is block.grad_sumsq
+        total.reset_mock()
+        given = torch.ones(1, dtype=torch.float64)
+        block.adamw_step(0.1, max_norm=2.0, sumsq=given)
+        assert step.call_args.kwargs["sumsq"] is given and not total.called
+    for kw in (dict(extra=more), dict(sumsq=given), dict(max_norm=1.0, extra=more, sumsq=given)):
+        with pytest.raises(ValueError):
+            block.adamw_step(0.1, **kw)
+    assert block.adamw_steps == 2
+
+
 def test_the_norm_is_clip_grads_own(block):
     """adamw_step() leaves it (it held nothing before), and both sum into one buffer."""
     block.adamw_step(0.1, max_norm=1.0)

@@ -75,3 +75,26 @@ def test_a_captured_step_goes_on_after_load_weights(state, master):
     blk.adamw_step(1e-2, **kw)   # and an eager one after them
     other.adamw_step(1e-2, **kw)
     assert _equal(blk, other)
+
+
+def test_norm_over_other_gradients():
+    """A step with the router's gradient in the norm is the step of gradients that
+    clip_grads() scaled with it.  (It rounds them to bf16, 2^-8; the update of a first step
+    hardly depends on their size: its error is that of eps beside their root.)"""
+    blk, *_ = _block(3)
+    two, *_ = _block(3)
+    extra = torch.randn(300, device=DEV)
+    for b in (blk, two):
+        _grads(b, 4)
+    kept = extra.clone()
+    blk.adamw_step(1e-2, max_norm=1.0, extra=[extra], beta1=0.0, beta2=0.0, eps=1.0)
+    norm = two.clip_grads(1.0, extra=[extra])
+    assert torch.equal(blk.grad_sumsq, two.grad_sumsq) and abs(blk.grad_sumsq.sqrt().item() - norm.item()) <= 2.0 ** -23 * norm.item()
+    assert blk.grad_sumsq.item() > (blk.dw1.double().square().sum() + blk.dw2.double().square().sum() + kept.double().square().sum()).item() * (1 - 1e-12)
+    two.adamw_step(1e-2, beta1=0.0, beta2=0.0, eps=1.0)
+    for a, b, w, g in zip(blk._adamw["master"], two._adamw["master"], (blk.w1i, blk.w2), (two.dw1, two.dw2)):
+        assert ((a - b).abs() <= 1e-2 * 2.0 ** -8 * 1.01 * g.float().abs().view(-1) + 2.0 ** -22 * a.abs()).all()
+    given, *_ = _block(3)
+    _grads(given, 4)
+    given.adamw_step(1e-2, max_norm=1.0, sumsq=blk.grad_sumsq, beta1=0.0, beta2=0.0, eps=1.0)
+    assert _equal(blk, given)
