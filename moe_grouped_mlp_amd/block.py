@@ -827,18 +827,9 @@ class ExpertBlock:
             raise ValueError("the sum of squares is either given (sumsq) or made, with extra")
         params, grads = [self.w1i, self.w2], [self.dw1, self.dw2]
         kind = (state, master, capturable)
-        if self._adamw is not None and self._adamw["kind"] != kind:
-            if self._adamw_used:
-                raise ValueError("the states were made by steps of another kind (load_weights() begins them anew)")
-            self._adamw = None
-        if self._adamw is None:
-            self._adamw = next((st for st in self._adamw_captured if st["kind"] == kind), None)
-        if self._adamw is None:
-            if capturing:
-                raise RuntimeError("the first adamw_step() makes the states: it cannot be captured")
-            self._adamw = self._adamw_states(params, state, master, capturable)
-            self.adamw_steps = 0   # (of steps that are not capturable)
-        st = self._adamw
+        if self._adamw is not None and self._adamw["kind"] != kind and self._adamw_used:
+            raise ValueError("the states were made by steps of another kind (load_weights() begins them anew)")
+        st = self._adamw_of(kind, capturing)
         if capturing and not any(st is c for c in self._adamw_captured):
             self._adamw_captured.append(st)
         kw = {}
@@ -875,6 +866,49 @@ class ExpertBlock:
                 t.zero_()
             for copy, w in zip(st["master"] or (), (self.w1i, self.w2)):
                 copy.copy_(w.view(-1))
+
+    def _adamw_of(self, kind, capturing=False):
+        """The states of this kind, made if there are none, as those to go on from."""
+        if self._adamw is None or self._adamw["kind"] != kind:
+            st = next((st for st in self._adamw_captured if st["kind"] == kind), None)
+            if st is None:
+                if capturing:
+                    raise RuntimeError("the first adamw_step() makes the states: it cannot be captured")
+                st = self._adamw_states([self.w1i, self.w2], *kind)
+            self._adamw, self.adamw_steps = st, 0   # (of steps that are not capturable)
+        return self._adamw
+
+    def adamw_state(self) -> dict:
+        """What adamw_step() goes on from, for a checkpoint: its own tensors and
+        numbers, not copies."""
+        if self._adamw is None:
+            raise RuntimeError("adamw_state() needs adamw_step() first")
+        state, master, capturable = self._adamw["kind"]
+        return dict(state=state, master=master, capturable=capturable,
+                    step=self._adamw["step"] if capturable else self.adamw_steps,
+                    **{name: self._adamw[name] for name in self._ADAMW_LISTS}, weights=self._adamw["master"])
+
+    def load_adamw_state(self, saved: dict) -> None:
+        """Copies what adamw_state() gave into the block's own states, where they are.
+        load_weights() comes before, with the weights of that moment: it begins the
+        states anew."""
+        kind = (saved["state"], saved["master"], saved["capturable"])
+        if self._adamw is not None and self._adamw["kind"] != kind and self._adamw_used:
+            raise ValueError("the states were made by steps of another kind (load_weights() begins them anew)")
+        st = self._adamw_of(kind, _capturing(self.w2))
+        pairs = [(mine, theirs) for name in self._ADAMW_LISTS for mine, theirs in zip(st[name] or (), saved[name] or ())]
+        pairs += zip(st["master"] or (), saved["weights"] or ())
+        if any(mine.shape != theirs.shape or mine.dtype != theirs.dtype for mine, theirs in pairs):
+            raise ValueError("the states are of another block's sizes")
+        for mine, theirs in pairs:
+            mine.copy_(theirs)
+        if saved["capturable"]:
+            st["step"].copy_(saved["step"])
+        else:
+            self.adamw_steps = saved["step"]
+        self._adamw_used = True
+
+    _ADAMW_LISTS = ("m", "v", "m_scale", "v_scale")
 
     def _adamw_states(self, params, state, master, capturable):
         dev = self.w2.device

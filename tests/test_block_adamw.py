@@ -138,3 +138,26 @@ def test_the_norm_is_clip_grads_own(block):
     with mock.patch.object(B, "moe_grad_clip"):
         norm = block.clip_grads(1.0)
     assert norm is block.grad_norm and block.grad_sumsq is total
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(state=mg.STATE_FP8, master=False), dict(capturable=True)])
+def test_states_are_saved_and_loaded_in_place(block, kw):
+    for call in (block.adamw_state,):
+        with pytest.raises(RuntimeError, match="adamw_step"):
+            call()
+    block.adamw_step(0.1, **kw)
+    block.adamw_step(0.1, **kw)
+    for i, t in enumerate(_tensors(block._adamw)[:-1]):
+        t.fill_(i + 1)
+    saved = {k: [t.clone() for t in v] if isinstance(v, list) else v.clone() if torch.is_tensor(v) else v for k, v in block.adamw_state().items()}
+    kept = _tensors(block._adamw)
+    _load(block, 1.0)
+    block.load_adamw_state(saved)
+    now = _tensors(block._adamw)
+    assert all(a is b for a, b in zip(now, kept)) and all((t == i + 1).all() for i, t in enumerate(now[:-1]))
+    block.adamw_step(0.1, **kw)
+    assert (block._adamw["step"].item() if kw.get("capturable") else block.adamw_steps) == 3
+    with pytest.raises(ValueError, match="kind"):
+        block.load_adamw_state({**saved, "state": 1 - saved["state"]})
+    with pytest.raises(ValueError, match="sizes"):
+        block.load_adamw_state({**saved, "m": [t[1:] for t in saved["m"]]})

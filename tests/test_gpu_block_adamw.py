@@ -98,3 +98,26 @@ def test_norm_over_other_gradients():
     _grads(given, 4)
     given.adamw_step(1e-2, max_norm=1.0, sumsq=blk.grad_sumsq, beta1=0.0, beta2=0.0, eps=1.0)
     assert _equal(blk, given)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(state=mg.STATE_FP8, master=False, stochastic=True, seed=2), dict(capturable=True)])
+def test_resumed_steps(kw, tmp_path):
+    """A block that goes on from a file is the block that wrote it, bit for bit."""
+    blk, *_ = _block(5)
+    for step in range(2):
+        _grads(blk, step)
+        blk.adamw_step(1e-2, **kw)
+    w1, w2 = torch.empty_like(blk.w1i), blk.w2.clone()
+    mg.moe_weight_repack_interleave(blk.w1i, w1, E, I, H, inverse=True)
+    torch.save(dict(w1=w1, w2=w2, adamw=blk.adamw_state()), tmp_path / "state.pt")
+    for step in (2, 3):
+        _grads(blk, step)
+        blk.adamw_step(1e-2, **kw)
+    saved = torch.load(tmp_path / "state.pt", weights_only=True)
+    other, *_ = _block(6)
+    other.load_weights(saved["w1"], saved["w2"])
+    other.load_adamw_state(saved["adamw"])
+    for step in (2, 3):
+        _grads(other, step)
+        other.adamw_step(1e-2, **kw)
+    assert _equal(blk, other)
