@@ -752,12 +752,13 @@ class ExpertBlock:
             self.probs = torch.empty(T, self.k, dtype=torch.float32, device=dev)
         if E_all not in self._gate_bufs:
             self._gate_bufs[E_all] = torch.zeros(E_all, dtype=torch.int32, device=dev)
-        self.gate_counts = self._gate_bufs[E_all]
-        self._gate_args = dict(T=T, E=E_all, k=self.k, logits=logits, expert_idx=self.expert_idx,
-                               score=score, renorm=renorm, scale=scale)
-        B.moe_router_gate(**self._gate_args, probs=self.probs, bias=bias, n_groups=n_groups,
+        args = dict(T=T, E=E_all, k=self.k, logits=logits, expert_idx=self.expert_idx,
+                    score=score, renorm=renorm, scale=scale)
+        B.moe_router_gate(**args, probs=self.probs, bias=bias, n_groups=n_groups,
                           topk_groups=topk_groups, group_top=group_top, token_mask=token_mask,
-                          counts=self.gate_counts if count else None)
+                          counts=self._gate_bufs[E_all] if count else None)
+        # (a call that is refused leaves those of the picks that are there)
+        self._gate_args, self.gate_counts = args, self._gate_bufs[E_all]
         self.route(self.expert_idx, self.probs, x)
 
     def gate_backward(self, dprobs: Optional[torch.Tensor] = None,
