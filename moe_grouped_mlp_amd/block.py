@@ -789,12 +789,12 @@ class ExpertBlock:
 
     def update_bias(self, bias: torch.Tensor, rate: float) -> None:
         """The balance bias [E_total] after a step, from the picks that
-        gate(count=True) counted since the last update (several processes: sum
-        gate_counts over them before); the counts are cleared."""
+        gate(count=True) of so many experts counted since the last update (several
+        processes: sum gate_counts over them before); the counts are cleared."""
         if not hasattr(self, "gate_counts"):
             raise RuntimeError("update_bias() needs gate(count=True) first")
-        B.moe_router_bias_update(E=self.gate_counts.numel(), counts=self.gate_counts, bias=bias,
-                                 rate=rate, reset=True)
+        counts = self._gate_bufs.get(bias.numel(), self.gate_counts)
+        B.moe_router_bias_update(E=counts.numel(), counts=counts, bias=bias, rate=rate, reset=True)
 
     # ------------------------------------------------------------ update --
     def adamw_step(self, lr, *, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,

@@ -47,3 +47,16 @@ def test_a_refused_first_gate_leaves_nothing(block):
         block.gate_backward(torch.zeros(T, K))
     with pytest.raises(RuntimeError, match="gate"):
         block.update_bias(torch.zeros(E), 0.1)
+
+
+def test_bias_updates_of_two_routers(block):
+    """Each bias goes by the counts of its own number of experts, in any order."""
+    block.gate(torch.zeros(T, E), count=True)
+    few = block.gate_counts
+    block.gate(torch.zeros(T, 2 * E), count=True)
+    many = block.gate_counts
+    for size, counts in ((E, few), (2 * E, many)):
+        block.gate(torch.zeros(T, 3 * E - size))   # (the other one was the last)
+        with mock.patch.object(B, "moe_router_bias_update") as update:
+            block.update_bias(torch.zeros(size), 0.1)
+        assert update.call_args.kwargs["counts"] is counts and update.call_args.kwargs["E"] == size
