@@ -228,7 +228,8 @@ MOE_DEV float renormed(bool sigmoid, bool live, float x) {
 // up to 1024 terms over 32 additions and 6 exchanges: under 2^-18 (1 + |c|).
 MOE_DEV float score_error(bool sigmoid) { return sigmoid ? 0x1p-22f : 0x1p-18f; }
 
-// A float's bits with the order of its value; 0 is left for no choice.
+// A float's bits with the order of its value (that of -0 is below that of +0, so
+// logits come with + 0.0f, which makes one of the other); 0 is left for no choice.
 MOE_DEV uint32_t key_of(float f) {
   const uint32_t u = __float_as_uint(f);
   return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
@@ -415,7 +416,7 @@ MOE_DEV void picks64(const GateP& g, const T* row, double* choice, Room64* room,
   float m = neg_inf();
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    x[i] = fmaxf(i < p.n ? x[i] : neg_inf(), neg_inf());
+    x[i] = fmaxf(i < p.n ? x[i] : neg_inf(), neg_inf()) + 0.0f;   // (-0 too)
     m = fmaxf(m, x[i]);
     choice[kWave * i] = x[i];
   }
@@ -663,6 +664,8 @@ __global__ __launch_bounds__(gate_threads(V)) void gate_kernel(const GateP g) {
   float x[V], bias[V] = {};
   if (g.bias) load_row<V>(g.bias, g.l.vec_bias, p, bias);
   load_logits<V>(row, g.l, p, x);
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] += 0.0f;   // -0 becomes +0
   if (g.counts) {
     for (int e = threadIdx.x; e < g.l.E; e += threads) s_count[e] = 0;
     __syncthreads();

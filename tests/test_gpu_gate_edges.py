@@ -1,0 +1,73 @@
+"""The router's choice by scores (moe_router_gate) where equal and nearly equal
+values decide, and in all of its plans for many tokens, against the float64 oracle.
+Picks are compared exactly; the weights' tolerance is that of test_gpu_gate."""
+
+import gc
+
+import numpy as np
+import pytest
+import torch
+
+import moe_grouped_mlp_amd as mg
+from oracle import layer as ol
+
+from .test_gpu_gate import DEV, INF, _gate, _logits, _np
+
+pytestmark = pytest.mark.gpu
+MANY = 1500   # tokens: more than four a CU, so that tokens share a wave where their experts allow it
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _give_back():
+    """Tests after these measure what torch's allocator holds."""
+    yield
+    gc.collect()
+    torch.cuda.empty_cache()
+
+
+def setup_module(module):
+    assert torch.cuda.is_available(), "GPU tests need a ROCm device"
+    mg.lib()
+
+
+def _check(x, k, sigmoid=False, bias=None, mask=None, rows=40, **kw):
+    """One call against the oracle on a sample of the rows (the first and last among them); all
+    rows' counts against the picks."""
+    T, E = x.shape
+    counts = torch.zeros(E, dtype=torch.int32, device=DEV)
+    idx, probs = _gate(x, k, sigmoid, bias=bias, token_mask=mask, counts=counts, **kw)
+    at = np.unique(np.r_[np.arange(min(T, 8)), T - 1, np.random.default_rng(T + E).integers(0, T, rows)]) if T > rows else np.arange(T)
+    xn = _np(x[torch.from_numpy(at).to(DEV)])
+    ref, w = ol.gate(xn, k, sigmoid, _np(bias), mask=None if mask is None else mask.cpu().numpy()[at], **kw)
+    got = idx.cpu().numpy()
+    bad = np.flatnonzero((got[at] != ref).any(1))
+    assert not len(bad), (at[bad[:5]], got[at][bad[:5]], ref[bad[:5]])
+    fin = np.where(np.isfinite(xn), xn, 0)
+    d = np.abs(fin).max(1, keepdims=True) * 2 if not sigmoid or kw.get("renorm") else 0
+    assert (np.abs(_np(probs)[at] - w) <= (d + 40) * 2.0 ** -23 * np.abs(w) + 2.0 ** -140).all()
+    assert np.array_equal(counts.cpu().numpy(), np.bincount(got[got >= 0], minlength=E))
+    return got
+
+
+def _of(values, T, E, seed, dtype=torch.float32):
+    g = torch.Generator(DEV).manual_seed(seed)
+    v = torch.tensor(values, device=DEV, dtype=torch.float32)
+    return v[torch.randint(0, len(values), (T, E), generator=g, device=DEV)].to(dtype)
+
+
+SIZES = [(20, 4, 1), (20, 30, 5), (20, 64, 8), (20, 128, 8), (20, 256, 8), (20, 300, 6), (20, 512, 8), (20, 1024, 16),
+         (MANY, 30, 5), (MANY, 64, 8), (MANY, 100, 4), (MANY, 128, 8), (MANY, 160, 8), (MANY, 256, 8), (MANY, 1024, 16)]
+
+
+@pytest.mark.parametrize("T,E,groups", SIZES)
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_zeros_of_both_signs(T, E, groups, dtype):
+    """-0 and +0 are equal: the lower id goes first."""
+    k = min(E, 6)
+    for values in ([-0.0, 0.0], [-0.0, 0.0, -0.0, 0.0, 1.0, -1.0], [-0.0, 0.0, -2.5, -INF]):
+        x = _of(values, T, E, E + len(values), dtype)
+        for sigmoid in (False, True):
+            _check(x, k, sigmoid)
+            if groups > 1:
+                kw = dict(n_groups=groups, topk_groups=max(2, groups // 2), renorm=True)
+                _check(x, min(k, E // groups * kw["topk_groups"]), sigmoid, **kw)
