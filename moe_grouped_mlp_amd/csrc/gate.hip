@@ -438,8 +438,11 @@ MOE_DEV void picks64(const GateP& g, const T* row, double* choice, Room64* room,
   for (int i = 0; i < V; ++i) {
     double c = choice[kWave * i] + static_cast<double>(bias[i]);
     c = x[i] > neg_inf() && c > neg_inf64() ? c : neg_inf64();
-    b = fmax(b, fmin(a, c));
-    a = fmax(a, c);
+    // a group's largest choice is a logit without a bias (scores of different logits
+    // may be equal), two of them are added as scores
+    const double by = g.bias || g.top == 2 ? c : x[i];
+    b = fmax(b, fmin(a, by));
+    a = fmax(a, by);
     choice[kWave * i] = c;
   }
   bool stays = true;

@@ -71,3 +71,20 @@ def test_zeros_of_both_signs(T, E, groups, dtype):
             if groups > 1:
                 kw = dict(n_groups=groups, topk_groups=max(2, groups // 2), renorm=True)
                 _check(x, min(k, E // groups * kw["topk_groups"]), sigmoid, **kw)
+
+
+@pytest.mark.parametrize("T,E,groups", [s for s in SIZES if s[2] > 1])
+@pytest.mark.parametrize("stay", [1, 2, 3])
+def test_groups_go_by_logits_where_scores_are_equal(T, E, groups, stay):
+    """Without a bias and judged by its largest choice, a group is judged by a logit:
+    sigmoids of 40 and 60 are the same number, and so are softmax terms that underflow.
+    Logits that are listed twice leave the order of picks open in fp32."""
+    k = min(6, E // groups * stay)
+    kw = dict(n_groups=groups, topk_groups=stay, group_top=1)
+    near = [v + d for v in (25.3, 33.7, 38.51, 41.3, 47.9, 59.7) for d in (0.0, 4e-6, 8e-6)]
+    for sigmoid, values in ((True, near), (True, near + [-INF] * 40 + [3.1] * 40), (False, near), (False, [100.7, -900.3, -1801.1, -900.30005, -2700.9]),
+                            (False, [-900.3] * 3 + [-1801.1] * 30 + [0.7])):
+        _check(_of(values, T, E, E + stay + len(values)), k, sigmoid, **kw)
+    x = _logits(T, E, 3, spread=1.0)
+    x[:, 1], x[:, -2:] = 38.5, 41.3
+    _check(x, k, True, **kw)
