@@ -88,3 +88,108 @@ def test_groups_go_by_logits_where_scores_are_equal(T, E, groups, stay):
     x = _logits(T, E, 3, spread=1.0)
     x[:, 1], x[:, -2:] = 38.5, 41.3
     _check(x, k, True, **kw)
+
+
+PLANS = [(MANY, 30, 5), (MANY, 64, 8), (MANY, 100, 4), (MANY, 128, 8), (MANY, 160, 8), (MANY, 256, 8), (MANY, 260, 13), (MANY, 512, 8), (MANY, 1000, 8),
+         (MANY, 1024, 32), (300, 300, 1), (300, 1024, 16), (9001, 30, 5), (9001, 64, 8), (9001, 100, 4), (9001, 256, 8)]   # (and larger workgroups)
+
+
+@pytest.mark.parametrize("T,E,groups", PLANS)
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_tokens(T, E, groups, sigmoid, dtype):
+    x = _logits(T, E, E, dtype)
+    bias = 0.2 * torch.randn(E, generator=torch.Generator(DEV).manual_seed(E), device=DEV)
+    _check(x, 8, sigmoid)
+    _check(x, 4, sigmoid, renorm=True, scale=2.5)
+    _check(x, 8, sigmoid, bias=bias, renorm=True)
+    _check(x, 1, sigmoid, bias=bias)
+    if groups == 1:
+        return
+    for top in (1, 2):
+        for stay in (1, groups // 2):
+            k = min(8, E // groups * stay)
+            kw = dict(n_groups=groups, topk_groups=stay, group_top=top)
+            _check(x, k, sigmoid, **kw, renorm=True)
+            _check(x, k, sigmoid, bias=bias, **kw)
+
+
+@pytest.mark.parametrize("T,E,groups", PLANS)
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_many_tokens_masked_and_ruled_out(T, E, groups, sigmoid):
+    g = torch.Generator(DEV).manual_seed(3)
+    x = _logits(T, E, 3)
+    x[torch.rand(T, E, generator=g, device=DEV) < 0.6] = -INF
+    x[torch.rand(T, E, generator=g, device=DEV) < 0.1] = float("nan")
+    x[1], x[2], x[3], x[5] = -INF, float("nan"), -INF, -INF
+    x[3, E - 1] = 0.5
+    x[4] = torch.finfo(torch.float32).min
+    x[5, ::3] = torch.finfo(torch.float32).min
+    mask = torch.rand(T, generator=g, device=DEV) < 0.8
+    mask[3:6] = True
+    bias = 0.1 * torch.randn(E, generator=g, device=DEV)
+    bias[E // 2], bias[E // 3] = -INF, float("nan")
+    k = min(8, E // groups * max(1, groups // 2))
+    for b in (None, bias):
+        for kw in (dict(), dict(n_groups=groups, topk_groups=max(1, groups // 2), group_top=1 + (E % 3 != 0), renorm=True)):
+            got = _check(x, k, sigmoid, bias=b, mask=mask, **kw)
+            assert (got[1:3] == -1).all() and (got[~mask.cpu().numpy()] == -1).all()
+
+
+@pytest.mark.parametrize("T,E,groups", PLANS + [(20, 64, 8), (20, 256, 8), (20, 1024, 16)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_equal_choices(T, E, groups, dtype):
+    """Ties of single choices and of groups' sums, which are sums of the same two scores."""
+    few = _of([0.0, 1.0, 2.0], T, E, 1).to(dtype)
+    for sigmoid in (False, True):
+        for x in (few, few - 90.0, few + 30.0):
+            for bias in (None, torch.zeros(E, device=DEV), 0.25 * (torch.arange(E, device=DEV) % 3)):
+                _check(x, 6, sigmoid, bias=bias)
+                for top in (1, 2) if groups > 1 else ():
+                    _check(x, min(6, E // groups * 2), sigmoid, bias=bias, n_groups=groups, topk_groups=2, group_top=top)
+    # neighbours in fp32, in descending and ascending order of ids
+    base = np.float32(1.5) + np.arange(E, dtype=np.float32) * np.float32(2.0 ** -23)
+    for order in (base, base[::-1].copy()):
+        x = torch.from_numpy(np.tile(order, (T, 1))).to(DEV)
+        for kw in (dict(), dict(n_groups=groups, topk_groups=max(1, groups // 2))):
+            k = min(6, E // groups * max(1, groups // 2))
+            _check(x, k, rows=4, **kw)
+            _check(x, k, True, bias=torch.full((E,), 3.0, device=DEV), rows=4, **kw)
+
+
+@pytest.mark.parametrize("T,E,groups", PLANS)
+@pytest.mark.parametrize("spread", [1e-6, 1e-3, 30.0, 1e4])
+def test_narrow_and_wide_logits(T, E, groups, spread):
+    """Far out, scores are 0 and 1 and sums of them and a bias decide: all in 64 bits."""
+    x = _logits(T, E, 7, spread=spread)
+    bias = 1e-3 * torch.randn(E, generator=torch.Generator(DEV).manual_seed(4), device=DEV)
+    stay = max(1, groups // 2)
+    k = min(8, E // groups * stay)
+    for sigmoid in (False, True):
+        _check(x, k, sigmoid, renorm=True)
+        for top in (1, 2):
+            kw = dict(n_groups=groups, topk_groups=stay, group_top=top)
+            _check(x, k, sigmoid, bias=bias, **kw)
+            _check(x - 300.0, k, sigmoid, bias=bias, renorm=True, **kw)
+            _check(x, k, sigmoid, renorm=True, **kw)
+
+
+@pytest.mark.parametrize("T,E,groups", [(9, 16, 1), (9, 64, 8), (9, 256, 8), (MANY, 64, 8), (MANY, 256, 8), (MANY, 1024, 16)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_picks_of_infinite_logits(T, E, groups, dtype):
+    x = _logits(T, E, 1, dtype)
+    x[0, 3] = INF
+    x[1, 5] = x[1, 9] = INF
+    x[2, 0] = 1e30
+    x[3, -3:] = INF
+    x[4] = INF
+    x[5, ::2], x[5, 1::2] = INF, -INF
+    bias = 0.1 * torch.randn(E, generator=torch.Generator(DEV).manual_seed(4), device=DEV)
+    bias[E - 5] = INF
+    for sigmoid in (False, True):
+        for b in (None, bias):
+            for renorm in (False, True):
+                _check(x, 4, sigmoid, bias=b, renorm=renorm, rows=9)
+                if groups > 1:
+                    for top in (1, 2):
+                        _check(x, 4, sigmoid, bias=b, renorm=renorm, rows=9, n_groups=groups, topk_groups=2, group_top=top)
