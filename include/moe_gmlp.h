@@ -1021,8 +1021,8 @@ moe_status moe_grad_clip(const moe_grad_args* args, void* stream);
  *   moe_router_bias_update).
  *   Needs 0 <= T, 1 <= E <= 1024, 1 <= k <= min(8, experts of topk_groups
  *   groups), T * k < 2^31, n_groups 0 (none) to 64 and a divisor of E, 1 <=
- *   topk_groups <= n_groups, group_top 1 or 2; scale finite.  2^26 tokens and
- *   more are MOE_ERR_UNSUPPORTED (in moe_router_gate_bwd too).
+ *   topk_groups <= n_groups, group_top 1 or 2; scale finite.  More than
+ *   2^26 - 16 tokens are MOE_ERR_UNSUPPORTED (in moe_router_gate_bwd too).
  * ---------------------------------------------------------------------- */
 typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
 

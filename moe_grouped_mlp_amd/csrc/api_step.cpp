@@ -22,7 +22,7 @@ constexpr int kMaxInt8K = 131056;   // K 2^14 < 2^31
 constexpr int kBlk = MOE_FP8_BLOCK;
 constexpr int kTileN = 256;              // weight rows of a product's tile
 constexpr int64_t kMaxGridX = 1 << 24;   // workgroups of 256 threads in x
-constexpr int kMaxGateTokens = 1 << 26;   // of a wave each: 2^32 threads
+constexpr int kMaxGateTokens = (1 << 26) - 16;   // of a wave each, in whole workgroups of 1024: a launch has less than 2^32 threads
 
 moe_status launched(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_LAUNCH; }
 
@@ -369,7 +369,7 @@ moe_status moe_router_gate(const moe_gate_args* a, void* stream) {
   if (a->n_groups > 1 && (a->E % a->n_groups != 0 || a->topk_groups < 1 || a->topk_groups > a->n_groups ||
                           (a->group_top != 1 && a->group_top != 2) || a->k > a->E / a->n_groups * a->topk_groups))
     return MOE_ERR_INVALID_ARG;
-  if (a->T >= kMaxGateTokens) return MOE_ERR_UNSUPPORTED;
+  if (a->T > kMaxGateTokens) return MOE_ERR_UNSUPPORTED;
   int cu = 0;
   if (moe_status st = moe::current_device(&cu)) return st;
   if (a->T == 0) return MOE_OK;
@@ -383,7 +383,7 @@ moe_status moe_router_gate_bwd(const moe_gate_bwd_args* a, void* stream) {
       (reinterpret_cast<uintptr_t>(a->logits) | reinterpret_cast<uintptr_t>(a->dlogits)) % type_bytes(a->logits_type) != 0 ||
       (a->T > 0 && (!a->logits || !a->expert_idx || !a->dprobs || !a->dlogits)))
     return MOE_ERR_INVALID_ARG;
-  if (a->T >= kMaxGateTokens) return MOE_ERR_UNSUPPORTED;
+  if (a->T > kMaxGateTokens) return MOE_ERR_UNSUPPORTED;
   int cu = 0;
   if (moe_status st = moe::current_device(&cu)) return st;
   if (a->T == 0) return MOE_OK;

@@ -2,8 +2,9 @@
 
 from moe_grouped_mlp_amd import binding as B
 
-from .test_abi import DEVICE, INVALID, _call, no_device
-from .test_layer_abi import _adamw, _tensor
+from .test_abi import DEVICE, INVALID, UNSUPPORTED, _call, no_device
+from .test_layer_abi import _adamw, _tensor, bwd, gate
+from .test_step_abi import _refuses
 
 
 def test_the_largest_norm_keeps_64_bits():
@@ -22,3 +23,17 @@ def test_adamw_refuses_a_subnormal_eps():
 def test_adamw_accepts_small_eps():
     for eps in (0.0, 2.0 ** -126, 1e-30):
         assert _call("moe_adamw", _adamw([_tensor()], eps=eps)) == DEVICE, eps
+
+
+MOST = 2 ** 26 - 16   # tokens of a wave each: whole workgroups of 1024 threads, less than 2^32
+
+
+def test_tokens_that_a_launch_rounds_up_to_too_many():
+    for name, make in (("moe_router_gate", gate), ("moe_router_gate_bwd", bwd)):
+        _refuses(name, make, [dict(T=MOST + 1), dict(T=2 ** 26 - 1)], UNSUPPORTED)
+
+
+@no_device
+def test_most_tokens():
+    for name, make in (("moe_router_gate", gate), ("moe_router_gate_bwd", bwd)):
+        _refuses(name, make, [dict(T=MOST)], DEVICE)
