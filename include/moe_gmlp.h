@@ -1190,7 +1190,8 @@ moe_status moe_quantize_int8(const moe_quant_int8_args* args, void* stream);
  *     C[r][n] = a_s[r] * b_s[e][n] * sum_k a[r][k] * b[e][n][k]
  *   for every row r in [padded_offsets[e], padded_offsets[e] +
  *   split_sizes[e]).  The sums are integers and exact; they are rounded to
- *   fp32, scaled there and rounded once to the output type.
+ *   fp32, scaled there (by a_s, then by b_s) and rounded once to the output
+ *   type.
  *   a [M_cap][K], a_s [M_cap]; per expert b [N][K] and b_s [N] (b_stride
  *   bytes and b_s_stride floats apart, 0: N * K and N).  c, ldc, c_type,
  *   max_rows, cu_margin, workspace (with it the last round of tiles may be

@@ -58,7 +58,8 @@ bias, groups of experts, renormalised weights; moe_router_gate),
 gate_backward() the gradient of its logits from the dprobs of backward(), and
 update_bias() the balance bias's update from the picks that gate() counted.
 adamw_step() updates the weights from dw1 and dw2 (moe_adamw), clipped to a
-largest norm on the way, with states in fp32 or 8 bits.
+largest norm on the way, with states in fp32 or 8 bits, which adamw_state() and
+load_adamw_state() save and load.
 
 Around the experts, router_loss() gives the router's balance and z losses and
 per-expert counts, router_backward() the gradient of its logits from these

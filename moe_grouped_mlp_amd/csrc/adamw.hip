@@ -11,7 +11,7 @@
 //
 // Bound by HBM: an element of a bf16 weight with an fp32 master, gradient and
 // states moves 30 bytes, one with 8-bit states and a bf16 gradient 10.1.  705 M
-// elements take 3.72 ms (5.7 TB/s) and 1.22 ms (5.8; roots, codes and random bits
+// elements take 3.73 ms (5.7 TB/s) and 1.23 ms (5.8; roots, codes and random bits
 // keep the vector units busy for all of that time too); a copy of as much reaches
 // 5.5 .. 5.8, one that reads 4 arrays and writes 3 5.5.  12 small tensors take 8 us,
 // 6 of them the kernel's.
@@ -146,7 +146,7 @@ MOE_DEV float stepped(const Consts& c, float wd_lr, float m, float r, float w) {
 
 // The hardware's root, off by an ulp.  It takes values below 2^-126 for zero: SMALL
 // scales small ones before and after, for an eps that their roots are not lost beside.
-// (Always, 705 M elements take 3.78 ms, else 3.72.)
+// (Always, 705 M elements take 3.78 ms, else 3.73.)
 template <bool SMALL>
 MOE_DEV float root_ulp(float v) {
   if constexpr (!SMALL) return __builtin_amdgcn_sqrtf(v);
@@ -478,9 +478,10 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamList l) {
 }  // namespace
 
 hipError_t launch_adamw(const AdamList& l, bool fp8, hipStream_t s) {
-  // a workgroup for every chunk (705 M elements, fp32 states, 30 bytes each: 3.71
-  // ms; 2048 workgroups that stride over the chunks 4.15); where the constants are
-  // made on the device, every workgroup makes them, so fewer
+  // a workgroup for every chunk (705 M elements, fp32 states, 30 bytes each: 3.73
+  // ms; 2048 workgroups that stride over the chunks 4.15); where the step is counted
+  // on the device every workgroup makes the constants, so fewer (4.19 ms, 8-bit states
+  // 1.57 against 1.23)
   const int64_t most = l.step_dev ? 4096 : kAdamBlocks;
   const int grid = static_cast<int>(l.chunks < most ? l.chunks : most);
   int64_t bytes = 0;

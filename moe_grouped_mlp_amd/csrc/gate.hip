@@ -704,7 +704,7 @@ struct GateBwdP {
 // The gradient reads the logits (where every one has a part in it) and writes as
 // many: bound by these bytes for many tokens, by the launch for few.  A wave for a
 // token from 65 experts on (16384 x 256, 35 MB: 8.5 us, with 16 lanes 10.9; 256 x
-// 8 takes 4.1).  Rows go out through LDS of their own, where the picks' terms are
+// 8 takes 4.2).  Rows go out through LDS of their own, where the picks' terms are
 // added to them.
 template <int LPT, int V, typename T>
 __global__ __launch_bounds__(kThreads) void gate_bwd_kernel(const GateBwdP g) {

@@ -26,7 +26,7 @@ namespace {
 // second launch, so the best number is near sqrt(16 steps / tiles) (of four
 // steps each at least), and it has to save more steps than it costs.  16384 rows
 // over 8 experts x 4096 x 14336, 1104 tiles on 256 CUs: 800 us uncut, 767 with the
-// last 80 in 3 parts (755 .. 790 over runs, 2.44 .. 2.55 PFLOP/s; a library's product
+// last 80 in 3 parts (754 .. 796 over runs, 2.42 .. 2.55 PFLOP/s; a library's product
 // of 16384 x 4096 x 14336 and one scale for all: 2.52).
 struct Int8Cut {
   int whole, parts;
