@@ -194,8 +194,9 @@ MOE_DEV float sigmoid_of(float x) {
 }
 
 // The lane's weight share: its pick's score over the sum of the token's, which
-// its first kMaxTopK lanes hold.  The scores of picks that are all small are
-// taken times a factor that keeps the largest in range.
+// its first kMaxTopK lanes hold.  Scores so small that they, or their share of a
+// small sum, would lose bits as subnormal numbers are taken times a factor that
+// keeps the token's largest in range, with a sum of such ones.
 MOE_DEV float renormed(bool sigmoid, bool live, float x) {
   static_assert(kMaxTopK == 8, "sums over 8 lanes");
   float s = 0.0f, z = 0.0f;
@@ -203,13 +204,14 @@ MOE_DEV float renormed(bool sigmoid, bool live, float x) {
     s = live ? sigmoid_of(x) : 0.0f;
     z = sum_lanes<8>(s);
   }
-  if (__ballot(!(z > 1e-30f))) {
+  const bool small = live && !(s > 1e-30f);   // (all, without a sigmoid)
+  if (__ballot(small)) {
     const float top = max_lanes<8>(live ? x : neg_inf());
     float r = expf(below(x, top));
     if (sigmoid) r = top < 0.0f ? r / (1.0f + expf(x)) : sigmoid_of(x);
     r = live ? r : 0.0f;
     const float y = sum_lanes<8>(r);
-    if (!(z > 1e-30f)) {
+    if (small) {
       s = r;
       z = y;
     }

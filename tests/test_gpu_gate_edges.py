@@ -193,3 +193,25 @@ def test_picks_of_infinite_logits(T, E, groups, dtype):
                 if groups > 1:
                     for top in (1, 2):
                         _check(x, 4, sigmoid, bias=b, renorm=renorm, rows=9, n_groups=groups, topk_groups=2, group_top=top)
+
+
+@pytest.mark.parametrize("T,E", [(8, 16), (8, 128), (8, 300), (MANY, 64), (MANY, 256)])
+def test_weights_and_gradients_of_tiny_sigmoids(T, E):
+    """Renormalised weights of scores that are subnormal numbers beside a small sum: as
+    exact as others, while the weight itself is a normal number (2^-126)."""
+    k = 4
+    x = torch.full((T, E), -200.0, device=DEV)
+    rows = [(-11.7, -101.66, -48.0, -97.3), (-60.0, -100.0, -103.2, -90.0), (-68.9, -103.9, -110.0, -150.0), (3.0, -84.2, -87.5, -1.0),
+            (-103.0, -103.5, -110.0, -120.0), (-69.1, -69.0, -104.5, -87.4), (80.0, -6.0, 30.0, 0.5), (-40.0, -126.0, -122.0, -43.0)]
+    g = torch.Generator(DEV).manual_seed(1)
+    for t in range(T):
+        at = torch.randperm(E, generator=g, device=DEV)[:k]
+        x[t, at] = torch.tensor(rows[t % len(rows)], device=DEV)
+    got = _check(x, k, True, renorm=True, rows=16)
+    idx = torch.from_numpy(got).to(DEV).int()
+    d = torch.randn(T, k, generator=g, device=DEV)
+    out = torch.empty_like(x)
+    mg.moe_router_gate_bwd(T=T, E=E, k=k, logits=x, expert_idx=idx, dprobs=d, dlogits=out, score=mg.SCORE_SIGMOID, renorm=True)
+    n = 40
+    ref, mag = ol.gate_bwd(_np(x[:n]), got[:n], _np(d[:n]), True, renorm=True)
+    assert (np.abs(_np(out[:n]) - ref) <= (400 + 40) * 2.0 ** -23 * mag + 2.0 ** -140).all()
