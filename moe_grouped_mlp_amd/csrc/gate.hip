@@ -12,11 +12,11 @@
 //
 // Few tokens wait for a launch and its code, many for the steps of the choice,
 // each of which needs the one before; their bytes take less.  16 tokens of 256
-// experts in 8 groups take 5.3 us, 16384 of them 16.5 (17.8 MB: 3.2 at the rate of
-// a copy) and 16384 of 128 experts without groups 9.3.  The second would take 9.7
+// experts in 8 groups take 5.2 us, 16384 of them 15.7 (17.8 MB: 3.2 at the rate of
+// a copy) and 16384 of 128 experts without groups 9.4.  The second would take 10.5
 // without the counts (every workgroup's atomics on the same lines, one after the
 // other) and without the tokens that fp32 leaves open, some 20, for which a wave
-// each goes on alone; with either it takes 15.5 .. 16.5, since the two overlap.  All
+// each goes on alone; with either it takes 15.0, since the two overlap.  All
 // choices in 64 bits took 127, 32 bits and a search for the largest by a whole wave
 // 27 .. 36.
 #include <type_traits>
@@ -810,7 +810,7 @@ int next_pow2(int v) {
 // Lanes a token takes and logits a lane holds: the first that hold it of those
 // up to 16 lanes, or of a wave's.  A wave shortens the way of one token, more of
 // them share the instructions of 16 lanes each: 256 experts in 8 groups take 5.2
-// us (wave) or 8.4 for 16 tokens, 27 .. 36 or 16.6 for 16384; a wave it is up to
+// us (wave) or 8.4 for 16 tokens, 27 .. 36 or 15.7 for 16384; a wave it is up to
 // 4 tokens a CU, one for each of its SIMDs.
 struct Shape {
   int lanes, values;
