@@ -800,8 +800,8 @@ class ExpertBlock:
     # ------------------------------------------------------------ update --
     def adamw_step(self, lr, *, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                    weight_decay: float = 0.0, max_norm: Optional[float] = None, extra=(),
-                   sumsq: Optional[torch.Tensor] = None, state: int = B.STATE_F32, master: bool = True, stochastic: bool = False,
-                   seed: int = 0, capturable: bool = False, requantize: bool = True) -> None:
+                   sumsq: Optional[torch.Tensor] = None, state: int = B.STATE_F32,
+                   master: bool = True, stochastic: bool = False, seed: int = 0, capturable: bool = False, requantize: bool = True) -> None:
         """One AdamW step of w1i and w2 from dw1 and dw2 (moe_adamw).  The first
         call makes the states (state: fp32, or 8 bits with their roots rounded
         stochastically if asked) and, with master, fp32 copies of the weights
@@ -882,7 +882,7 @@ class ExpertBlock:
 
     def adamw_state(self) -> dict:
         """What adamw_step() goes on from, for a checkpoint: its own tensors and
-        numbers, not copies."""
+        numbers, not copies (which steps and load_weights() change)."""
         if self._adamw is None:
             raise RuntimeError("adamw_state() needs adamw_step() first")
         state, master, capturable = self._adamw["kind"]
@@ -902,6 +902,8 @@ class ExpertBlock:
         pairs += zip(st["master"] or (), saved["weights"] or ())
         if any(mine.shape != theirs.shape or mine.dtype != theirs.dtype for mine, theirs in pairs):
             raise ValueError("the states are of another block's sizes")
+        if any(mine.data_ptr() == theirs.data_ptr() for mine, theirs in pairs):
+            raise ValueError("these are the block's own states as they are now: load copies of them")
         for mine, theirs in pairs:
             mine.copy_(theirs)
         if saved["capturable"]:

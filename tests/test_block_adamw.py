@@ -161,3 +161,14 @@ def test_states_are_saved_and_loaded_in_place(block, kw):
         block.load_adamw_state({**saved, "state": 1 - saved["state"]})
     with pytest.raises(ValueError, match="sizes"):
         block.load_adamw_state({**saved, "m": [t[1:] for t in saved["m"]]})
+
+
+def test_the_blocks_own_states_are_no_checkpoint(block):
+    """load_weights() has begun them anew: loading them would go on from zeros with
+    the old step's number."""
+    block.adamw_step(0.1)
+    own = block.adamw_state()
+    _load(block, 1.0)
+    with pytest.raises(ValueError, match="own"):
+        block.load_adamw_state(own)
+    assert block.adamw_steps == 0
