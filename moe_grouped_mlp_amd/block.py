@@ -801,7 +801,8 @@ class ExpertBlock:
     def adamw_step(self, lr, *, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                    weight_decay: float = 0.0, max_norm: Optional[float] = None, extra=(),
                    sumsq: Optional[torch.Tensor] = None, state: int = B.STATE_F32,
-                   master: bool = True, stochastic: bool = False, seed: int = 0, capturable: bool = False, requantize: bool = True) -> None:
+                   master: bool = True, stochastic: bool = False, seed: int = 0,
+                   capturable: bool = False, requantize: bool = True) -> None:
         """One AdamW step of w1i and w2 from dw1 and dw2 (moe_adamw).  The first
         call makes the states (state: fp32, or 8 bits with their roots rounded
         stochastically if asked) and, with master, fp32 copies of the weights
